@@ -28,6 +28,12 @@
  *   sg_format_sizes         the Pull side: hash bitmap back to indices, the
  *                           aggregate scattered into a dense tensor, and the
  *                           aggregate's size under the sparse formats
+ *   sg_topk_rows,
+ *   sg_distill_loss,
+ *   sg_policy_loss,
+ *   sg_preference_loss      losses over a vocabulary with their gradients (the
+ *                           dense gradients the path starts from), and the
+ *                           teacher's top logits that distillation takes
  *
  * Sources: "Zen: Empowering Distributed Training with Sparsity-driven Data
  * Synchronization" (OSDI'25) digest page [Zen]; "SkipReduce: (Interconnection)
@@ -514,6 +520,115 @@ int sg_stats_async(const uint32_t* d_idx, const uint64_t* d_in_off, uint32_t n, 
                    size_t ws_bytes, void* stream);
 int sg_stats_collect(const void* h_block, uint32_t n, uint64_t M, uint64_t total, uint32_t P, int hashed,
                      sg_stats_out* h_out);
+
+/* ------------------------------------------------------------------------
+ * Losses over a vocabulary: where the gradients of a language model's step
+ * start.  Common to the four calls:
+ *   d_logits [T] rows of V logits of dt, row t at d_logits + t * ld elements
+ *            (ld >= V; any element alignment).  z = inv_temp * logit,
+ *            lse = log sum_i exp(z_i), log q_i = z_i - lse.  The
+ *            log-probability of a logit of -inf is -inf, also in a row of
+ *            nothing else; a NaN or +inf makes its own row's results NaN.
+ *   d_weight [T] fp32 or NULL (every row 1).  A row of weight 0 is not read:
+ *            its loss and its gradient are 0 whatever it holds.
+ *   d_loss   the weighted losses; the loss of the batch is their sum.
+ *   d_grad   [T] rows of V of dt, ld_grad elements apart, or NULL (loss only):
+ *            the gradient of that sum with respect to the logits, rounded
+ *            once.  d_grad may be d_logits itself with ld_grad == ld (the
+ *            gradient replaces the logits); otherwise they must not overlap.
+ *            Elements between V and ld_grad are left untouched.
+ *   d_ws     of at least the size the call's *_workspace_bytes returns; it
+ *            may be NULL where that is 0.
+ * Sums, row scalars: fp32 terms of at most 1 per lane, joined in fp32, the
+ * row's scalars in fp64.  Results do not depend on timing (no float atomics).
+ * Limits: T < 2^31, 1 <= V < 2^31, ld and ld_grad < 2^40, 0 < inv_temp <= 1e6.
+ * T = 0 is a no-op.
+ * ------------------------------------------------------------------------ */
+#define SG_ROWS_MAX_K 1024 /* longest list per row of sg_topk_rows and sg_distill_loss */
+
+/* The k largest logits of every row as COO rows with their log-probabilities:
+ * the teacher's answer that sg_distill_loss takes.
+ *   d_idx  [T][k] u32 out, ascending within a row; equal logits (+0 and -0
+ *          included) are taken lowest index first; a NaN orders above +inf,
+ *          or below -inf if its sign bit is set.
+ *   d_logp [T][k] fp32 out: z - lse over the whole row (not over the list)
+ *   d_lse  [T] fp32 out, or NULL
+ * Limits: 1 <= k <= V (else SG_EINVAL), k <= SG_ROWS_MAX_K (else SG_EUNSUPPORTED). */
+size_t sg_topk_rows_workspace_bytes(uint64_t T, uint64_t V, uint32_t k, sg_dtype dt);
+int sg_topk_rows(const void* d_logits, sg_dtype dt, uint64_t T, uint64_t V, uint64_t ld, double inv_temp, uint32_t k,
+                 uint32_t* d_idx, float* d_logp, float* d_lse, void* d_ws, size_t ws_bytes, void* stream);
+
+typedef enum sg_distill_mode {
+    SG_DISTILL_PLAIN = 0,  /* sum p (log p - log q) over the list as it is */
+    SG_DISTILL_RENORM = 1, /* the list's masses scaled to sum 1 */
+    SG_DISTILL_TAIL = 2    /* the list plus one bucket for all other tokens */
+} sg_distill_mode;
+
+/* Distillation from a teacher's listed log-probabilities.  With p = exp(logp)
+ * over the row's list, P = sum p and Q = sum q over the list:
+ *   PLAIN   L = sum p (log p - log q)
+ *   RENORM  the same with p / P (a list of no mass: L = 0)
+ *   TAIL    PLAIN + R (log R - log(1 - Q)), R = max(0, 1 - P); 1 - Q is summed
+ *           over the unlisted tokens, not subtracted; where they hold nothing
+ *           (the list covers every finite logit) the bucket is left out, R = 0
+ * d loss / d logit_i = weight * inv_temp * (W q_i - p_i), W = P + R (RENORM: 1),
+ * and for an unlisted token weight * inv_temp * q_i (W - R / (1 - Q)).
+ *   d_idx  [T][k] u32, in any order, no token twice in a row (a kernel that
+ *          notices one records it for sg_device_error; that row's results are
+ *          unspecified).  An index >= V is padding and carries no mass.
+ *   d_logp [T][k] fp32, the teacher's log-probabilities at the same temperature
+ *   d_loss [T] fp32 out
+ * Limits: 1 <= k (else SG_EINVAL), k <= SG_ROWS_MAX_K (else SG_EUNSUPPORTED). */
+size_t sg_distill_workspace_bytes(uint64_t T, uint64_t V, uint32_t k, sg_dtype dt);
+int sg_distill_loss(const void* d_logits, sg_dtype dt, uint64_t T, uint64_t V, uint64_t ld, double inv_temp,
+                    const uint32_t* d_idx, const float* d_logp, uint32_t k, sg_distill_mode mode,
+                    const float* d_weight, float* d_loss, void* d_grad, uint64_t ld_grad, void* d_ws,
+                    size_t ws_bytes, void* stream);
+
+/* Clipped policy loss per token, with a KL term to a reference policy.  With
+ * lp the log-probability of the row's action, r = exp(lp - old),
+ * d = ref - lp:
+ *   L = -min(r A, clip(r, 1 - clip_low, 1 + clip_high) A) + kl_coef (exp(d) - d - 1)
+ *   dL/dlp = -r A, or 0 where A > 0 and r > 1 + clip_high or A < 0 and
+ *            r < 1 - clip_low;  plus kl_coef (1 - exp(d))
+ *   d loss / d logit_i = weight * inv_temp * dL/dlp * (1[i = action] - q_i)
+ *   d_action   [T] i32; a row whose action is outside [0, V) counts as weight 0
+ *   d_old_logp [T] fp32, or NULL: the policy is its own old one (r = 1)
+ *   d_ref_logp [T] fp32, or NULL: no KL term
+ *   d_adv      [T] fp32 advantages, or NULL: 0 (log-probabilities and KL only)
+ *   d_loss [T], d_logp [T] fp32 out (d_logp may be NULL; 0 for rows of weight 0)
+ * Limits: 0 <= clip_low <= 1, 0 <= clip_high <= 1e6, 0 <= kl_coef <= 1e6. */
+size_t sg_policy_workspace_bytes(uint64_t T, uint64_t V, sg_dtype dt);
+int sg_policy_loss(const void* d_logits, sg_dtype dt, uint64_t T, uint64_t V, uint64_t ld, double inv_temp,
+                   const int32_t* d_action, const float* d_old_logp, const float* d_ref_logp, const float* d_adv,
+                   const float* d_weight, double clip_low, double clip_high, double kl_coef, float* d_loss,
+                   float* d_logp, void* d_grad, uint64_t ld_grad, void* d_ws, size_t ws_bytes, void* stream);
+
+typedef enum sg_pref_kind {
+    SG_PREF_SIGMOID = 0, /* -(1 - smoothing) log sigmoid(beta d) - smoothing log sigmoid(-beta d) */
+    SG_PREF_HINGE = 1,   /* max(0, 1 - beta d) */
+    SG_PREF_IPO = 2      /* (d - 1 / (2 beta))^2 */
+} sg_pref_kind;
+
+/* Preference loss over pairs of packed sequences.  Sequence s holds the rows
+ * [seq_off[s], seq_off[s+1]); pair b is the chosen sequence b and the rejected
+ * sequence pairs + b.  S_s is the sum of the log-probabilities of the labels
+ * that count (average != 0: their mean; 0 for a sequence without any) and
+ * d = (S_chosen - ref_chosen) - (S_rejected - ref_rejected).
+ *   d_label    [T] i32; a row whose label is outside [0, V) does not count:
+ *              it is not read, its gradient is 0.  So does a row of no sequence.
+ *   d_seq_off  [2 * pairs + 1] u64, non-decreasing, at most T (a violation the
+ *              kernel notices is recorded for sg_device_error)
+ *   d_ref_logp [2 * pairs] fp32, or NULL: 0 (no reference model)
+ *   d_weight   [pairs] fp32, or NULL: every pair 1
+ *   d_loss [pairs], d_logp [2 * pairs] (S, may be NULL) fp32 out
+ * The temperature is 1.  Limits: pairs < 2^30, 0 < beta <= 1e6,
+ * 0 <= smoothing < 0.5 (other than 0 with SG_PREF_SIGMOID only). */
+size_t sg_preference_workspace_bytes(uint64_t T, uint64_t V, sg_dtype dt);
+int sg_preference_loss(const void* d_logits, sg_dtype dt, uint64_t T, uint64_t V, uint64_t ld, const int32_t* d_label,
+                       const uint64_t* d_seq_off, uint32_t pairs, const float* d_ref_logp, const float* d_weight,
+                       sg_pref_kind kind, double beta, double smoothing, int average, float* d_loss, float* d_logp,
+                       void* d_grad, uint64_t ld_grad, void* d_ws, size_t ws_bytes, void* stream);
 
 #ifdef __cplusplus
 }

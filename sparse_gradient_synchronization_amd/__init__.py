@@ -22,6 +22,9 @@ LIB_PATH = os.path.join(_HERE, "libsg.so")
 
 SG_F32, SG_BF16 = 0, 1
 SG_RESCALE_NONE, SG_RESCALE_DROP = 0, 1
+SG_DISTILL_PLAIN, SG_DISTILL_RENORM, SG_DISTILL_TAIL = 0, 1, 2
+SG_PREF_SIGMOID, SG_PREF_HINGE, SG_PREF_IPO = 0, 1, 2
+SG_ROWS_MAX_K = 1024
 
 _STATUS = {0: "SG_OK", -1: "SG_EINVAL", -2: "SG_ECAPACITY", -3: "SG_EUNSORTED", -4: "SG_EHIP",
            -5: "SG_EUNSUPPORTED", -6: "SG_ERANGE", -7: "SG_EDEVICE"}
@@ -92,6 +95,17 @@ SIGNATURES = {
     "sg_stats_block_bytes": (_sz, [_u32, _u32]),
     "sg_stats_async": (_int, [_vp, _vp, _u32, _u64, _u64, _u32, _vp, _sz, _vp, _sz, _vp, _sz, _vp]),
     "sg_stats_collect": (_int, [_vp, _u32, _u64, _u64, _u32, _int, C.POINTER(StatsOut)]),
+    "sg_topk_rows_workspace_bytes": (_sz, [_u64, _u64, _u32, _int]),
+    "sg_topk_rows": (_int, [_vp, _int, _u64, _u64, _u64, _dbl, _u32, _vp, _vp, _vp, _vp, _sz, _vp]),
+    "sg_distill_workspace_bytes": (_sz, [_u64, _u64, _u32, _int]),
+    "sg_distill_loss": (_int, [_vp, _int, _u64, _u64, _u64, _dbl, _vp, _vp, _u32, _int, _vp, _vp, _vp, _u64, _vp,
+                               _sz, _vp]),
+    "sg_policy_workspace_bytes": (_sz, [_u64, _u64, _int]),
+    "sg_policy_loss": (_int, [_vp, _int, _u64, _u64, _u64, _dbl, _vp, _vp, _vp, _vp, _vp, _dbl, _dbl, _dbl, _vp, _vp,
+                              _vp, _u64, _vp, _sz, _vp]),
+    "sg_preference_workspace_bytes": (_sz, [_u64, _u64, _int]),
+    "sg_preference_loss": (_int, [_vp, _int, _u64, _u64, _u64, _vp, _vp, _u32, _vp, _vp, _int, _dbl, _dbl, _int, _vp,
+                                  _vp, _vp, _u64, _vp, _sz, _vp]),
 }
 
 _lib = None
@@ -541,6 +555,157 @@ def _stats_result(arr, o, n, P):
     for k in ("overlap_mean", "overlap_min", "overlap_max", "gamma_n", "push_imbalance", "pull_imbalance"):
         res[k] = float(getattr(o, k))
     return res
+
+
+# --------------------------------------------------------------------------
+# losses over a vocabulary
+# --------------------------------------------------------------------------
+
+def _rows(logits: torch.Tensor):
+    """(logits, dtype code, T, V, row stride): a 2-D tensor whose rows are
+    contiguous is taken as it is, whatever its row stride."""
+    if logits.dim() != 2:
+        raise ValueError("logits must be [rows, vocabulary], got %d dimensions" % logits.dim())
+    dt = _dtype_code(logits)
+    T, V = logits.shape
+    if V > 1 and logits.stride(1) != 1 or T > 1 and logits.stride(0) < V:
+        logits = logits.contiguous()
+    return logits, dt, T, V, (logits.stride(0) if T > 1 else V)
+
+
+def _same_device(logits, **tensors):
+    """Shape, type and device checks of a call's other tensors: name=(tensor
+    or None, dtype, shape).  Returns them contiguous."""
+    out = []
+    for name, (t, dtype, shape) in tensors.items():
+        if t is not None:
+            if t.dtype != dtype or tuple(t.shape) != shape:
+                raise ValueError("%s must be %s of shape %s, got %s %s" % (name, dtype, list(shape), t.dtype,
+                                                                           list(t.shape)))
+            if t.device != logits.device:
+                raise ValueError("%s is on %s, the logits on %s" % (name, t.device, logits.device))
+            t = t.contiguous()
+        out.append(t)
+    return out
+
+
+def _grad_of(logits, want_grad, grad):
+    """The gradient's tensor and row stride: allocated, the caller's, or none."""
+    if grad is None:
+        if not want_grad:
+            return None, 0
+        grad = torch.empty(logits.shape, dtype=logits.dtype, device=logits.device)
+        return grad, grad.shape[1]
+    T, V = logits.shape
+    if grad.dtype != logits.dtype or grad.shape != logits.shape or grad.device != logits.device:
+        raise ValueError("grad must have the logits' type, shape and device")
+    if V > 1 and grad.stride(1) != 1 or T > 1 and grad.stride(0) < V:
+        raise ValueError("grad must have contiguous rows (it is written in place)")
+    return grad, (grad.stride(0) if T > 1 else V)
+
+
+def _inv_temp(temperature):
+    if not temperature > 0:
+        raise ValueError("temperature must be positive, got %r" % (temperature,))
+    return 1.0 / temperature
+
+
+def _ws_or_none(need, workspace, device):
+    if need == 0:
+        return None, 0
+    if workspace is None or workspace.numel() < need:
+        workspace = torch.empty(need, dtype=torch.uint8, device=device)
+    return workspace, workspace.numel()
+
+
+def sg_topk_rows(logits: torch.Tensor, k: int, temperature: float = 1.0, workspace: torch.Tensor | None = None):
+    """The k largest logits of every row: logits [T, V] float32/bfloat16 ->
+    (idx [T, k] int32 holding uint32 indices, ascending; logp [T, k] float32,
+    log-probabilities over the whole row; lse [T] float32)."""
+    _need_cuda(logits)
+    logits, dt, T, V, ld = _rows(logits)
+    dev = logits.device
+    idx = torch.empty((T, k), dtype=torch.int32, device=dev)
+    logp = torch.empty((T, k), dtype=torch.float32, device=dev)
+    lse = torch.empty(T, dtype=torch.float32, device=dev)
+    ws, nws = _ws_or_none(lib().sg_topk_rows_workspace_bytes(T, V, k, dt), workspace, dev)
+    _check(lib().sg_topk_rows(_p(logits), dt, T, V, ld, _inv_temp(temperature), k, _p(idx), _p(logp), _p(lse), _p(ws), nws,
+                              _stream()), "sg_topk_rows")
+    return idx, logp, lse
+
+
+def sg_distill_loss(logits: torch.Tensor, idx: torch.Tensor, logp: torch.Tensor, temperature: float = 1.0,
+                    mode: int = SG_DISTILL_TAIL, weight: torch.Tensor | None = None, want_grad: bool = True,
+                    grad: torch.Tensor | None = None, workspace: torch.Tensor | None = None):
+    """Distillation from a teacher's listed log-probabilities (sg_topk_rows):
+    logits [T, V], idx [T, k] int32, logp [T, k] float32, weight [T] float32
+    -> (loss [T] float32, weighted; grad [T, V] of loss.sum(), or None).
+    grad: where to write the gradient, logits itself included."""
+    _need_cuda(logits, idx, logp, weight, grad)
+    grad, ldg = _grad_of(logits, want_grad, grad)
+    logits, dt, T, V, ld = _rows(logits)
+    k = idx.shape[-1]
+    idx, logp, weight = _same_device(logits, idx=(idx, torch.int32, (T, k)), logp=(logp, torch.float32, (T, k)),
+                                     weight=(weight, torch.float32, (T,)))
+    loss = torch.empty(T, dtype=torch.float32, device=logits.device)
+    ws, nws = _ws_or_none(lib().sg_distill_workspace_bytes(T, V, k, dt), workspace, logits.device)
+    _check(lib().sg_distill_loss(_p(logits), dt, T, V, ld, _inv_temp(temperature), _p(idx), _p(logp), k, mode, _p(weight),
+                                 _p(loss), _p(grad), ldg, _p(ws), nws, _stream()), "sg_distill_loss")
+    return loss, grad
+
+
+def sg_policy_loss(logits: torch.Tensor, action: torch.Tensor, old_logp=None, adv=None, ref_logp=None, weight=None,
+                   clip_low: float = 0.2, clip_high: float = 0.2, kl_coef: float = 0.0, temperature: float = 1.0,
+                   want_grad: bool = True, grad: torch.Tensor | None = None, workspace: torch.Tensor | None = None):
+    """Clipped policy loss with a KL term: logits [T, V], action [T] int32,
+    old_logp, adv, ref_logp, weight [T] float32 or None -> (loss [T] float32,
+    weighted; logp [T] float32 of the actions; grad [T, V] of loss.sum(), or
+    None).  grad: where to write the gradient, logits itself included."""
+    _need_cuda(logits, action, old_logp, adv, ref_logp, weight, grad)
+    grad, ldg = _grad_of(logits, want_grad, grad)
+    logits, dt, T, V, ld = _rows(logits)
+    f = torch.float32
+    action, old_logp, adv, ref_logp, weight = _same_device(
+        logits, action=(action, torch.int32, (T,)), old_logp=(old_logp, f, (T,)), adv=(adv, f, (T,)),
+        ref_logp=(ref_logp, f, (T,)), weight=(weight, f, (T,)))
+    loss = torch.empty(T, dtype=f, device=logits.device)
+    logp = torch.empty(T, dtype=f, device=logits.device)
+    ws, nws = _ws_or_none(lib().sg_policy_workspace_bytes(T, V, dt), workspace, logits.device)
+    _check(lib().sg_policy_loss(_p(logits), dt, T, V, ld, _inv_temp(temperature), _p(action), _p(old_logp), _p(ref_logp),
+                                _p(adv), _p(weight), clip_low, clip_high, kl_coef, _p(loss), _p(logp), _p(grad), ldg,
+                                _p(ws), nws, _stream()), "sg_policy_loss")
+    return loss, logp, grad
+
+
+def sg_preference_loss(logits: torch.Tensor, label: torch.Tensor, seq_off: torch.Tensor, ref_logp=None, weight=None,
+                       kind: int = SG_PREF_SIGMOID, beta: float = 0.1, smoothing: float = 0.0, average: bool = False,
+                       want_grad: bool = True, grad: torch.Tensor | None = None,
+                       workspace: torch.Tensor | None = None):
+    """Preference loss over packed sequences, the B chosen ones first, then
+    the B rejected ones: logits [T, V], label [T] int32 (outside [0, V): does
+    not count), seq_off [2B + 1] int64, ref_logp [2B], weight [B] float32 or
+    None -> (loss [B] float32, weighted; logp [2B] float32 of the sequences;
+    grad [T, V] of loss.sum(), or None).  smoothing applies to
+    SG_PREF_SIGMOID.  grad: where to write the gradient, logits itself
+    included."""
+    _need_cuda(logits, label, seq_off, ref_logp, weight, grad)
+    grad, ldg = _grad_of(logits, want_grad, grad)
+    logits, dt, T, V, ld = _rows(logits)
+    if seq_off.numel() % 2 != 1:
+        raise ValueError("seq_off must hold 2 * pairs + 1 offsets, got %d" % seq_off.numel())
+    B = seq_off.numel() // 2
+    f = torch.float32
+    label, seq_off, ref_logp, weight = _same_device(
+        logits, label=(label, torch.int32, (T,)), seq_off=(seq_off, torch.int64, (2 * B + 1,)),
+        ref_logp=(ref_logp, f, (2 * B,)), weight=(weight, f, (B,)))
+    loss = torch.empty(B, dtype=f, device=logits.device)
+    seq_logp = torch.empty(2 * B, dtype=f, device=logits.device)
+    ws, nws = _ws_or_none(lib().sg_preference_workspace_bytes(T, V, dt), workspace, logits.device)
+    _check(lib().sg_preference_loss(_p(logits), dt, T, V, ld, _p(label), _p(seq_off), B, _p(ref_logp), _p(weight),
+                                    kind, beta, smoothing if kind == SG_PREF_SIGMOID else 0.0, 1 if average else 0,
+                                    _p(loss), _p(seq_logp), _p(grad), ldg, _p(ws), nws, _stream()),
+           "sg_preference_loss")
+    return loss, seq_logp, grad
 
 
 def sg_validate_coo(idx: torch.Tensor, in_off: torch.Tensor, M: int) -> int:
