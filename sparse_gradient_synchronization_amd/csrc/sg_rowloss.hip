@@ -34,7 +34,7 @@ struct PolicyOp {
     double lo, hi, kl;
     uint32_t V;
 
-    static constexpr bool kListed = false;
+    static constexpr bool kListed = false, kGrad = true;
     struct Shared {
         float za, fix;
     };
@@ -57,10 +57,10 @@ struct PolicyOp {
     __device__ __forceinline__ RowCoef finish(const Rows& r, uint64_t row, RowStat st, Shared& sh) const
     {
         const double S = st.s;
-        const double lp = sh.za == -INFINITY ? -(double)INFINITY : ((double)sh.za - st.m) * r.it - log(S);
+        const double lp = sh.za == -INFINITY ? -(double)INFINITY : ((double)sh.za - st.m) * r.it - row_log(S);
         const double w = weight ? (double)weight[row] : 1.0;
         const double A = adv ? (double)adv[row] : 0.0;
-        const double ratio = old_logp ? exp(lp - (double)old_logp[row]) : 1.0;
+        const double ratio = old_logp ? row_exp(lp - (double)old_logp[row]) : 1.0;
         const double bounded = ratio < lo ? lo : (ratio > hi ? hi : ratio);
         const double a = ratio * A, b = bounded * A;
         double L = a <= b ? -a : (b <= a ? -b : a + b); // a NaN stays
@@ -68,14 +68,14 @@ struct PolicyOp {
         const bool clipped = (A > 0.0 && ratio > hi) || (A < 0.0 && ratio < lo);
         double slope = clipped ? 0.0 : -a;
         if (ref_logp) {
-            const double d = (double)ref_logp[row] - lp, e = expm1(d);
+            const double d = (double)ref_logp[row] - lp, e = row_expm1(d);
             L += kl * (e - d);
             slope -= kl * e;
         }
         loss[row] = (float)(w * L);
         if (logp) logp[row] = (float)lp;
         const double g = w * slope * r.it;
-        sh.fix = (float)(g * -expm1(lp)); // 1 - q of the token, without the cancellation
+        sh.fix = (float)(g * -row_expm1(lp)); // 1 - q of the token, without the cancellation
         return {st.m, (float)(-g * inverse_of(S))};
     }
     template <typename E, int NT>
@@ -97,7 +97,7 @@ struct TokenOp {
     float* slope; // cleared here, set by the pair pass for rows of a sequence
     uint32_t V;
 
-    static constexpr bool kListed = false;
+    static constexpr bool kListed = false, kGrad = false;
     struct Shared {
         float za;
     };
@@ -114,15 +114,11 @@ struct TokenOp {
     }
     __device__ __forceinline__ RowCoef finish(const Rows& r, uint64_t row, RowStat st, Shared& sh) const
     {
-        logp[row] = sh.za == -INFINITY ? -(double)INFINITY : ((double)sh.za - st.m) * r.it - log((double)st.s);
+        logp[row] = sh.za == -INFINITY ? -(double)INFINITY : ((double)sh.za - st.m) * r.it - row_log((double)st.s);
         m[row] = st.m;
         inv[row] = (float)inverse_of(st.s);
         slope[row] = 0.f;
         return {st.m, 0.f};
-    }
-    template <typename E, int NT>
-    __device__ __forceinline__ void fix(const Rows&, uint64_t, E*, const Shared&, RowCoef) const
-    {
     }
     __device__ __forceinline__ uint32_t bits(const uint32_t*, uint32_t, int) const { return 0; }
 };
@@ -142,7 +138,7 @@ struct DistillOp {
     uint32_t k, V;
     int mode;
 
-    static constexpr bool kListed = true;
+    static constexpr bool kListed = true, kGrad = true;
     struct Shared {
         float z[RL_MAX_K]; // the listed logits, read before the gradient may overwrite them
         double P, A, S;    // mass, sum p (log p - (z - m)), sum exp(z - m), z scaled by inv_temp
@@ -176,10 +172,10 @@ struct DistillOp {
             double P = 0.0, A = 0.0, S = 0.0;
             for (uint32_t j = threadIdx.x; j < k; j += SG_WAVE) {
                 if (id[j] >= V) continue;
-                const double t = lp[j], z = sh.z[j], p = exp(t);
+                const double t = lp[j], z = sh.z[j], p = row_exp(t);
                 P += p;
                 if (p != 0.0) A += p * (t - (z - shift) * r.it);
-                S += exp((z - shift) * r.it);
+                S += row_exp((z - shift) * r.it);
             }
             P = wave_sum_f64(P);
             A = wave_sum_f64(A);
@@ -196,25 +192,25 @@ struct DistillOp {
     {
         const float m = fmaxf(st.m, sh.m);
         const double shift = shift_of(m);
-        const double rest = (double)st.s * exp(((double)st.m - shift) * r.it);
-        const double own = sh.S * exp(((double)sh.m - shift) * r.it);
+        const double rest = (double)st.s * row_exp(((double)st.m - shift) * r.it);
+        const double own = sh.S * row_exp(((double)sh.m - shift) * r.it);
         const double S = rest + own;
         // lse less the listed maximum (a row may lie at the type's lowest
         // value, where lse itself holds no digit of log S); of a row of
         // nothing but -inf, A decides
-        const double lse = m == -INFINITY ? 0.0 : (shift - shift_of(sh.m)) * r.it + log(S);
+        const double lse = m == -INFINITY ? 0.0 : (shift - shift_of(sh.m)) * r.it + row_log(S);
         const double w = weight ? (double)weight[row] : 1.0;
         double P = sh.P, A = sh.A, R = 0.0, gp = 1.0, L;
         if (mode == SG_DISTILL_RENORM) {
             gp = P > 0.0 ? 1.0 / P : P; // nothing listed: no mass, no loss (a NaN stays)
-            L = P > 0.0 ? A * gp - log(P) + lse : P;
+            L = P > 0.0 ? A * gp - row_log(P) + lse : P;
             P = P > 0.0 ? 1.0 : P;
         } else {
             L = A + P * lse;
             // what is left for the unlisted tokens, where there are any
             if (mode == SG_DISTILL_TAIL && P < 1.0 && rest != 0.0) {
                 R = 1.0 - P;
-                L += R * (log(R) + log(S / rest));
+                L += R * (row_log(R) + row_log(S / rest));
             }
         }
         loss[row] = (float)(w * L);
@@ -233,7 +229,7 @@ struct DistillOp {
             const uint32_t i = id[j];
             if (i >= V) continue;
             const float e = exp2_fast((sh.z[j] - shift_of(co.m)) * r.c);
-            RowIO<E>::put(g + i, (float)((double)sh.within * e - sh.gp * exp((double)lp[j])));
+            RowIO<E>::put(g + i, (float)((double)sh.within * e - sh.gp * row_exp((double)lp[j])));
         }
     }
     // bit v of the result: element i0 + v is listed (i0 a multiple of n, n = 4 or 8)
@@ -256,78 +252,140 @@ __device__ __forceinline__ void zero_row(E* g, uint32_t V, uint32_t t, uint32_t 
     for (uint32_t i = nc * VEC + t; i < V; i += nt) RowIO<E>::put(g + i, 0.f);
 }
 
-// gradient of one element range: coef * exp2(c (x - m)).  x and g may be the
-// same row: every thread reads an element before it writes it, and nobody
-// else touches it.
+template <typename E>
+__device__ __forceinline__ void grad_chunk(u32x4 w, E* g, RowCoef k, float c)
+{
+    constexpr int VEC = RowIO<E>::VEC;
+    const float sh = shift_of(k.m);
+    float v[VEC];
+    RowIO<E>::unpack(w, v);
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) v[i] = k.coef * exp2_fast((v[i] - sh) * c);
+    store_chunk(g, RowIO<E>::pack(v));
+}
+
+// the elements after the last whole chunk
+template <typename E>
+__device__ __forceinline__ void grad_rest(const E* x, E* g, uint32_t V, RowCoef k, float c, uint32_t t, uint32_t nt)
+{
+    const float sh = shift_of(k.m);
+    for (uint32_t i = V / RowIO<E>::VEC * RowIO<E>::VEC + t; i < V; i += nt)
+        RowIO<E>::put(g + i, k.coef * exp2_fast((RowIO<E>::get(x + i) - sh) * c));
+}
+
+// gradient of a row: coef * exp2(c (x - m)).  x and g may be the same row:
+// every thread reads an element before it writes it, and nobody else touches
+// it.
 template <typename E>
 __device__ __forceinline__ void grad_row(const E* x, E* g, uint32_t V, RowCoef k, float c, uint32_t t, uint32_t nt)
 {
     constexpr int VEC = RowIO<E>::VEC;
     const uint32_t nc = V / VEC;
-    const float sh = shift_of(k.m);
-    for (uint32_t j = t; j < nc; j += nt) {
-        float v[VEC];
-        RowIO<E>::unpack(load_chunk(x + (uint64_t)j * VEC), v);
-#pragma unroll
-        for (int i = 0; i < VEC; ++i) v[i] = k.coef * exp2_fast((v[i] - sh) * c);
-        store_chunk(g + (uint64_t)j * VEC, RowIO<E>::pack(v));
-    }
-    for (uint32_t i = nc * VEC + t; i < V; i += nt)
-        RowIO<E>::put(g + i, k.coef * exp2_fast((RowIO<E>::get(x + i) - sh) * c));
+    for (uint32_t j = t; j < nc; j += nt)
+        grad_chunk<E>(load_chunk(x + (uint64_t)j * VEC), g + (uint64_t)j * VEC, k, c);
+    grad_rest(x, g, V, k, c, t, nt);
 }
 
-template <typename E, class Op, bool GRAD>
-__global__ __launch_bounds__(RL_NT) void row_loss_kernel(Rows r, Op op, void* grad, uint64_t ldg)
+// address of chunk j + j0: j is the same for all lanes, so it goes into a
+// scalar base and one 32-bit lane offset serves every chunk of the row
+template <typename E, typename P>
+__device__ __forceinline__ P* chunk_at(P* x, uint32_t j, uint32_t j0)
 {
-    constexpr int VEC = RowIO<E>::VEC, NT = RL_NT, NW = NT / SG_WAVE;
+    return x + (uint64_t)j * RowIO<E>::VEC + j0 * RowIO<E>::VEC;
+}
+
+// chunks j0, j0 + NT, ... of a row; past its end, chunks of -inf
+template <int J, int NT, typename E>
+__device__ __forceinline__ void load_chunks(u32x4* w, const E* x, uint32_t j0, uint32_t nc)
+{
+    constexpr uint32_t none = RowIO<E>::VEC == 8 ? 0xff80ff80u : 0xff800000u;
+#pragma unroll
+    for (int j = 0; j < J; ++j) {
+        w[j] = u32x4{none, none, none, none};
+        if (j0 + j * NT < nc) w[j] = load_chunk(chunk_at<E>(x, j * NT, j0));
+    }
+}
+
+template <typename E, int J, int NT, class Op>
+__device__ __forceinline__ void stat_chunks(RowStat& st, const u32x4* w, const Op& op, const uint32_t* bm, uint32_t j0,
+                                            float c)
+{
+    constexpr int VEC = RowIO<E>::VEC;
+#pragma unroll
+    for (int j = 0; j < J; ++j) {
+        float v[VEC];
+        u32x4 u = w[j];
+        if (Op::kListed) {
+            const uint32_t b = op.bits(bm, (j0 + j * NT) * VEC, VEC);
+            if (b) u = RowIO<E>::without(u, b);
+            asm volatile("" : "+v"(u)); // one unpacked form of the chunk, not one for each side of the branch
+        }
+        RowIO<E>::unpack(u, v);
+        stat_add<VEC>(st, v, c);
+        __builtin_amdgcn_sched_barrier(0); // a chunk at a time: unpacked, a chunk takes twice its registers
+    }
+}
+
+// One block per row (no loop over rows: the constants of the fp64 functions
+// would be hoisted out of it into registers that the row needs).  With GRAD the first NT * J chunks of the
+// row stay in registers from the sums to the gradient, so the row is read
+// from HBM once; what is beyond them is read again (from the last-level cache,
+// the blocks in flight hold few rows).  Without GRAD nothing is kept and J is
+// the number of loads a thread has in flight.
+template <typename E, int NT, int J, class Op, bool GRAD>
+__global__ __launch_bounds__(NT) void row_loss_kernel(Rows r, Op op, void* grad, uint64_t ldg)
+{
+    constexpr int VEC = RowIO<E>::VEC, NW = NT / SG_WAVE;
     extern __shared__ uint32_t rl_bitmap[];
     __shared__ typename Op::Shared sh;
     __shared__ RowStat part[NW];
     __shared__ RowCoef coef;
-    const uint32_t t = threadIdx.x;
-    for (uint64_t row = blockIdx.x; row < r.T; row += gridDim.x) {
-        const E* x = static_cast<const E*>(r.x) + row * r.ld;
-        E* g = GRAD ? static_cast<E*>(grad) + row * ldg : nullptr;
-        if (!op.live(row)) { // the same for the whole block
-            if (t == 0) op.skip(row);
-            if (GRAD) zero_row(g, r.V, t, NT);
-            continue;
-        }
-        op.template begin<E, NT>(r, row, x, sh, rl_bitmap);
-        RowStat st = {-INFINITY, 0.f};
-        const uint32_t nc = r.V / VEC;
-        for (uint32_t j = t; j < nc; j += NT) {
-            float v[VEC];
-            RowIO<E>::unpack(load_chunk(x + (uint64_t)j * VEC), v);
-            const uint32_t b = op.bits(rl_bitmap, j * VEC, VEC);
-            if (b) {
+    const uint32_t t = threadIdx.x, nc = r.V / VEC;
+    const uint64_t row = r.row0 + blockIdx.x;
+    const E* x = static_cast<const E*>(r.x) + row * r.ld;
+    E* g = GRAD ? static_cast<E*>(grad) + row * ldg : nullptr;
+    if (!op.live(row)) { // the same for the whole block
+        if (t == 0) op.skip(row);
+        if (GRAD) zero_row(g, r.V, t, NT);
+        return;
+    }
+    u32x4 kept[J];
+    load_chunks<J, NT>(kept, x, t, nc);
+    op.template begin<E, NT>(r, row, x, sh, rl_bitmap);
+    RowStat st = {-INFINITY, 0.f};
+    stat_chunks<E, J, NT>(st, kept, op, rl_bitmap, t, r.c);
+    constexpr int M = GRAD ? 2 : J; // chunks in flight beyond the kept ones
+    for (uint32_t j = t + J * NT; j < nc; j += M * NT) {
+        u32x4 more[M];
+        load_chunks<M, NT>(more, x, j, nc);
+        stat_chunks<E, M, NT>(st, more, op, rl_bitmap, j, r.c);
+    }
+    for (uint32_t i = nc * VEC + t; i < r.V; i += NT) {
+        float v = RowIO<E>::get(x + i);
+        if (Op::kListed && op.bits(rl_bitmap, i, 1)) v = -INFINITY;
+        stat_add<1>(st, &v, r.c);
+    }
+    st = wave_stat(st, r.c);
+    if (lane_id() == 0) part[t / SG_WAVE] = st;
+    __syncthreads();
+    if (t < NW) {
+        const RowStat a = wave_stat<NW>(part[t], r.c);
+        if (t == 0) coef = op.finish(r, row, a, sh);
+    }
+    if constexpr (GRAD) {
+    __syncthreads();
+    const RowCoef k = coef;
 #pragma unroll
-                for (int i = 0; i < VEC; ++i)
-                    if (b >> i & 1u) v[i] = -INFINITY;
-            }
-            stat_add<VEC>(st, v, r.c);
-        }
-        for (uint32_t i = nc * VEC + t; i < r.V; i += NT) {
-            float v = RowIO<E>::get(x + i);
-            if (Op::kListed && op.bits(rl_bitmap, i, 1)) v = -INFINITY;
-            stat_add<1>(st, &v, r.c);
-        }
-        st = wave_stat(st, r.c);
-        if (lane_id() == 0) part[t / SG_WAVE] = st;
-        __syncthreads();
-        if (t == 0) {
-            RowStat a = part[0];
-            for (int w = 1; w < NW; ++w) a = stat_join(a, part[w], r.c);
-            coef = op.finish(r, row, a, sh);
-        }
-        __syncthreads();
-        if (GRAD) {
-            const RowCoef k = coef;
-            grad_row(x, g, r.V, k, r.c, t, NT);
-            __syncthreads(); // the corrections overwrite elements of other threads
-            op.template fix<E, NT>(r, row, g, sh, k);
-        }
-        __syncthreads();
+    for (int j = 0; j < J; ++j) {
+        asm volatile("" : "+v"(kept[j])); // unpack again rather than keep the unpacked values
+        if (t + j * NT < nc) grad_chunk<E>(kept[j], chunk_at<E>(g, j * NT, t), k, r.c);
+        __builtin_amdgcn_sched_barrier(0);
+    }
+    for (uint32_t j = t + J * NT; j < nc; j += NT)
+        grad_chunk<E>(load_chunk(x + (uint64_t)j * VEC), g + (uint64_t)j * VEC, k, r.c);
+    grad_rest(x, g, r.V, k, r.c, t, NT);
+    __syncthreads(); // the corrections overwrite elements of other threads
+    op.template fix<E, NT>(r, row, g, sh, k);
     }
 }
 
@@ -399,7 +457,7 @@ __global__ __launch_bounds__(PF_NT) void pref_pair_kernel(PairArgs p)
                 L = gap <= 0.0 ? 0.0 : gap; // a NaN stays
                 g = gap <= 0.0 ? 0.0 : -p.beta;
             } else {
-                const double h = p.beta * d, u = exp(-fabs(h)), l = log1p(u);
+                const double h = p.beta * d, u = row_exp(-fabs(h)), l = row_log1p(u);
                 const double up = l + (h < 0.0 ? -h : 0.0), down = l + (h > 0.0 ? h : 0.0);
                 L = (1.0 - p.eps) * up + (p.eps != 0.0 ? p.eps * down : 0.0);
                 const double sig = h >= 0.0 ? 1.0 / (1.0 + u) : u / (1.0 + u);
@@ -439,13 +497,15 @@ __global__ __launch_bounds__(RL_NT) void pref_grad_kernel(Rows r, TokenOp op, vo
         grad_row(x, g, r.V, RowCoef{op.m[row], -slope * op.inv[row]}, r.c, threadIdx.x, RL_NT);
         __syncthreads();
         if (threadIdx.x == 0)
-            RowIO<E>::put(g + op.label[row], (float)((double)slope * -expm1(op.logp[row])));
+            RowIO<E>::put(g + op.label[row], (float)((double)slope * -row_expm1(op.logp[row])));
     }
 }
 
 // ---------------------------------------------------------------------------
 // host side
 // ---------------------------------------------------------------------------
+constexpr uint64_t ROWS_PER_LAUNCH = 1u << 20; // a launch holds fewer than 2^32 threads
+
 struct RowCheck {
     Rows r;
     unsigned grid;
@@ -462,6 +522,7 @@ static int rows_args(const void* x, sg_dtype dt, uint64_t T, uint64_t V, uint64_
     if (T > 0 && (!x || reinterpret_cast<uintptr_t>(x) % row_esize(dt) != 0)) return SG_EINVAL;
     out->r.x = x;
     out->r.T = T;
+    out->r.row0 = 0;
     out->r.ld = ld;
     out->r.V = (uint32_t)V;
     out->r.it = inv_temp;
@@ -478,19 +539,36 @@ static int grad_args(const void* x, uint64_t ld, const void* grad, sg_dtype dt, 
     return SG_OK;
 }
 
+template <typename E, int NT, int J, class Op>
+static int launch_rows(const RowCheck& c, const Op& op, size_t lds, void* grad, uint64_t ldg, hipStream_t st)
+{
+    Rows r = c.r;
+    for (r.row0 = 0; r.row0 < r.T; r.row0 += ROWS_PER_LAUNCH) {
+        const uint64_t left = r.T - r.row0;
+        const unsigned grid = (unsigned)(left < ROWS_PER_LAUNCH ? left : ROWS_PER_LAUNCH);
+        if constexpr (Op::kGrad)
+            if (grad) row_loss_kernel<E, NT, J, Op, true><<<grid, NT, lds, st>>>(r, op, grad, ldg);
+        if (!grad) row_loss_kernel<E, NT, 4, Op, false><<<grid, NT, lds, st>>>(r, op, grad, ldg);
+        SG_TRY_LAUNCH();
+    }
+    return SG_OK;
+}
+
+template <typename E, class Op>
+static int launch_row_loss_of(const RowCheck& c, const Op& op, size_t lds, void* grad, uint64_t ldg, hipStream_t st)
+{
+    const uint64_t bytes = (uint64_t)c.r.V * sizeof(E);
+    if (bytes <= 256 * 8 * 16) return launch_rows<E, 256, 8>(c, op, lds, grad, ldg, st);
+    if (bytes <= 512 * 16 * 16) return launch_rows<E, 512, 16>(c, op, lds, grad, ldg, st);
+    return launch_rows<E, 1024, 16>(c, op, lds, grad, ldg, st);
+}
+
 template <class Op>
 static int launch_row_loss(const RowCheck& c, sg_dtype dt, const Op& op, size_t lds, void* grad, uint64_t ldg,
                            hipStream_t st)
 {
-    if (dt == SG_BF16) {
-        if (grad) row_loss_kernel<bf16_bits, Op, true><<<c.grid, RL_NT, lds, st>>>(c.r, op, grad, ldg);
-        else row_loss_kernel<bf16_bits, Op, false><<<c.grid, RL_NT, lds, st>>>(c.r, op, grad, ldg);
-    } else {
-        if (grad) row_loss_kernel<float, Op, true><<<c.grid, RL_NT, lds, st>>>(c.r, op, grad, ldg);
-        else row_loss_kernel<float, Op, false><<<c.grid, RL_NT, lds, st>>>(c.r, op, grad, ldg);
-    }
-    SG_TRY_LAUNCH();
-    return SG_OK;
+    if (dt == SG_BF16) return launch_row_loss_of<bf16_bits>(c, op, lds, grad, ldg, st);
+    return launch_row_loss_of<float>(c, op, lds, grad, ldg, st);
 }
 
 } // namespace sg

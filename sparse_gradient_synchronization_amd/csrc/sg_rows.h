@@ -15,6 +15,7 @@ typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 struct Rows {
     const void* x; // [T] rows, ld elements apart
     uint64_t T, ld;
+    uint64_t row0; // first row of this launch
     uint32_t V;
     float c;   // exp(inv_temp * d) = exp2(c * d)
     double it; // inv_temp
@@ -46,6 +47,13 @@ struct RowIO<float> {
         for (int i = 0; i < 4; ++i) w[i] = __float_as_uint(v[i]);
         return w;
     }
+    // the elements of set bits replaced by -inf
+    static __device__ __forceinline__ u32x4 without(u32x4 w, uint32_t b)
+    {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) w[i] = b >> i & 1u ? 0xff800000u : w[i];
+        return w;
+    }
     static __device__ __forceinline__ float get(const float* p) { return *p; }
     static __device__ __forceinline__ void put(float* p, float v) { *p = v; }
 };
@@ -62,6 +70,15 @@ struct RowIO<bf16_bits> {
             v[2 * i] = __uint_as_float(w[i] << 16);
             v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
         }
+    }
+    static __device__ __forceinline__ u32x4 without(u32x4 w, uint32_t b)
+    {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            w[i] = b >> (2 * i) & 1u ? (w[i] & 0xffff0000u) | 0xff80u : w[i];
+            w[i] = b >> (2 * i + 1) & 1u ? (w[i] & 0xffffu) | 0xff800000u : w[i];
+        }
+        return w;
     }
     // rounded to nearest even, once, from the fp32 value
     static __device__ __forceinline__ u32x4 pack(const float* v)
@@ -125,11 +142,13 @@ __device__ __forceinline__ RowStat stat_join(RowStat a, RowStat b, float c)
     return {m, a.s * exp2_fast((a.m - sh) * c) + b.s * exp2_fast((b.m - sh) * c)};
 }
 
-// the lanes' parts joined in a fixed order; every lane holds the result
+// the parts of the first N lanes (of every N) joined in a fixed order; every
+// lane holds its result
+template <int N = SG_WAVE>
 __device__ __forceinline__ RowStat wave_stat(RowStat r, float c)
 {
 #pragma unroll
-    for (int d = 1; d < SG_WAVE; d <<= 1) {
+    for (int d = 1; d < N; d <<= 1) {
         RowStat o = {__shfl_xor(r.m, d, SG_WAVE), __shfl_xor(r.s, d, SG_WAVE)};
         // the lower lane's part first on both sides, so both hold the same bits
         r = (lane_id() & d) ? stat_join(o, r, c) : stat_join(r, o, c);
@@ -142,6 +161,66 @@ __device__ __forceinline__ double wave_sum_f64(double v)
 #pragma unroll
     for (int d = 1; d < SG_WAVE; d <<= 1) v += __shfl_xor(v, d, SG_WAVE);
     return v;
+}
+
+// exp and log of the row scalars in fp64, from their series: 1e-12 relative
+// is plenty for results of 24 bits.  The loops are not unrolled: the library's
+// own functions keep some 60 registers of constants alive, which the row held
+// in registers has no room for.
+__device__ constexpr double kRowInv[12] = {1.0, 1.0, 1.0 / 2, 1.0 / 3, 1.0 / 4, 1.0 / 5, 1.0 / 6, 1.0 / 7, 1.0 / 8,
+                                           1.0 / 9, 1.0 / 10, 1.0 / 11};
+__device__ constexpr double kRowOdd[9] = {1.0, 1.0 / 3, 1.0 / 5, 1.0 / 7, 1.0 / 9, 1.0 / 11, 1.0 / 13, 1.0 / 15,
+                                          1.0 / 17};
+constexpr double kLn2 = 0.69314718055994530942, kLn2Lo = 2.3190468138462996e-17; // kLn2 + kLn2Lo = log 2
+
+// exp(r) - 1 for |r| <= 0.35: r (1 + r/2 (1 + r/3 (...)))
+__device__ __forceinline__ double row_expm1_small(double r)
+{
+    double a = 1.0;
+#pragma unroll 1
+    for (int n = 11; n > 1; --n) a = 1.0 + r * kRowInv[n] * a;
+    return r * a;
+}
+
+__device__ __forceinline__ double row_exp(double x)
+{
+    if (!(x > -745.0)) return x != x ? x : 0.0;
+    if (x > 709.7) return INFINITY;
+    const double k = rint(x * (1.0 / kLn2));
+    const double r = (x - k * kLn2) - k * kLn2Lo;
+    return ldexp(1.0 + row_expm1_small(r), (int)k);
+}
+
+__device__ __forceinline__ double row_expm1(double x)
+{
+    return fabs(x) <= 0.34 ? row_expm1_small(x) : row_exp(x) - 1.0;
+}
+
+// log(m 2^e) = e log 2 + 2 (s + s^3/3 + s^5/5 + ...), s = (m - 1) / (m + 1), m in [1/sqrt 2, sqrt 2]
+__device__ __forceinline__ double row_log(double x)
+{
+    if (!(x > 0.0) || x == INFINITY) return x == 0.0 ? -(double)INFINITY : x;
+    double m = __builtin_amdgcn_frexp_mant(x);
+    int e = __builtin_amdgcn_frexp_exp(x);
+    if (m < 0.70710678118654752440) {
+        m *= 2.0;
+        --e;
+    }
+    const double s = (m - 1.0) / (m + 1.0), q = s * s;
+    double a = kRowOdd[8];
+#pragma unroll 1
+    for (int n = 7; n >= 0; --n) a = a * q + kRowOdd[n];
+    return e * kLn2 + 2.0 * s * a;
+}
+
+// log(1 + u) for u in [0, 1]
+__device__ __forceinline__ double row_log1p(double u)
+{
+    const double s = u / (2.0 + u), q = s * s; // at most 1/3
+    double a = 0.0;
+#pragma unroll 1
+    for (int n = 14; n >= 0; --n) a = a * q + 1.0 / (2 * n + 1);
+    return 2.0 * s * a;
 }
 
 // 1/S with a row of nothing (S = 0) giving 0; a NaN stays
