@@ -49,7 +49,7 @@ struct PolicyOp {
         if (logp) logp[row] = 0.f;
     }
     template <typename E, int NT>
-    __device__ __forceinline__ void begin(const Rows&, uint64_t row, const E* x, Shared& sh, uint32_t*) const
+    __device__ __forceinline__ void begin(const Rows&, uint64_t row, const E* x, uint32_t, Shared& sh, uint32_t*) const
     {
         if (threadIdx.x == 0) sh.za = RowIO<E>::get(x + action[row]);
     }
@@ -108,7 +108,7 @@ struct TokenOp {
         slope[row] = 0.f;
     }
     template <typename E, int NT>
-    __device__ __forceinline__ void begin(const Rows&, uint64_t row, const E* x, Shared& sh, uint32_t*) const
+    __device__ __forceinline__ void begin(const Rows&, uint64_t row, const E* x, uint32_t, Shared& sh, uint32_t*) const
     {
         if (threadIdx.x == 0) sh.za = RowIO<E>::get(x + label[row]);
     }
@@ -149,17 +149,18 @@ struct DistillOp {
     __device__ __forceinline__ bool live(uint64_t row) const { return !weight || weight[row] != 0.f; }
     __device__ __forceinline__ void skip(uint64_t row) const { loss[row] = 0.f; }
     template <typename E, int NT>
-    __device__ __forceinline__ void begin(const Rows& r, uint64_t row, const E* x, Shared& sh, uint32_t* bm) const
+    __device__ __forceinline__ void begin(const Rows& r, uint64_t row, const E* x, uint32_t pad, Shared& sh,
+                                          uint32_t* bm) const
     {
         const uint32_t* id = idx + row * k;
         const float* lp = logp + row * k;
-        for (uint32_t i = threadIdx.x; i < (V + 31) / 32; i += NT) bm[i] = 0;
+        for (uint32_t i = threadIdx.x; i < (V + pad + 31) / 32; i += NT) bm[i] = 0;
         __syncthreads();
         for (uint32_t j = threadIdx.x; j < k; j += NT) {
             const uint32_t i = id[j];
             if (i >= V) continue;
-            const uint32_t was = atomicOr(&bm[i / 32], 1u << (i % 32));
-            if (was >> (i % 32) & 1u) report_error(kDevErrUnsorted); // listed twice
+            const uint32_t at = i + pad, was = atomicOr(&bm[at / 32], 1u << (at % 32));
+            if (was >> (at % 32) & 1u) report_error(kDevErrUnsorted); // listed twice
             sh.z[j] = RowIO<E>::get(x + i);
         }
         __syncthreads();
@@ -232,7 +233,8 @@ struct DistillOp {
             RowIO<E>::put(g + i, (float)((double)sh.within * e - sh.gp * row_exp((double)lp[j])));
         }
     }
-    // bit v of the result: element i0 + v is listed (i0 a multiple of n, n = 4 or 8)
+    // bit v of the result: element i0 + v - pad is listed (i0 a multiple of n = 4 or 8, or n = 1); pad is
+    // what makes the first element of a chunk a multiple of the chunk's size
     __device__ __forceinline__ uint32_t bits(const uint32_t* bm, uint32_t i0, int n) const
     {
         return bm[i0 / 32] >> (i0 % 32) & ((1u << n) - 1u);
@@ -242,14 +244,23 @@ struct DistillOp {
 // ---------------------------------------------------------------------------
 // one block per row
 // ---------------------------------------------------------------------------
+// address of chunk j + j0: j is the same for all lanes, so it goes into a
+// scalar base and one 32-bit lane offset serves every chunk of the row
+template <typename E, typename P>
+__device__ __forceinline__ P* chunk_at(P* x, uint32_t j, uint32_t j0)
+{
+    return x + (uint64_t)j * RowIO<E>::VEC + j0 * RowIO<E>::VEC;
+}
+
 template <typename E>
 __device__ __forceinline__ void zero_row(E* g, uint32_t V, uint32_t t, uint32_t nt)
 {
     constexpr int VEC = RowIO<E>::VEC;
-    const uint32_t nc = V / VEC;
+    const RowSpan sp = span_of(g, V);
     const u32x4 z = {0, 0, 0, 0};
-    for (uint32_t j = t; j < nc; j += nt) store_chunk(g + (uint64_t)j * VEC, z);
-    for (uint32_t i = nc * VEC + t; i < V; i += nt) RowIO<E>::put(g + i, 0.f);
+#pragma unroll 4
+    for (uint32_t j = t; j < sp.nc; j += nt) store_chunk(chunk_at<E>(g + sp.head, j, 0), z);
+    for (uint32_t i = loose_element(sp, VEC, t); i < V; i = loose_element(sp, VEC, t += nt)) RowIO<E>::put(g + i, 0.f);
 }
 
 template <typename E>
@@ -264,12 +275,15 @@ __device__ __forceinline__ void grad_chunk(u32x4 w, E* g, RowCoef k, float c)
     store_chunk(g, RowIO<E>::pack(v));
 }
 
-// the elements after the last whole chunk
+// the elements outside the chunks
 template <typename E>
-__device__ __forceinline__ void grad_rest(const E* x, E* g, uint32_t V, RowCoef k, float c, uint32_t t, uint32_t nt)
+__device__ __forceinline__ void grad_loose(const E* x, E* g, const RowSpan& sp, RowCoef k, float c, uint32_t t,
+                                           uint32_t nt)
 {
+    constexpr int VEC = RowIO<E>::VEC;
     const float sh = shift_of(k.m);
-    for (uint32_t i = V / RowIO<E>::VEC * RowIO<E>::VEC + t; i < V; i += nt)
+#pragma unroll 1
+    for (uint32_t i = loose_element(sp, VEC, t); i < sp.V; i = loose_element(sp, VEC, t += nt))
         RowIO<E>::put(g + i, k.coef * exp2_fast((RowIO<E>::get(x + i) - sh) * c));
 }
 
@@ -279,68 +293,60 @@ __device__ __forceinline__ void grad_rest(const E* x, E* g, uint32_t V, RowCoef 
 template <typename E>
 __device__ __forceinline__ void grad_row(const E* x, E* g, uint32_t V, RowCoef k, float c, uint32_t t, uint32_t nt)
 {
-    constexpr int VEC = RowIO<E>::VEC;
-    const uint32_t nc = V / VEC;
-    for (uint32_t j = t; j < nc; j += nt)
-        grad_chunk<E>(load_chunk(x + (uint64_t)j * VEC), g + (uint64_t)j * VEC, k, c);
-    grad_rest(x, g, V, k, c, t, nt);
+    const RowSpan sp = span_of(x, V);
+#pragma unroll 2
+    for (uint32_t j = t; j < sp.nc; j += nt)
+        grad_chunk<E>(load_chunk(chunk_at<E>(x + sp.head, j, 0)), chunk_at<E>(g + sp.head, j, 0), k, c);
+    grad_loose(x, g, sp, k, c, t, nt);
 }
 
-// address of chunk j + j0: j is the same for all lanes, so it goes into a
-// scalar base and one 32-bit lane offset serves every chunk of the row
-template <typename E, typename P>
-__device__ __forceinline__ P* chunk_at(P* x, uint32_t j, uint32_t j0)
-{
-    return x + (uint64_t)j * RowIO<E>::VEC + j0 * RowIO<E>::VEC;
-}
-
-// chunks j0, j0 + NT, ... of a row; past its end, chunks of -inf
+// chunks j0, j0 + NT, ... of a row
 template <int J, int NT, typename E>
 __device__ __forceinline__ void load_chunks(u32x4* w, const E* x, uint32_t j0, uint32_t nc)
 {
-    constexpr uint32_t none = RowIO<E>::VEC == 8 ? 0xff80ff80u : 0xff800000u;
 #pragma unroll
-    for (int j = 0; j < J; ++j) {
-        w[j] = u32x4{none, none, none, none};
+    for (int j = 0; j < J; ++j)
         if (j0 + j * NT < nc) w[j] = load_chunk(chunk_at<E>(x, j * NT, j0));
-    }
 }
 
 template <typename E, int J, int NT, class Op>
 __device__ __forceinline__ void stat_chunks(RowStat& st, const u32x4* w, const Op& op, const uint32_t* bm, uint32_t j0,
-                                            float c)
+                                            uint32_t nc, float c)
 {
     constexpr int VEC = RowIO<E>::VEC;
 #pragma unroll
     for (int j = 0; j < J; ++j) {
-        float v[VEC];
-        u32x4 u = w[j];
-        if (Op::kListed) {
-            const uint32_t b = op.bits(bm, (j0 + j * NT) * VEC, VEC);
-            if (b) u = RowIO<E>::without(u, b);
-            asm volatile("" : "+v"(u)); // one unpacked form of the chunk, not one for each side of the branch
+        if (j0 + j * NT < nc) {
+            float v[VEC];
+            u32x4 u = w[j];
+            if (Op::kListed) {
+                const uint32_t b = op.bits(bm, (j0 + j * NT + 1) * VEC, VEC);
+                if (b) u = RowIO<E>::without(u, b);
+                asm volatile("" : "+v"(u)); // one unpacked form of the chunk, not one for each side of the branch
+            }
+            RowIO<E>::unpack(u, v);
+            stat_add<VEC>(st, v, c);
         }
-        RowIO<E>::unpack(u, v);
-        stat_add<VEC>(st, v, c);
         __builtin_amdgcn_sched_barrier(0); // a chunk at a time: unpacked, a chunk takes twice its registers
     }
 }
 
 // One block per row (no loop over rows: the constants of the fp64 functions
-// would be hoisted out of it into registers that the row needs).  With GRAD the first NT * J chunks of the
-// row stay in registers from the sums to the gradient, so the row is read
-// from HBM once; what is beyond them is read again (from the last-level cache,
-// the blocks in flight hold few rows).  Without GRAD nothing is kept and J is
-// the number of loads a thread has in flight.
+// would be hoisted out of it into registers that the row needs).  With GRAD
+// the first NT * J chunks of the row stay in registers from the sums to the
+// gradient, so the row is read from HBM once; what is beyond them is read
+// again (from the last-level cache, the blocks in flight hold few rows).
+// Without GRAD nothing is kept and J is the number of loads a thread has in
+// flight.
 template <typename E, int NT, int J, class Op, bool GRAD>
-__global__ __launch_bounds__(NT) void row_loss_kernel(Rows r, Op op, void* grad, uint64_t ldg)
+__global__ __launch_bounds__(NT, GRAD ? 4 : 8) void row_loss_kernel(Rows r, Op op, void* grad, uint64_t ldg)
 {
     constexpr int VEC = RowIO<E>::VEC, NW = NT / SG_WAVE;
     extern __shared__ uint32_t rl_bitmap[];
     __shared__ typename Op::Shared sh;
     __shared__ RowStat part[NW];
     __shared__ RowCoef coef;
-    const uint32_t t = threadIdx.x, nc = r.V / VEC;
+    const uint32_t t = threadIdx.x;
     const uint64_t row = r.row0 + blockIdx.x;
     const E* x = static_cast<const E*>(r.x) + row * r.ld;
     E* g = GRAD ? static_cast<E*>(grad) + row * ldg : nullptr;
@@ -349,21 +355,27 @@ __global__ __launch_bounds__(NT) void row_loss_kernel(Rows r, Op op, void* grad,
         if (GRAD) zero_row(g, r.V, t, NT);
         return;
     }
+    const RowSpan sp = span_of(x, r.V);
+    const E* xc = x + sp.head;
     u32x4 kept[J];
-    load_chunks<J, NT>(kept, x, t, nc);
-    op.template begin<E, NT>(r, row, x, sh, rl_bitmap);
+    load_chunks<J, NT>(kept, xc, t, sp.nc);
+    op.template begin<E, NT>(r, row, x, VEC - sp.head, sh, rl_bitmap);
     RowStat st = {-INFINITY, 0.f};
-    stat_chunks<E, J, NT>(st, kept, op, rl_bitmap, t, r.c);
+    stat_chunks<E, J, NT>(st, kept, op, rl_bitmap, t, sp.nc, r.c);
     constexpr int M = GRAD ? 2 : J; // chunks in flight beyond the kept ones
-    for (uint32_t j = t + J * NT; j < nc; j += M * NT) {
+#pragma unroll 1
+    for (uint32_t j = t + J * NT; j < sp.nc; j += M * NT) {
         u32x4 more[M];
-        load_chunks<M, NT>(more, x, j, nc);
-        stat_chunks<E, M, NT>(st, more, op, rl_bitmap, j, r.c);
+        load_chunks<M, NT>(more, xc, j, sp.nc);
+        stat_chunks<E, M, NT>(st, more, op, rl_bitmap, j, sp.nc, r.c);
     }
-    for (uint32_t i = nc * VEC + t; i < r.V; i += NT) {
-        float v = RowIO<E>::get(x + i);
-        if (Op::kListed && op.bits(rl_bitmap, i, 1)) v = -INFINITY;
-        stat_add<1>(st, &v, r.c);
+    if (t < 2 * VEC) {
+        const uint32_t i = loose_element(sp, VEC, t);
+        if (i < r.V) {
+            float v = RowIO<E>::get(x + i);
+            if (Op::kListed && op.bits(rl_bitmap, i + VEC - sp.head, 1)) v = -INFINITY;
+            stat_add<1>(st, &v, r.c);
+        }
     }
     st = wave_stat(st, r.c);
     if (lane_id() == 0) part[t / SG_WAVE] = st;
@@ -373,19 +385,21 @@ __global__ __launch_bounds__(NT) void row_loss_kernel(Rows r, Op op, void* grad,
         if (t == 0) coef = op.finish(r, row, a, sh);
     }
     if constexpr (GRAD) {
-    __syncthreads();
-    const RowCoef k = coef;
+        __syncthreads();
+        const RowCoef k = coef;
+        E* gc = g + sp.head;
 #pragma unroll
-    for (int j = 0; j < J; ++j) {
-        asm volatile("" : "+v"(kept[j])); // unpack again rather than keep the unpacked values
-        if (t + j * NT < nc) grad_chunk<E>(kept[j], chunk_at<E>(g, j * NT, t), k, r.c);
-        __builtin_amdgcn_sched_barrier(0);
-    }
-    for (uint32_t j = t + J * NT; j < nc; j += NT)
-        grad_chunk<E>(load_chunk(x + (uint64_t)j * VEC), g + (uint64_t)j * VEC, k, r.c);
-    grad_rest(x, g, r.V, k, r.c, t, NT);
-    __syncthreads(); // the corrections overwrite elements of other threads
-    op.template fix<E, NT>(r, row, g, sh, k);
+        for (int j = 0; j < J; ++j) {
+            asm volatile("" : "+v"(kept[j])); // unpack again rather than keep the unpacked values
+            if (t + j * NT < sp.nc) grad_chunk<E>(kept[j], chunk_at<E>(gc, j * NT, t), k, r.c);
+            __builtin_amdgcn_sched_barrier(0);
+        }
+#pragma unroll 1
+        for (uint32_t j = t + J * NT; j < sp.nc; j += NT)
+            grad_chunk<E>(load_chunk(chunk_at<E>(xc, j, 0)), chunk_at<E>(gc, j, 0), k, r.c);
+        grad_loose(x, g, sp, k, r.c, t, NT);
+        __syncthreads(); // the corrections overwrite elements of other threads
+        op.template fix<E, NT>(r, row, g, sh, k);
     }
 }
 
@@ -592,7 +606,7 @@ extern "C" int sg_distill_loss(const void* d_logits, sg_dtype dt, uint64_t T, ui
     if (k > SG_ROWS_MAX_K || V > 14 * 32768u) return SG_EUNSUPPORTED;
     if (T == 0) return SG_OK;
     DistillOp op = {d_idx, d_logp, d_weight, d_loss, k, (uint32_t)V, (int)mode};
-    return launch_row_loss(c, dt, op, ceil_div(V, 32) * 4, d_grad, ld_grad, as_stream(stream));
+    return launch_row_loss(c, dt, op, ceil_div(V + 8, 32) * 4, d_grad, ld_grad, as_stream(stream));
 }
 
 extern "C" size_t sg_policy_workspace_bytes(uint64_t T, uint64_t V, sg_dtype dt) { return 0; }

@@ -1,10 +1,13 @@
 // sg_rows.h -- device helpers of the vocabulary operators: rows of logits
 // read as 16-byte chunks, and the running maximum and sum of a softmax.
 //
-// A row is V elements of fp32 or bf16 that start anywhere (rows of an odd
-// vocabulary are only element-aligned; gfx950 loads and stores 16 bytes at
-// any address).  Chunk j holds elements [j*VEC, (j+1)*VEC); the V % VEC
-// elements after the last whole chunk are handled one by one.
+// A row is V elements of fp32 or bf16 that start anywhere: rows of an odd
+// vocabulary are only element-aligned.  gfx950 loads and stores 16 bytes at
+// any address, but a wave's unaligned kilobyte touches one more cache line
+// than it fills: reading 3000 rows of 100003 bf16 ran at 4.9 TB/s that way
+// and at 6.2 TB/s with rows that start on 16 bytes.  So the chunks of a row
+// start at its first 16-byte boundary, `head` elements in; the elements
+// before it and after the last whole chunk are handled one by one.
 #pragma once
 #include "sg_device.h"
 
@@ -20,6 +23,29 @@ struct Rows {
     float c;   // exp(inv_temp * d) = exp2(c * d)
     double it; // inv_temp
 };
+
+// the chunks of one row
+struct RowSpan {
+    uint32_t head, nc, V; // first element of chunk 0, whole chunks, elements
+};
+
+template <typename E>
+__device__ __forceinline__ RowSpan span_of(const E* x, uint32_t V)
+{
+    constexpr uint32_t VEC = 16 / sizeof(E);
+    RowSpan s;
+    s.head = (uint32_t)(-(reinterpret_cast<uintptr_t>(x) / sizeof(E))) % VEC;
+    s.head = s.head < V ? s.head : V;
+    s.nc = (V - s.head) / VEC;
+    s.V = V;
+    return s;
+}
+
+// the i-th element outside the chunks, V or more if there is none
+__device__ __forceinline__ uint32_t loose_element(const RowSpan& s, uint32_t vec, uint32_t i)
+{
+    return i < s.head ? i : i + s.nc * vec;
+}
 
 // what one pass over (a part of) a row gives: maximum of the raw logits and
 // sum of exp2(c * (x - m)); {-inf, 0} for nothing.  fp32: every thread adds
@@ -164,31 +190,36 @@ __device__ __forceinline__ double wave_sum_f64(double v)
 }
 
 // exp and log of the row scalars in fp64, from their series: 1e-12 relative
-// is plenty for results of 24 bits.  The loops are not unrolled: the library's
-// own functions keep some 60 registers of constants alive, which the row held
-// in registers has no room for.
-__device__ constexpr double kRowInv[12] = {1.0, 1.0, 1.0 / 2, 1.0 / 3, 1.0 / 4, 1.0 / 5, 1.0 / 6, 1.0 / 7, 1.0 / 8,
-                                           1.0 / 9, 1.0 / 10, 1.0 / 11};
-__device__ constexpr double kRowOdd[9] = {1.0, 1.0 / 3, 1.0 / 5, 1.0 / 7, 1.0 / 9, 1.0 / 11, 1.0 / 13, 1.0 / 15,
-                                          1.0 / 17};
+// is plenty for results of 24 bits.  Terms are added one at a time (the
+// scheduling barrier): left alone, the compiler loads all constants first,
+// into registers that the row held in them has no room for.
+template <int N>
+__device__ __forceinline__ double series_step(double a, double q, const double (&k)[N])
+{
+#pragma unroll
+    for (int n = N - 1; n >= 0; --n) {
+        a = a * q + k[n];
+        __builtin_amdgcn_sched_barrier(0);
+    }
+    return a;
+}
+
 constexpr double kLn2 = 0.69314718055994530942, kLn2Lo = 2.3190468138462996e-17; // kLn2 + kLn2Lo = log 2
 
-// exp(r) - 1 for |r| <= 0.35: r (1 + r/2 (1 + r/3 (...)))
+// exp(r) - 1 for |r| <= 0.35: r + r^2/2! + ... + r^11/11!
 __device__ __forceinline__ double row_expm1_small(double r)
 {
-    double a = 1.0;
-#pragma unroll 1
-    for (int n = 11; n > 1; --n) a = 1.0 + r * kRowInv[n] * a;
-    return r * a;
+    constexpr double k[11] = {1.0, 1.0 / 2, 1.0 / 6, 1.0 / 24, 1.0 / 120, 1.0 / 720, 1.0 / 5040, 1.0 / 40320,
+                              1.0 / 362880, 1.0 / 3628800, 1.0 / 39916800};
+    return r * series_step(0.0, r, k);
 }
 
 __device__ __forceinline__ double row_exp(double x)
 {
-    if (!(x > -745.0)) return x != x ? x : 0.0;
-    if (x > 709.7) return INFINITY;
-    const double k = rint(x * (1.0 / kLn2));
+    const double k = rint(fmin(fmax(x, -1100.0), 1100.0) * (1.0 / kLn2));
     const double r = (x - k * kLn2) - k * kLn2Lo;
-    return ldexp(1.0 + row_expm1_small(r), (int)k);
+    const double y = ldexp(1.0 + row_expm1_small(r), (int)k);
+    return x != x ? x : (x < -745.0 ? 0.0 : (x > 709.7 ? (double)INFINITY : y));
 }
 
 __device__ __forceinline__ double row_expm1(double x)
@@ -199,28 +230,25 @@ __device__ __forceinline__ double row_expm1(double x)
 // log(m 2^e) = e log 2 + 2 (s + s^3/3 + s^5/5 + ...), s = (m - 1) / (m + 1), m in [1/sqrt 2, sqrt 2]
 __device__ __forceinline__ double row_log(double x)
 {
-    if (!(x > 0.0) || x == INFINITY) return x == 0.0 ? -(double)INFINITY : x;
+    constexpr double k[9] = {1.0, 1.0 / 3, 1.0 / 5, 1.0 / 7, 1.0 / 9, 1.0 / 11, 1.0 / 13, 1.0 / 15, 1.0 / 17};
     double m = __builtin_amdgcn_frexp_mant(x);
     int e = __builtin_amdgcn_frexp_exp(x);
     if (m < 0.70710678118654752440) {
         m *= 2.0;
         --e;
     }
-    const double s = (m - 1.0) / (m + 1.0), q = s * s;
-    double a = kRowOdd[8];
-#pragma unroll 1
-    for (int n = 7; n >= 0; --n) a = a * q + kRowOdd[n];
-    return e * kLn2 + 2.0 * s * a;
+    const double s = (m - 1.0) / (m + 1.0);
+    const double y = e * kLn2 + 2.0 * s * series_step(0.0, s * s, k);
+    return x > 0.0 && x < INFINITY ? y : (x == 0.0 ? -(double)INFINITY : x);
 }
 
-// log(1 + u) for u in [0, 1]
+// log(1 + u) for u in [0, 1]: s = u / (2 + u) is at most 1/3
 __device__ __forceinline__ double row_log1p(double u)
 {
-    const double s = u / (2.0 + u), q = s * s; // at most 1/3
-    double a = 0.0;
-#pragma unroll 1
-    for (int n = 14; n >= 0; --n) a = a * q + 1.0 / (2 * n + 1);
-    return 2.0 * s * a;
+    constexpr double k[13] = {1.0, 1.0 / 3, 1.0 / 5, 1.0 / 7, 1.0 / 9, 1.0 / 11, 1.0 / 13, 1.0 / 15, 1.0 / 17,
+                              1.0 / 19, 1.0 / 21, 1.0 / 23, 1.0 / 25};
+    const double s = u / (2.0 + u);
+    return 2.0 * s * series_step(0.0, s * s, k);
 }
 
 // 1/S with a row of nothing (S = 0) giving 0; a NaN stays
