@@ -560,6 +560,19 @@ def _stats_result(arr, o, n, P):
 # --------------------------------------------------------------------------
 # losses over a vocabulary
 # --------------------------------------------------------------------------
+# A call on a few rows takes the GPU a few microseconds, so these wrappers
+# keep the host's share small: pointers and the stream go to ctypes as plain
+# integers.
+
+def _raw_stream(t: torch.Tensor) -> int:
+    """The current stream of t's device, which must be the current device
+    (the library launches there)."""
+    index = t.get_device()
+    if index != torch._C._cuda_getDevice():
+        raise ValueError("the tensors are on cuda:%d, the current device is cuda:%d"
+                         % (index, torch._C._cuda_getDevice()))
+    return torch._C._cuda_getCurrentRawStream(index)
+
 
 def _rows(logits: torch.Tensor):
     """(logits, dtype code, T, V, row stride): a 2-D tensor whose rows are
@@ -568,40 +581,39 @@ def _rows(logits: torch.Tensor):
         raise ValueError("logits must be [rows, vocabulary], got %d dimensions" % logits.dim())
     dt = _dtype_code(logits)
     T, V = logits.shape
-    if V > 1 and logits.stride(1) != 1 or T > 1 and logits.stride(0) < V:
+    ld, step = logits.stride()
+    if V > 1 and step != 1 or T > 1 and ld < V:
         logits = logits.contiguous()
-    return logits, dt, T, V, (logits.stride(0) if T > 1 else V)
+        ld = V
+    return logits, dt, T, V, (ld if T > 1 else V)
 
 
-def _same_device(logits, **tensors):
-    """Shape, type and device checks of a call's other tensors: name=(tensor
-    or None, dtype, shape).  Returns them contiguous."""
-    out = []
-    for name, (t, dtype, shape) in tensors.items():
-        if t is not None:
-            if t.dtype != dtype or tuple(t.shape) != shape:
-                raise ValueError("%s must be %s of shape %s, got %s %s" % (name, dtype, list(shape), t.dtype,
-                                                                           list(t.shape)))
-            if t.device != logits.device:
-                raise ValueError("%s is on %s, the logits on %s" % (name, t.device, logits.device))
-            t = t.contiguous()
-        out.append(t)
-    return out
+def _beside(logits, name, t, dtype, shape):
+    """Checks one of a call's other tensors; (tensor, its address)."""
+    if t is None:
+        return None, None
+    if t.dtype != dtype or t.shape != shape:
+        raise ValueError("%s must be %s of shape %s, got %s %s" % (name, dtype, list(shape), t.dtype, list(t.shape)))
+    if t.get_device() != logits.get_device():
+        raise ValueError("%s is on %s, the logits on %s" % (name, t.device, logits.device))
+    t = t.contiguous()
+    return t, t.data_ptr()
 
 
 def _grad_of(logits, want_grad, grad):
-    """The gradient's tensor and row stride: allocated, the caller's, or none."""
+    """The gradient's tensor, address and row stride: allocated, the caller's, or none."""
     if grad is None:
         if not want_grad:
-            return None, 0
+            return None, None, 0
         grad = torch.empty(logits.shape, dtype=logits.dtype, device=logits.device)
-        return grad, grad.shape[1]
+        return grad, grad.data_ptr(), logits.shape[1]
     T, V = logits.shape
-    if grad.dtype != logits.dtype or grad.shape != logits.shape or grad.device != logits.device:
+    if grad.dtype != logits.dtype or grad.shape != logits.shape or grad.get_device() != logits.get_device():
         raise ValueError("grad must have the logits' type, shape and device")
-    if V > 1 and grad.stride(1) != 1 or T > 1 and grad.stride(0) < V:
+    ld, step = grad.stride()
+    if V > 1 and step != 1 or T > 1 and ld < V:
         raise ValueError("grad must have contiguous rows (it is written in place)")
-    return grad, (grad.stride(0) if T > 1 else V)
+    return grad, grad.data_ptr(), (ld if T > 1 else V)
 
 
 def _inv_temp(temperature):
@@ -610,12 +622,14 @@ def _inv_temp(temperature):
     return 1.0 / temperature
 
 
-def _ws_or_none(need, workspace, device):
+def _scratch(need, workspace, device):
+    """(workspace or None, its address, its size) of at least `need` bytes."""
     if need == 0:
-        return None, 0
-    if workspace is None or workspace.numel() < need:
+        return None, None, 0
+    if workspace is None or workspace.numel() * workspace.element_size() < need:
         workspace = torch.empty(need, dtype=torch.uint8, device=device)
-    return workspace, workspace.numel()
+        return workspace, workspace.data_ptr(), need
+    return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
 
 
 def sg_topk_rows(logits: torch.Tensor, k: int, temperature: float = 1.0, workspace: torch.Tensor | None = None):
@@ -623,14 +637,15 @@ def sg_topk_rows(logits: torch.Tensor, k: int, temperature: float = 1.0, workspa
     (idx [T, k] int32 holding uint32 indices, ascending; logp [T, k] float32,
     log-probabilities over the whole row; lse [T] float32)."""
     _need_cuda(logits)
+    L, dev = lib(), logits.device
     logits, dt, T, V, ld = _rows(logits)
-    dev = logits.device
+    stream = _raw_stream(logits)
     idx = torch.empty((T, k), dtype=torch.int32, device=dev)
     logp = torch.empty((T, k), dtype=torch.float32, device=dev)
     lse = torch.empty(T, dtype=torch.float32, device=dev)
-    ws, nws = _ws_or_none(lib().sg_topk_rows_workspace_bytes(T, V, k, dt), workspace, dev)
-    _check(lib().sg_topk_rows(_p(logits), dt, T, V, ld, _inv_temp(temperature), k, _p(idx), _p(logp), _p(lse), _p(ws), nws,
-                              _stream()), "sg_topk_rows")
+    ws, p_ws, n_ws = _scratch(L.sg_topk_rows_workspace_bytes(T, V, k, dt), workspace, dev)
+    _check(L.sg_topk_rows(logits.data_ptr(), dt, T, V, ld, _inv_temp(temperature), k, idx.data_ptr(), logp.data_ptr(),
+                          lse.data_ptr(), p_ws, n_ws, stream), "sg_topk_rows")
     return idx, logp, lse
 
 
@@ -642,15 +657,18 @@ def sg_distill_loss(logits: torch.Tensor, idx: torch.Tensor, logp: torch.Tensor,
     -> (loss [T] float32, weighted; grad [T, V] of loss.sum(), or None).
     grad: where to write the gradient, logits itself included."""
     _need_cuda(logits, idx, logp, weight, grad)
-    grad, ldg = _grad_of(logits, want_grad, grad)
+    L, dev, f = lib(), logits.device, torch.float32
+    grad, p_grad, ldg = _grad_of(logits, want_grad, grad)
     logits, dt, T, V, ld = _rows(logits)
+    stream = _raw_stream(logits)
     k = idx.shape[-1]
-    idx, logp, weight = _same_device(logits, idx=(idx, torch.int32, (T, k)), logp=(logp, torch.float32, (T, k)),
-                                     weight=(weight, torch.float32, (T,)))
-    loss = torch.empty(T, dtype=torch.float32, device=logits.device)
-    ws, nws = _ws_or_none(lib().sg_distill_workspace_bytes(T, V, k, dt), workspace, logits.device)
-    _check(lib().sg_distill_loss(_p(logits), dt, T, V, ld, _inv_temp(temperature), _p(idx), _p(logp), k, mode, _p(weight),
-                                 _p(loss), _p(grad), ldg, _p(ws), nws, _stream()), "sg_distill_loss")
+    idx, p_idx = _beside(logits, "idx", idx, torch.int32, (T, k))
+    logp, p_logp = _beside(logits, "logp", logp, f, (T, k))
+    weight, p_weight = _beside(logits, "weight", weight, f, (T,))
+    loss = torch.empty(T, dtype=f, device=dev)
+    ws, p_ws, n_ws = _scratch(L.sg_distill_workspace_bytes(T, V, k, dt), workspace, dev)
+    _check(L.sg_distill_loss(logits.data_ptr(), dt, T, V, ld, _inv_temp(temperature), p_idx, p_logp, k, mode, p_weight,
+                             loss.data_ptr(), p_grad, ldg, p_ws, n_ws, stream), "sg_distill_loss")
     return loss, grad
 
 
@@ -662,18 +680,22 @@ def sg_policy_loss(logits: torch.Tensor, action: torch.Tensor, old_logp=None, ad
     weighted; logp [T] float32 of the actions; grad [T, V] of loss.sum(), or
     None).  grad: where to write the gradient, logits itself included."""
     _need_cuda(logits, action, old_logp, adv, ref_logp, weight, grad)
-    grad, ldg = _grad_of(logits, want_grad, grad)
+    L, dev, f = lib(), logits.device, torch.float32
+    grad, p_grad, ldg = _grad_of(logits, want_grad, grad)
     logits, dt, T, V, ld = _rows(logits)
-    f = torch.float32
-    action, old_logp, adv, ref_logp, weight = _same_device(
-        logits, action=(action, torch.int32, (T,)), old_logp=(old_logp, f, (T,)), adv=(adv, f, (T,)),
-        ref_logp=(ref_logp, f, (T,)), weight=(weight, f, (T,)))
-    loss = torch.empty(T, dtype=f, device=logits.device)
-    logp = torch.empty(T, dtype=f, device=logits.device)
-    ws, nws = _ws_or_none(lib().sg_policy_workspace_bytes(T, V, dt), workspace, logits.device)
-    _check(lib().sg_policy_loss(_p(logits), dt, T, V, ld, _inv_temp(temperature), _p(action), _p(old_logp), _p(ref_logp),
-                                _p(adv), _p(weight), clip_low, clip_high, kl_coef, _p(loss), _p(logp), _p(grad), ldg,
-                                _p(ws), nws, _stream()), "sg_policy_loss")
+    stream = _raw_stream(logits)
+    row = (T,)
+    action, p_action = _beside(logits, "action", action, torch.int32, row)
+    old_logp, p_old = _beside(logits, "old_logp", old_logp, f, row)
+    adv, p_adv = _beside(logits, "adv", adv, f, row)
+    ref_logp, p_ref = _beside(logits, "ref_logp", ref_logp, f, row)
+    weight, p_weight = _beside(logits, "weight", weight, f, row)
+    loss = torch.empty(T, dtype=f, device=dev)
+    logp = torch.empty(T, dtype=f, device=dev)
+    ws, p_ws, n_ws = _scratch(L.sg_policy_workspace_bytes(T, V, dt), workspace, dev)
+    _check(L.sg_policy_loss(logits.data_ptr(), dt, T, V, ld, _inv_temp(temperature), p_action, p_old, p_ref, p_adv,
+                            p_weight, clip_low, clip_high, kl_coef, loss.data_ptr(), logp.data_ptr(), p_grad, ldg,
+                            p_ws, n_ws, stream), "sg_policy_loss")
     return loss, logp, grad
 
 
@@ -689,22 +711,23 @@ def sg_preference_loss(logits: torch.Tensor, label: torch.Tensor, seq_off: torch
     SG_PREF_SIGMOID.  grad: where to write the gradient, logits itself
     included."""
     _need_cuda(logits, label, seq_off, ref_logp, weight, grad)
-    grad, ldg = _grad_of(logits, want_grad, grad)
+    L, dev, f = lib(), logits.device, torch.float32
+    grad, p_grad, ldg = _grad_of(logits, want_grad, grad)
     logits, dt, T, V, ld = _rows(logits)
-    if seq_off.numel() % 2 != 1:
-        raise ValueError("seq_off must hold 2 * pairs + 1 offsets, got %d" % seq_off.numel())
-    B = seq_off.numel() // 2
-    f = torch.float32
-    label, seq_off, ref_logp, weight = _same_device(
-        logits, label=(label, torch.int32, (T,)), seq_off=(seq_off, torch.int64, (2 * B + 1,)),
-        ref_logp=(ref_logp, f, (2 * B,)), weight=(weight, f, (B,)))
-    loss = torch.empty(B, dtype=f, device=logits.device)
-    seq_logp = torch.empty(2 * B, dtype=f, device=logits.device)
-    ws, nws = _ws_or_none(lib().sg_preference_workspace_bytes(T, V, dt), workspace, logits.device)
-    _check(lib().sg_preference_loss(_p(logits), dt, T, V, ld, _p(label), _p(seq_off), B, _p(ref_logp), _p(weight),
-                                    kind, beta, smoothing if kind == SG_PREF_SIGMOID else 0.0, 1 if average else 0,
-                                    _p(loss), _p(seq_logp), _p(grad), ldg, _p(ws), nws, _stream()),
-           "sg_preference_loss")
+    stream = _raw_stream(logits)
+    if seq_off.dim() != 1 or seq_off.shape[0] % 2 != 1:
+        raise ValueError("seq_off must hold 2 * pairs + 1 offsets, got %s" % list(seq_off.shape))
+    B = seq_off.shape[0] // 2
+    label, p_label = _beside(logits, "label", label, torch.int32, (T,))
+    seq_off, p_off = _beside(logits, "seq_off", seq_off, torch.int64, (2 * B + 1,))
+    ref_logp, p_ref = _beside(logits, "ref_logp", ref_logp, f, (2 * B,))
+    weight, p_weight = _beside(logits, "weight", weight, f, (B,))
+    loss = torch.empty(B, dtype=f, device=dev)
+    seq_logp = torch.empty(2 * B, dtype=f, device=dev)
+    ws, p_ws, n_ws = _scratch(L.sg_preference_workspace_bytes(T, V, dt), workspace, dev)
+    _check(L.sg_preference_loss(logits.data_ptr(), dt, T, V, ld, p_label, p_off, B, p_ref, p_weight, kind, beta,
+                                smoothing if kind == SG_PREF_SIGMOID else 0.0, 1 if average else 0, loss.data_ptr(),
+                                seq_logp.data_ptr(), p_grad, ldg, p_ws, n_ws, stream), "sg_preference_loss")
     return loss, seq_logp, grad
 
 

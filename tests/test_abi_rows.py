@@ -134,9 +134,9 @@ def test_binding_refuses():
     with pytest.raises(TypeError):
         sg._rows(torch.zeros(4, 5, dtype=torch.float16))
     with pytest.raises(ValueError):
-        sg._same_device(x, weight=(torch.zeros(5), torch.float32, (4,)))
+        sg._beside(x, "weight", torch.zeros(5), torch.float32, (4,))
     with pytest.raises(ValueError):
-        sg._same_device(x, weight=(torch.zeros(4, dtype=torch.float64), torch.float32, (4,)))
+        sg._beside(x, "weight", torch.zeros(4, dtype=torch.float64), torch.float32, (4,))
     with pytest.raises(ValueError):
         sg._grad_of(x, True, torch.zeros(4, 16, dtype=torch.bfloat16))
     with pytest.raises(ValueError):
