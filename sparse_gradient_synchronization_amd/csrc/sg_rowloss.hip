@@ -244,14 +244,6 @@ struct DistillOp {
 // ---------------------------------------------------------------------------
 // one block per row
 // ---------------------------------------------------------------------------
-// address of chunk j + j0: j is the same for all lanes, so it goes into a
-// scalar base and one 32-bit lane offset serves every chunk of the row
-template <typename E, typename P>
-__device__ __forceinline__ P* chunk_at(P* x, uint32_t j, uint32_t j0)
-{
-    return x + (uint64_t)j * RowIO<E>::VEC + j0 * RowIO<E>::VEC;
-}
-
 template <typename E>
 __device__ __forceinline__ void zero_row(E* g, uint32_t V, uint32_t t, uint32_t nt)
 {
@@ -298,15 +290,6 @@ __device__ __forceinline__ void grad_row(const E* x, E* g, uint32_t V, RowCoef k
     for (uint32_t j = t; j < sp.nc; j += nt)
         grad_chunk<E>(load_chunk(chunk_at<E>(x + sp.head, j, 0)), chunk_at<E>(g + sp.head, j, 0), k, c);
     grad_loose(x, g, sp, k, c, t, nt);
-}
-
-// chunks j0, j0 + NT, ... of a row
-template <int J, int NT, typename E>
-__device__ __forceinline__ void load_chunks(u32x4* w, const E* x, uint32_t j0, uint32_t nc)
-{
-#pragma unroll
-    for (int j = 0; j < J; ++j)
-        if (j0 + j * NT < nc) w[j] = load_chunk(chunk_at<E>(x, j * NT, j0));
 }
 
 template <typename E, int J, int NT, class Op>

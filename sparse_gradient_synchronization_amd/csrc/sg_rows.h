@@ -140,6 +140,23 @@ __device__ __forceinline__ void store_chunk(E* p, u32x4 v)
     __builtin_memcpy(p, &v, 16);
 }
 
+// address of chunk j + j0: j is the same for all lanes, so it goes into a
+// scalar base and one 32-bit lane offset serves every chunk of the row
+template <typename E, typename P>
+__device__ __forceinline__ P* chunk_at(P* x, uint32_t j, uint32_t j0)
+{
+    return x + (uint64_t)j * RowIO<E>::VEC + j0 * RowIO<E>::VEC;
+}
+
+// chunks j0, j0 + NT, ... of a row
+template <int J, int NT, typename E>
+__device__ __forceinline__ void load_chunks(u32x4* w, const E* x, uint32_t j0, uint32_t nc)
+{
+#pragma unroll
+    for (int j = 0; j < J; ++j)
+        if (j0 + j * NT < nc) w[j] = load_chunk(chunk_at<E>(x, j * NT, j0));
+}
+
 __device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
 
 // the maximum as it is subtracted: a row (or part) of nothing but -inf has
