@@ -570,7 +570,8 @@ typedef enum sg_distill_mode {
  *   RENORM  the same with p / P (a list of no mass: L = 0)
  *   TAIL    PLAIN + R (log R - log(1 - Q)), R = max(0, 1 - P); 1 - Q is summed
  *           over the unlisted tokens, not subtracted; where they hold nothing
- *           (the list covers every finite logit) the bucket is left out, R = 0
+ *           (all masked, or a share of the row below 1e-300) the bucket is
+ *           left out, R = 0
  * d loss / d logit_i = weight * inv_temp * (W q_i - p_i), W = P + R (RENORM: 1),
  * and for an unlisted token weight * inv_temp * q_i (W - R / (1 - Q)).
  *   d_idx  [T][k] u32, in any order, no token twice in a row (a kernel that
@@ -578,7 +579,8 @@ typedef enum sg_distill_mode {
  *          unspecified).  An index >= V is padding and carries no mass.
  *   d_logp [T][k] fp32, the teacher's log-probabilities at the same temperature
  *   d_loss [T] fp32 out
- * Limits: 1 <= k (else SG_EINVAL), k <= SG_ROWS_MAX_K (else SG_EUNSUPPORTED). */
+ * Limits: 1 <= k (else SG_EINVAL), k <= SG_ROWS_MAX_K and V <= 2^24 (else
+ * SG_EUNSUPPORTED). */
 size_t sg_distill_workspace_bytes(uint64_t T, uint64_t V, uint32_t k, sg_dtype dt);
 int sg_distill_loss(const void* d_logits, sg_dtype dt, uint64_t T, uint64_t V, uint64_t ld, double inv_temp,
                     const uint32_t* d_idx, const float* d_logp, uint32_t k, sg_distill_mode mode,

@@ -16,13 +16,29 @@
 
 namespace sg {
 
-constexpr int RL_NT = 256;
 constexpr uint32_t RL_MAX_K = SG_ROWS_MAX_K;
+constexpr uint32_t RL_MAX_PARTS = 64;
 
-// the dense part of a row's gradient: coef * exp2(c * (x_i - m))
+// A row's gradient: coef * exp2(c * (x_i - m)) for the tokens it does not
+// name; a and b are what the operator needs for those it names.
 struct RowCoef {
-    float m, coef;
+    float m, coef, a, b;
 };
+
+// What an operator with a list keeps of it in LDS.
+struct RowList {
+    float z[RL_MAX_K], p[RL_MAX_K]; // logits, masses
+    uint32_t id[RL_MAX_K];
+    uint32_t flag[1024]; // bit r of flag[t]: the chunk that data thread t takes in round r has listed tokens
+};
+struct NoList {};
+
+// An operator says which rows it reads (live, skip), what it needs of the
+// named logits (Named, gathered before a gradient may overwrite them), how
+// the row's sum becomes loss and gradient (finish, by a wave), and the
+// gradient of the named tokens in [lo, hi) of the row (named_grad, put_named;
+// g is element lo).  kListed: tokens are listed, and left out of the
+// streaming pass's sum; a wave of its own handles the list.
 
 // ---------------------------------------------------------------------------
 // the clipped policy loss
@@ -35,9 +51,8 @@ struct PolicyOp {
     uint32_t V;
 
     static constexpr bool kListed = false, kGrad = true;
-    struct Shared {
-        float za, fix;
-    };
+    typedef float Named; // the action's logit
+    typedef NoList List;
 
     __device__ __forceinline__ bool live(uint64_t row) const
     {
@@ -48,16 +63,15 @@ struct PolicyOp {
         loss[row] = 0.f;
         if (logp) logp[row] = 0.f;
     }
-    template <typename E, int NT>
-    __device__ __forceinline__ void begin(const Rows&, uint64_t row, const E* x, uint32_t, Shared& sh, uint32_t*) const
+    template <typename E>
+    __device__ __forceinline__ Named named(const Rows&, uint64_t row, const E* x, NoList&) const
     {
-        if (threadIdx.x == 0) sh.za = RowIO<E>::get(x + action[row]);
+        return RowIO<E>::get(x + action[row]);
     }
-    // lane 0 of wave 0
-    __device__ __forceinline__ RowCoef finish(const Rows& r, uint64_t row, RowStat st, Shared& sh) const
+    __device__ __forceinline__ RowCoef finish(const Rows& r, uint64_t row, RowStat st, Named za, bool write) const
     {
         const double S = st.s;
-        const double lp = sh.za == -INFINITY ? -(double)INFINITY : ((double)sh.za - st.m) * r.it - row_log(S);
+        const double lp = za == -INFINITY ? -(double)INFINITY : ((double)za - st.m) * r.it - row_log(S);
         const double w = weight ? (double)weight[row] : 1.0;
         const double A = adv ? (double)adv[row] : 0.0;
         const double ratio = old_logp ? row_exp(lp - (double)old_logp[row]) : 1.0;
@@ -72,18 +86,22 @@ struct PolicyOp {
             L += kl * (e - d);
             slope -= kl * e;
         }
-        loss[row] = (float)(w * L);
-        if (logp) logp[row] = (float)lp;
+        if (write && lane_id() == 0) {
+            loss[row] = (float)(w * L);
+            if (logp) logp[row] = (float)lp;
+        }
         const double g = w * slope * r.it;
-        sh.fix = (float)(g * -row_expm1(lp)); // 1 - q of the token, without the cancellation
-        return {st.m, (float)(-g * inverse_of(S))};
+        // at the action 1 - q without the cancellation
+        return {st.m, (float)(-g * inverse_of(S)), (float)(g * -row_expm1(lp)), 0.f};
     }
-    template <typename E, int NT>
-    __device__ __forceinline__ void fix(const Rows& r, uint64_t row, E* g, const Shared& sh, RowCoef) const
+    __device__ __forceinline__ void named_grad(const Rows&, const RowCoef&, NoList&) const {}
+    template <typename E>
+    __device__ __forceinline__ void put_named(uint64_t row, E* g, const RowCoef& k, const NoList&, uint32_t lo_,
+                                              uint32_t hi_) const
     {
-        if (threadIdx.x == 0) RowIO<E>::put(g + action[row], sh.fix);
+        const uint32_t i = (uint32_t)action[row];
+        if (lane_id() == 0 && i >= lo_ && i < hi_) RowIO<E>::put(g + (i - lo_), k.a);
     }
-    __device__ __forceinline__ uint32_t bits(const uint32_t*, uint32_t, int) const { return 0; }
 };
 
 // ---------------------------------------------------------------------------
@@ -98,29 +116,30 @@ struct TokenOp {
     uint32_t V;
 
     static constexpr bool kListed = false, kGrad = false;
-    struct Shared {
-        float za;
-    };
+    typedef float Named;
+    typedef NoList List;
+
     __device__ __forceinline__ bool live(uint64_t row) const { return (uint32_t)label[row] < V; }
     __device__ __forceinline__ void skip(uint64_t row) const
     {
         logp[row] = 0.0;
         slope[row] = 0.f;
     }
-    template <typename E, int NT>
-    __device__ __forceinline__ void begin(const Rows&, uint64_t row, const E* x, uint32_t, Shared& sh, uint32_t*) const
+    template <typename E>
+    __device__ __forceinline__ Named named(const Rows&, uint64_t row, const E* x, NoList&) const
     {
-        if (threadIdx.x == 0) sh.za = RowIO<E>::get(x + label[row]);
+        return RowIO<E>::get(x + label[row]);
     }
-    __device__ __forceinline__ RowCoef finish(const Rows& r, uint64_t row, RowStat st, Shared& sh) const
+    __device__ __forceinline__ RowCoef finish(const Rows& r, uint64_t row, RowStat st, Named za, bool write) const
     {
-        logp[row] = sh.za == -INFINITY ? -(double)INFINITY : ((double)sh.za - st.m) * r.it - row_log((double)st.s);
-        m[row] = st.m;
-        inv[row] = (float)inverse_of(st.s);
-        slope[row] = 0.f;
-        return {st.m, 0.f};
+        if (write && lane_id() == 0) {
+            logp[row] = za == -INFINITY ? -(double)INFINITY : ((double)za - st.m) * r.it - row_log((double)st.s);
+            m[row] = st.m;
+            inv[row] = (float)inverse_of(st.s);
+            slope[row] = 0.f;
+        }
+        return {};
     }
-    __device__ __forceinline__ uint32_t bits(const uint32_t*, uint32_t, int) const { return 0; }
 };
 
 // ---------------------------------------------------------------------------
@@ -139,110 +158,131 @@ struct DistillOp {
     int mode;
 
     static constexpr bool kListed = true, kGrad = true;
-    struct Shared {
-        float z[RL_MAX_K]; // the listed logits, read before the gradient may overwrite them
-        double P, A, S;    // mass, sum p (log p - (z - m)), sum exp(z - m), z scaled by inv_temp
-        float m;
-        double gp;           // scale of p in the gradient
-        float within;        // the listed tokens' factor of exp2(c (x - m))
+    typedef RowList List;
+    struct Named {
+        double P, A, S; // mass, sum p (log p - (z - m)), sum exp(z - m), z scaled by inv_temp
+        float m;        // maximum of the listed logits
     };
+
     __device__ __forceinline__ bool live(uint64_t row) const { return !weight || weight[row] != 0.f; }
     __device__ __forceinline__ void skip(uint64_t row) const { loss[row] = 0.f; }
-    template <typename E, int NT>
-    __device__ __forceinline__ void begin(const Rows& r, uint64_t row, const E* x, uint32_t pad, Shared& sh,
-                                          uint32_t* bm) const
+    // The list's wave, in four steps.  fetch: its first 64 tokens, asked for
+    // before anything else, since the row's loads would hold them up.
+    __device__ __forceinline__ uint32_t fetch(uint64_t row) const
     {
-        const uint32_t* id = idx + row * k;
-        const float* lp = logp + row * k;
-        for (uint32_t i = threadIdx.x; i < (V + pad + 31) / 32; i += NT) bm[i] = 0;
-        __syncthreads();
-        for (uint32_t j = threadIdx.x; j < k; j += NT) {
-            const uint32_t i = id[j];
-            if (i >= V) continue;
-            const uint32_t at = i + pad, was = atomicOr(&bm[at / 32], 1u << (at % 32));
+        return lane_id() < k ? idx[row * k + lane_id()] : V;
+    }
+    // mark: the tokens of [lo, hi) in the bitmap, and their chunks in the flags
+    template <typename E, int ND>
+    __device__ __forceinline__ void mark(uint64_t row, uint32_t i, uint32_t lo, uint32_t hi, const RowSpan& sp,
+                                         RowList& ls, uint32_t* bm) const
+    {
+        constexpr uint32_t VEC = RowIO<E>::VEC;
+        for (uint32_t j = lane_id(); j < k; j += SG_WAVE) {
+            if (j >= SG_WAVE) i = idx[row * k + j];
+            ls.id[j] = i;
+            if (i < lo || i >= hi) continue;
+            const uint32_t at = i - lo + VEC - sp.head, was = atomicOr(&bm[at / 32], 1u << (at % 32));
             if (was >> (at % 32) & 1u) report_error(kDevErrUnsorted); // listed twice
-            sh.z[j] = RowIO<E>::get(x + i);
-        }
-        __syncthreads();
-        if (threadIdx.x < SG_WAVE) {
-            float m = -INFINITY;
-            for (uint32_t j = threadIdx.x; j < k; j += SG_WAVE)
-                if (id[j] < V) m = fmaxf(m, sh.z[j]);
-            for (int d = 1; d < SG_WAVE; d <<= 1) m = fmaxf(m, __shfl_xor(m, d, SG_WAVE));
-            const double shift = shift_of(m);
-            double P = 0.0, A = 0.0, S = 0.0;
-            for (uint32_t j = threadIdx.x; j < k; j += SG_WAVE) {
-                if (id[j] >= V) continue;
-                const double t = lp[j], z = sh.z[j], p = row_exp(t);
-                P += p;
-                if (p != 0.0) A += p * (t - (z - shift) * r.it);
-                S += row_exp((z - shift) * r.it);
-            }
-            P = wave_sum_f64(P);
-            A = wave_sum_f64(A);
-            S = wave_sum_f64(S);
-            if (threadIdx.x == 0) {
-                sh.P = P;
-                sh.A = A;
-                sh.S = S;
-                sh.m = m;
+            if (at >= VEC) {
+                const uint32_t c = at / VEC - 1, round = c / ND;
+                if (c < sp.nc && round < 32) atomicOr(&ls.flag[c % ND], 1u << round);
             }
         }
     }
-    __device__ __forceinline__ RowCoef finish(const Rows& r, uint64_t row, RowStat st, Shared& sh) const
+    // named: the listed logits and masses, and their sums
+    template <typename E>
+    __device__ __forceinline__ Named named(const Rows& r, uint64_t row, const E* x, RowList& ls) const
     {
-        const float m = fmaxf(st.m, sh.m);
+        const float* lp = logp + row * k;
+        float m = -INFINITY;
+        for (uint32_t j = lane_id(); j < k; j += SG_WAVE) {
+            const uint32_t i = ls.id[j];
+            const float v = i < V ? RowIO<E>::get(x + i) : -INFINITY;
+            ls.z[j] = v;
+            m = fmaxf(m, v);
+        }
+#pragma unroll
+        for (int d = 1; d < SG_WAVE; d <<= 1) m = fmaxf(m, __shfl_xor(m, d, SG_WAVE));
         const double shift = shift_of(m);
-        const double rest = (double)st.s * row_exp(((double)st.m - shift) * r.it);
-        const double own = sh.S * row_exp(((double)sh.m - shift) * r.it);
+        double P = 0.0, A = 0.0, S = 0.0;
+#pragma unroll 1
+        for (uint32_t j = lane_id(); j < k; j += SG_WAVE) {
+            double p = 0.0;
+            if (ls.id[j] < V) {
+                const double t = lp[j], d = (ls.z[j] - shift) * r.it;
+                p = row_exp(t);
+                P += p;
+                if (p != 0.0) A += p * (t - d);
+                S += row_exp(d);
+            }
+            ls.p[j] = (float)p;
+        }
+        return {wave_sum_f64(P), wave_sum_f64(A), wave_sum_f64(S), m};
+    }
+    // finish: by the whole wave, so that the functions of several numbers run
+    // side by side in its lanes
+    __device__ __forceinline__ RowCoef finish(const Rows& r, uint64_t row, RowStat st, const Named& nm, bool write) const
+    {
+        const uint32_t l = lane_id();
+        const float m = fmaxf(st.m, nm.m);
+        const double shift = shift_of(m);
+        const double scale = row_exp(((l ? (double)nm.m : (double)st.m) - shift) * r.it);
+        const double rest = st.s * __shfl(scale, 0), own = nm.S * __shfl(scale, 1);
         const double S = rest + own;
+        const double R0 = nm.P < 1.0 ? 1.0 - nm.P : 0.0, per_rest = 1.0 / rest, per_S = inverse_of(S);
+        const double lg = row_log(l == 0 ? S : (l == 1 ? R0 * S * per_rest : nm.P));
         // lse less the listed maximum (a row may lie at the type's lowest
         // value, where lse itself holds no digit of log S); of a row of
         // nothing but -inf, A decides
-        const double lse = m == -INFINITY ? 0.0 : (shift - shift_of(sh.m)) * r.it + row_log(S);
+        const double lse = m == -INFINITY ? 0.0 : (shift - shift_of(nm.m)) * r.it + __shfl(lg, 0);
+        const double log_tail = __shfl(lg, 1), log_mass = __shfl(lg, 2);
         const double w = weight ? (double)weight[row] : 1.0;
-        double P = sh.P, A = sh.A, R = 0.0, gp = 1.0, L;
+        double P = nm.P, R = 0.0, gp = 1.0, L;
         if (mode == SG_DISTILL_RENORM) {
             gp = P > 0.0 ? 1.0 / P : P; // nothing listed: no mass, no loss (a NaN stays)
-            L = P > 0.0 ? A * gp - row_log(P) + lse : P;
+            L = P > 0.0 ? nm.A * gp - log_mass + lse : P;
             P = P > 0.0 ? 1.0 : P;
         } else {
-            L = A + P * lse;
+            L = nm.A + P * lse;
             // what is left for the unlisted tokens, where there are any
-            if (mode == SG_DISTILL_TAIL && P < 1.0 && rest != 0.0) {
-                R = 1.0 - P;
-                L += R * (row_log(R) + row_log(S / rest));
+            if (mode == SG_DISTILL_TAIL && R0 > 0.0 && rest > 1e-300) {
+                R = R0;
+                L += R * log_tail;
             }
         }
-        loss[row] = (float)(w * L);
+        if (write && l == 0) loss[row] = (float)(w * L);
         const double g = w * r.it;
-        const double all = (P + R) * inverse_of(S);
-        sh.gp = g * gp;
-        sh.within = (float)(g * all);
-        return {m, (float)(g * (R != 0.0 ? all - R / rest : all))};
+        const double all = (P + R) * per_S;
+        return {m, (float)(g * (R != 0.0 ? all - R * per_rest : all)), (float)(g * all), (float)(g * gp)};
     }
-    template <typename E, int NT>
-    __device__ __forceinline__ void fix(const Rows& r, uint64_t row, E* g, const Shared& sh, RowCoef co) const
+    // ls.z[j] becomes the gradient of listed token j
+    __device__ __forceinline__ void named_grad(const Rows& r, const RowCoef& co, RowList& ls) const
     {
-        const uint32_t* id = idx + row * k;
-        const float* lp = logp + row * k;
-        for (uint32_t j = threadIdx.x; j < k; j += NT) {
-            const uint32_t i = id[j];
-            if (i >= V) continue;
-            const float e = exp2_fast((sh.z[j] - shift_of(co.m)) * r.c);
-            RowIO<E>::put(g + i, (float)((double)sh.within * e - sh.gp * row_exp((double)lp[j])));
+        for (uint32_t j = lane_id(); j < k; j += SG_WAVE)
+            ls.z[j] = co.a * exp2_fast((ls.z[j] - shift_of(co.m)) * r.c) - co.b * ls.p[j];
+    }
+    template <typename E>
+    __device__ __forceinline__ void put_named(uint64_t, E* g, const RowCoef&, const RowList& ls, uint32_t lo,
+                                              uint32_t hi) const
+    {
+        for (uint32_t j = lane_id(); j < k; j += SG_WAVE) {
+            const uint32_t i = ls.id[j];
+            if (i >= lo && i < hi) RowIO<E>::put(g + (i - lo), ls.z[j]);
         }
-    }
-    // bit v of the result: element i0 + v - pad is listed (i0 a multiple of n = 4 or 8, or n = 1); pad is
-    // what makes the first element of a chunk a multiple of the chunk's size
-    __device__ __forceinline__ uint32_t bits(const uint32_t* bm, uint32_t i0, int n) const
-    {
-        return bm[i0 / 32] >> (i0 % 32) & ((1u << n) - 1u);
     }
 };
 
+// n (4, 8 or 1) bits of the bitmap from bit i0, a multiple of n: an element's
+// bit is its place plus what makes the first element of a chunk a multiple of
+// the chunk's size
+__device__ __forceinline__ uint32_t marked(const uint32_t* bm, uint32_t i0, int n)
+{
+    return bm[i0 / 32] >> (i0 % 32) & ((1u << n) - 1u);
+}
+
 // ---------------------------------------------------------------------------
-// one block per row
+// the passes over (a part of) a row
 // ---------------------------------------------------------------------------
 template <typename E>
 __device__ __forceinline__ void zero_row(E* g, uint32_t V, uint32_t t, uint32_t nt)
@@ -256,55 +296,59 @@ __device__ __forceinline__ void zero_row(E* g, uint32_t V, uint32_t t, uint32_t 
 }
 
 template <typename E>
-__device__ __forceinline__ void grad_chunk(u32x4 w, E* g, RowCoef k, float c)
+__device__ __forceinline__ void grad_chunk(u32x4 w, E* g, float coef, float sh, float c)
 {
     constexpr int VEC = RowIO<E>::VEC;
-    const float sh = shift_of(k.m);
     float v[VEC];
     RowIO<E>::unpack(w, v);
 #pragma unroll
-    for (int i = 0; i < VEC; ++i) v[i] = k.coef * exp2_fast((v[i] - sh) * c);
+    for (int i = 0; i < VEC; ++i) v[i] = coef * exp2_fast((v[i] - sh) * c);
     store_chunk(g, RowIO<E>::pack(v));
 }
 
 // the elements outside the chunks
 template <typename E>
-__device__ __forceinline__ void grad_loose(const E* x, E* g, const RowSpan& sp, RowCoef k, float c, uint32_t t,
-                                           uint32_t nt)
+__device__ __forceinline__ void grad_loose(const E* x, E* g, const RowSpan& sp, float coef, float sh, float c,
+                                           uint32_t t)
 {
     constexpr int VEC = RowIO<E>::VEC;
-    const float sh = shift_of(k.m);
-#pragma unroll 1
-    for (uint32_t i = loose_element(sp, VEC, t); i < sp.V; i = loose_element(sp, VEC, t += nt))
-        RowIO<E>::put(g + i, k.coef * exp2_fast((RowIO<E>::get(x + i) - sh) * c));
+    if (t < 2 * VEC) {
+        const uint32_t i = loose_element(sp, VEC, t);
+        if (i < sp.V) RowIO<E>::put(g + i, coef * exp2_fast((RowIO<E>::get(x + i) - sh) * c));
+    }
 }
 
-// gradient of a row: coef * exp2(c (x - m)).  x and g may be the same row:
-// every thread reads an element before it writes it, and nobody else touches
-// it.
+// gradient of V elements: coef * exp2(c (x - m)).  x and g may be the same
+// memory: every thread reads an element before it writes it, and nobody else
+// touches it.
 template <typename E>
-__device__ __forceinline__ void grad_row(const E* x, E* g, uint32_t V, RowCoef k, float c, uint32_t t, uint32_t nt)
+__device__ __forceinline__ void grad_row(const E* x, E* g, uint32_t V, float coef, float m, float c, uint32_t t,
+                                         uint32_t nt)
 {
     const RowSpan sp = span_of(x, V);
+    const float sh = shift_of(m);
 #pragma unroll 2
     for (uint32_t j = t; j < sp.nc; j += nt)
-        grad_chunk<E>(load_chunk(chunk_at<E>(x + sp.head, j, 0)), chunk_at<E>(g + sp.head, j, 0), k, c);
-    grad_loose(x, g, sp, k, c, t, nt);
+        grad_chunk<E>(load_chunk(chunk_at<E>(x + sp.head, j, 0)), chunk_at<E>(g + sp.head, j, 0), coef, sh, c);
+    grad_loose(x, g, sp, coef, sh, c, t);
 }
 
-template <typename E, int J, int NT, class Op>
-__device__ __forceinline__ void stat_chunks(RowStat& st, const u32x4* w, const Op& op, const uint32_t* bm, uint32_t j0,
-                                            uint32_t nc, float c)
+// Chunks j0, j0 + ND, ... whose loads are in w.  LISTED: marked elements are
+// left out; bit j of `flags` says whether chunk j0 + j * ND has any.  Bits
+// that are looked up in the bitmap chunk by chunk cost an LDS round trip each
+// (60 us of 730 for 6000 x 131072 bf16).
+template <typename E, int J, int ND, bool LISTED>
+__device__ __forceinline__ void stat_chunks(RowStat& st, const u32x4* w, uint32_t flags, const uint32_t* bm,
+                                            uint32_t j0, uint32_t nc, float c)
 {
     constexpr int VEC = RowIO<E>::VEC;
 #pragma unroll
     for (int j = 0; j < J; ++j) {
-        if (j0 + j * NT < nc) {
+        if (j0 + j * ND < nc) {
             float v[VEC];
             u32x4 u = w[j];
-            if (Op::kListed) {
-                const uint32_t b = op.bits(bm, (j0 + j * NT + 1) * VEC, VEC);
-                if (b) u = RowIO<E>::without(u, b);
+            if (LISTED) {
+                if (flags >> j & 1u) u = RowIO<E>::without(u, marked(bm, (j0 + j * ND + 1) * VEC, VEC));
                 asm volatile("" : "+v"(u)); // one unpacked form of the chunk, not one for each side of the branch
             }
             RowIO<E>::unpack(u, v);
@@ -314,25 +358,71 @@ __device__ __forceinline__ void stat_chunks(RowStat& st, const u32x4* w, const O
     }
 }
 
-// One block per row (no loop over rows: the constants of the fp64 functions
-// would be hoisted out of it into registers that the row needs).  With GRAD
-// the first NT * J chunks of the row stay in registers from the sums to the
-// gradient, so the row is read from HBM once; what is beyond them is read
-// again (from the last-level cache, the blocks in flight hold few rows).
-// Without GRAD nothing is kept and J is the number of loads a thread has in
-// flight.
-template <typename E, int NT, int J, class Op, bool GRAD>
-__global__ __launch_bounds__(NT, GRAD ? 4 : 8) void row_loss_kernel(Rows r, Op op, void* grad, uint64_t ldg)
+// the chunks from round `first` on (thread t takes chunk t + round * ND), M loads in flight
+template <typename E, int M, int ND, bool LISTED>
+__device__ __forceinline__ void stat_more(RowStat& st, const E* xc, uint32_t flags, const uint32_t* bm, uint32_t t,
+                                          uint32_t first, uint32_t nc, float c)
 {
-    constexpr int VEC = RowIO<E>::VEC, NW = NT / SG_WAVE;
+    uint32_t round = first;
+    u32x4 more[M];
+#pragma unroll 1
+    for (; (round + M) * ND <= nc; round += M) { // the whole block has chunks in these rounds
+#pragma unroll
+        for (int j = 0; j < M; ++j) more[j] = load_chunk(chunk_at<E>(xc, (round + j) * ND, t));
+        stat_chunks<E, M, ND, LISTED>(st, more, round + M <= 32 ? flags >> round : ~0u, bm, t + round * ND, nc, c);
+    }
+#pragma unroll 1
+    for (; t + round * ND < nc; ++round) {
+        more[0] = load_chunk(chunk_at<E>(xc, round * ND, t));
+        stat_chunks<E, 1, ND, LISTED>(st, more, round < 32 ? flags >> round : ~0u, bm, t + round * ND, nc, c);
+    }
+}
+
+template <typename E, bool LISTED>
+__device__ __forceinline__ void stat_loose(RowStat& st, const E* x, const RowSpan& sp, const uint32_t* bm, uint32_t t,
+                                           float c)
+{
+    constexpr int VEC = RowIO<E>::VEC;
+    if (t < 2 * VEC) {
+        const uint32_t i = loose_element(sp, VEC, t);
+        if (i < sp.V) {
+            float v = RowIO<E>::get(x + i);
+            if (LISTED && marked(bm, i + VEC - sp.head, 1)) v = -INFINITY;
+            stat_add<1>(st, &v, c);
+        }
+    }
+}
+
+// ---------------------------------------------------------------------------
+// one block per row
+// ---------------------------------------------------------------------------
+// No loop over rows: the constants of the fp64 functions would be hoisted out
+// of it into registers that the row needs.  With GRAD the first ND * J chunks
+// of the row stay in registers from the sums to the gradient, so the row is
+// read from HBM once; what is beyond them is read again (from the last-level
+// cache, the blocks in flight hold few rows).  Without GRAD nothing is kept
+// and J is the number of loads a thread has in flight.
+//
+// A listed operator's last wave handles the list and no chunks: its gathers
+// and fp64 functions run beside the streaming pass of the others.
+template <typename E, int NT, int J, class Op, bool GRAD, int WAVES>
+__global__ __launch_bounds__(NT, WAVES) void row_loss_kernel(Rows r, Op op, void* grad, uint64_t ldg)
+{
+    constexpr bool LISTED = Op::kListed;
+    constexpr int ND = LISTED ? NT - SG_WAVE : NT, NW = ND / SG_WAVE; // data threads
+    constexpr int VEC = RowIO<E>::VEC;
     extern __shared__ uint32_t rl_bitmap[];
-    __shared__ typename Op::Shared sh;
+    __shared__ typename Op::List ls;
     __shared__ RowStat part[NW];
     __shared__ RowCoef coef;
     const uint32_t t = threadIdx.x;
+    const bool own = LISTED ? t >= ND : t < SG_WAVE; // the wave of the named tokens
     const uint64_t row = r.row0 + blockIdx.x;
     const E* x = static_cast<const E*>(r.x) + row * r.ld;
     E* g = GRAD ? static_cast<E*>(grad) + row * ldg : nullptr;
+    uint32_t first = 0;
+    if constexpr (LISTED)
+        if (own) first = op.fetch(row);
     if (!op.live(row)) { // the same for the whole block
         if (t == 0) op.skip(row);
         if (GRAD) zero_row(g, r.V, t, NT);
@@ -340,49 +430,151 @@ __global__ __launch_bounds__(NT, GRAD ? 4 : 8) void row_loss_kernel(Rows r, Op o
     }
     const RowSpan sp = span_of(x, r.V);
     const E* xc = x + sp.head;
+    constexpr int KEPT = GRAD ? J : 0;
     u32x4 kept[J];
-    load_chunks<J, NT>(kept, xc, t, sp.nc);
-    op.template begin<E, NT>(r, row, x, VEC - sp.head, sh, rl_bitmap);
-    RowStat st = {-INFINITY, 0.f};
-    stat_chunks<E, J, NT>(st, kept, op, rl_bitmap, t, sp.nc, r.c);
-    constexpr int M = GRAD ? 2 : J; // chunks in flight beyond the kept ones
-#pragma unroll 1
-    for (uint32_t j = t + J * NT; j < sp.nc; j += M * NT) {
-        u32x4 more[M];
-        load_chunks<M, NT>(more, xc, j, sp.nc);
-        stat_chunks<E, M, NT>(st, more, op, rl_bitmap, j, sp.nc, r.c);
+    typename Op::Named nm;
+    uint32_t flags = 0;
+    if (!LISTED) nm = op.named(r, row, x, ls); // one address: the same load for all lanes
+    if constexpr (GRAD)
+        if ((!LISTED || t < ND) && sp.nc > 0) load_chunks<J, ND>(kept, xc, t, sp.nc);
+    if constexpr (LISTED) {
+        for (uint32_t i = t; i < (r.V + VEC + 31) / 32; i += NT) rl_bitmap[i] = 0;
+        if (t < ND) ls.flag[t] = 0;
+        __syncthreads();
+        if (own) op.template mark<E, ND>(row, first, 0, r.V, sp, ls, rl_bitmap);
+        __syncthreads();
+        if (own) nm = op.named(r, row, x, ls);
+        else flags = ls.flag[t];
     }
-    if (t < 2 * VEC) {
-        const uint32_t i = loose_element(sp, VEC, t);
-        if (i < r.V) {
-            float v = RowIO<E>::get(x + i);
-            if (Op::kListed && op.bits(rl_bitmap, i + VEC - sp.head, 1)) v = -INFINITY;
-            stat_add<1>(st, &v, r.c);
-        }
+    if (!LISTED || t < ND) {
+        RowStat st = {-INFINITY, 0.f};
+        if constexpr (GRAD) stat_chunks<E, J, ND, LISTED>(st, kept, flags, rl_bitmap, t, sp.nc, r.c);
+        stat_more<E, GRAD ? 2 : J, ND, LISTED>(st, xc, flags, rl_bitmap, t, KEPT, sp.nc, r.c);
+        stat_loose<E, LISTED>(st, x, sp, rl_bitmap, t, r.c);
+        st = wave_stat(st, r.c);
+        if (lane_id() == 0) part[t / SG_WAVE] = st;
     }
-    st = wave_stat(st, r.c);
-    if (lane_id() == 0) part[t / SG_WAVE] = st;
     __syncthreads();
-    if (t < NW) {
-        const RowStat a = wave_stat<NW>(part[t], r.c);
-        if (t == 0) coef = op.finish(r, row, a, sh);
+    if (own) {
+        const uint32_t l = lane_id();
+        const RowStat a = wave_stat(l < NW ? part[l] : RowStat{-INFINITY, 0.f}, r.c);
+        const RowCoef k = op.finish(r, row, a, nm, true);
+        if (l == 0) coef = k;
     }
     if constexpr (GRAD) {
         __syncthreads();
-        const RowCoef k = coef;
-        E* gc = g + sp.head;
+        if (!LISTED || t < ND) {
+            E* gc = g + sp.head;
+            const float cf = coef.coef, sh = shift_of(coef.m);
 #pragma unroll
-        for (int j = 0; j < J; ++j) {
-            asm volatile("" : "+v"(kept[j])); // unpack again rather than keep the unpacked values
-            if (t + j * NT < sp.nc) grad_chunk<E>(kept[j], chunk_at<E>(gc, j * NT, t), k, r.c);
-            __builtin_amdgcn_sched_barrier(0);
-        }
+            for (int j = 0; j < J; ++j) {
+                asm volatile("" : "+v"(kept[j])); // unpack again rather than keep the unpacked values
+                if (t + j * ND < sp.nc) grad_chunk<E>(kept[j], chunk_at<E>(gc, j * ND, t), cf, sh, r.c);
+                __builtin_amdgcn_sched_barrier(0);
+            }
 #pragma unroll 1
-        for (uint32_t j = t + J * NT; j < sp.nc; j += NT)
-            grad_chunk<E>(load_chunk(chunk_at<E>(xc, j, 0)), chunk_at<E>(gc, j, 0), k, r.c);
-        grad_loose(x, g, sp, k, r.c, t, NT);
-        __syncthreads(); // the corrections overwrite elements of other threads
-        op.template fix<E, NT>(r, row, g, sh, k);
+            for (uint32_t j = t + J * ND; j < sp.nc; j += ND)
+                grad_chunk<E>(load_chunk(chunk_at<E>(xc, j, 0)), chunk_at<E>(gc, j, 0), cf, sh, r.c);
+            grad_loose(x, g, sp, cf, sh, r.c, t);
+        }
+        if (own) op.named_grad(r, coef, ls);
+        __syncthreads(); // the named tokens' gradients replace elements that other threads wrote
+        if (own) op.template put_named<E>(row, g, coef, ls, 0, r.V);
+    }
+}
+
+// ---------------------------------------------------------------------------
+// few long rows: several blocks per row, the sums first, then the rest
+// ---------------------------------------------------------------------------
+struct SplitArgs {
+    RowStat* stat; // [rows][parts]
+    uint32_t parts, len; // len elements to a part, a multiple of a chunk
+};
+
+constexpr int SP_NT = 512;
+
+// Sums of one part.  Part 0 also gathers what the operator needs of the named
+// tokens: a gradient in place overwrites them in the next kernel.
+template <typename E, class Op>
+__global__ __launch_bounds__(SP_NT, 4) void row_part_kernel(Rows r, Op op, SplitArgs s, typename Op::Named* keep)
+{
+    constexpr bool LISTED = Op::kListed;
+    constexpr int ND = LISTED ? SP_NT - SG_WAVE : SP_NT, NW = ND / SG_WAVE, VEC = RowIO<E>::VEC;
+    extern __shared__ uint32_t rl_bitmap[];
+    __shared__ typename Op::List ls;
+    __shared__ RowStat part[NW];
+    const uint32_t t = threadIdx.x, lo = blockIdx.x * s.len;
+    const uint64_t row = r.row0 + blockIdx.y;
+    if (!op.live(row)) return;
+    const bool own = LISTED ? t >= ND : t < SG_WAVE;
+    const uint32_t n = r.V - lo < s.len ? r.V - lo : s.len;
+    const E* xr = static_cast<const E*>(r.x) + row * r.ld;
+    const E* x = xr + lo;
+    const RowSpan sp = span_of(x, n);
+    uint32_t flags = 0;
+    if constexpr (LISTED) {
+        const uint32_t first = own ? op.fetch(row) : 0;
+        for (uint32_t i = t; i < (n + VEC + 31) / 32; i += SP_NT) rl_bitmap[i] = 0;
+        if (t < ND) ls.flag[t] = 0;
+        __syncthreads();
+        if (own) op.template mark<E, ND>(row, first, lo, lo + n, sp, ls, rl_bitmap);
+        __syncthreads();
+        if (!own) flags = ls.flag[t];
+    }
+    if (own && blockIdx.x == 0) {
+        const typename Op::Named nm = op.named(r, row, xr, ls);
+        if (lane_id() == 0) keep[row] = nm;
+    }
+    if (t < ND) {
+        RowStat st = {-INFINITY, 0.f};
+        stat_more<E, 4, ND, LISTED>(st, x + sp.head, flags, rl_bitmap, t, 0, sp.nc, r.c);
+        stat_loose<E, LISTED>(st, x, sp, rl_bitmap, t, r.c);
+        st = wave_stat(st, r.c);
+        if (lane_id() == 0) part[t / SG_WAVE] = st;
+    }
+    __syncthreads();
+    if (t < SG_WAVE) {
+        const RowStat a = wave_stat(t < NW ? part[t] : RowStat{-INFINITY, 0.f}, r.c);
+        if (t == 0) s.stat[row * s.parts + blockIdx.x] = a;
+    }
+}
+
+// The row's sums joined (by every block of the row), loss and gradient.
+// Without GRAD one wave a row.
+template <typename E, class Op, bool GRAD>
+__global__ __launch_bounds__(SP_NT, 4) void row_join_kernel(Rows r, Op op, SplitArgs s, const typename Op::Named* keep,
+                                                            void* grad, uint64_t ldg)
+{
+    __shared__ typename Op::List ls;
+    __shared__ RowCoef coef;
+    const uint32_t t = threadIdx.x;
+    const uint64_t row = r.row0 + blockIdx.y;
+    const uint32_t lo = blockIdx.x * s.len, n = r.V - lo < s.len ? r.V - lo : s.len;
+    const E* x = static_cast<const E*>(r.x) + row * r.ld + lo;
+    E* g = GRAD ? static_cast<E*>(grad) + row * ldg + lo : nullptr;
+    if (!op.live(row)) {
+        if (t == 0 && blockIdx.x == 0) op.skip(row);
+        if (GRAD) zero_row(g, n, t, SP_NT);
+        return;
+    }
+    if (t < SG_WAVE) {
+        const RowStat a = wave_stat(t < s.parts ? s.stat[row * s.parts + t] : RowStat{-INFINITY, 0.f}, r.c);
+        const RowCoef k = op.finish(r, row, a, keep[row], blockIdx.x == 0);
+        if (t == 0) coef = k;
+        if constexpr (GRAD && Op::kListed) // the part's listed logits, before the gradient may overwrite them
+            for (uint32_t j = t; j < op.k; j += SG_WAVE) {
+                const uint32_t i = op.idx[row * op.k + j];
+                ls.id[j] = i;
+                ls.z[j] = i >= lo && i < lo + n ? RowIO<E>::get(x + (i - lo)) : 0.f;
+                ls.p[j] = (float)row_exp((double)op.logp[row * op.k + j]);
+            }
+    }
+    if constexpr (GRAD) {
+        __syncthreads();
+        grad_row(x, g, n, coef.coef, coef.m, r.c, t, SP_NT);
+        if (t < SG_WAVE) op.named_grad(r, coef, ls);
+        __syncthreads();
+        if (t < SG_WAVE) op.template put_named<E>(row, g, coef, ls, lo, lo + n);
     }
 }
 
@@ -479,22 +671,25 @@ __global__ __launch_bounds__(PF_NT) void pref_pair_kernel(PairArgs p)
     }
 }
 
-// gradient rows from the kept maximum and 1/sum: slope * (1[i = y] - q_i)
+// gradient rows from the kept maximum and 1/sum: slope * (1[i = y] - q_i).
+// gridDim.x parts of len elements to a row.
 template <typename E>
-__global__ __launch_bounds__(RL_NT) void pref_grad_kernel(Rows r, TokenOp op, void* grad, uint64_t ldg)
+__global__ __launch_bounds__(PF_NT) void pref_grad_kernel(Rows r, TokenOp op, uint32_t len, void* grad, uint64_t ldg)
 {
-    for (uint64_t row = blockIdx.x; row < r.T; row += gridDim.x) {
-        const E* x = static_cast<const E*>(r.x) + row * r.ld;
-        E* g = static_cast<E*>(grad) + row * ldg;
+    const uint32_t lo = blockIdx.x * len, n = r.V - lo < len ? r.V - lo : len;
+    for (uint64_t row = blockIdx.y; row < r.T; row += gridDim.y) {
+        const E* x = static_cast<const E*>(r.x) + row * r.ld + lo;
+        E* g = static_cast<E*>(grad) + row * ldg + lo;
         const float slope = op.slope[row];
         if (slope == 0.f) {
-            zero_row(g, r.V, threadIdx.x, RL_NT);
+            zero_row(g, n, threadIdx.x, PF_NT);
             continue;
         }
-        grad_row(x, g, r.V, RowCoef{op.m[row], -slope * op.inv[row]}, r.c, threadIdx.x, RL_NT);
+        grad_row(x, g, n, -slope * op.inv[row], op.m[row], r.c, threadIdx.x, PF_NT);
         __syncthreads();
-        if (threadIdx.x == 0)
-            RowIO<E>::put(g + op.label[row], (float)((double)slope * -row_expm1(op.logp[row])));
+        const uint32_t y = (uint32_t)op.label[row];
+        if (threadIdx.x == 0 && y >= lo && y < lo + n)
+            RowIO<E>::put(g + (y - lo), (float)((double)slope * -row_expm1(op.logp[row])));
     }
 }
 
@@ -502,10 +697,10 @@ __global__ __launch_bounds__(RL_NT) void pref_grad_kernel(Rows r, TokenOp op, vo
 // host side
 // ---------------------------------------------------------------------------
 constexpr uint64_t ROWS_PER_LAUNCH = 1u << 20; // a launch holds fewer than 2^32 threads
+constexpr uint64_t GRID_Y = 65535;
 
 struct RowCheck {
     Rows r;
-    unsigned grid;
 };
 
 static uint64_t row_esize(sg_dtype dt) { return dt == SG_BF16 ? 2 : 4; }
@@ -524,7 +719,6 @@ static int rows_args(const void* x, sg_dtype dt, uint64_t T, uint64_t V, uint64_
     out->r.V = (uint32_t)V;
     out->r.it = inv_temp;
     out->r.c = (float)(inv_temp * 1.4426950408889634074); // log2(e)
-    out->grid = (unsigned)(T < (1u << 20) ? T : (1u << 20));
     return SG_OK;
 }
 
@@ -536,7 +730,64 @@ static int grad_args(const void* x, uint64_t ld, const void* grad, sg_dtype dt, 
     return SG_OK;
 }
 
-template <typename E, int NT, int J, class Op>
+// Few rows leave most of the chip idle with a block per row, and one compute
+// unit takes some 11 us for 128 KiB of row; parts of 32 KiB in two launches
+// take about 10 us and 4 us more on the host, so rows longer than that are
+// split when there are fewer than 128.
+static uint32_t row_parts(uint64_t T, uint64_t V, uint64_t esize)
+{
+    const uint64_t bytes = V * esize;
+    if (T >= 128 || bytes <= 128 * 1024) return 1;
+    const uint64_t p = ceil_div(bytes, 32 * 1024);
+    return (uint32_t)(p < RL_MAX_PARTS ? p : RL_MAX_PARTS);
+}
+
+// elements to a part: whole chunks, and no part empty
+static uint32_t part_len(uint64_t V, uint32_t* parts)
+{
+    const uint64_t len = align_up(ceil_div(V, *parts), 64);
+    *parts = (uint32_t)ceil_div(V, len);
+    return (uint32_t)len;
+}
+
+template <class Op>
+struct SplitWs {
+    RowStat* stat;
+    typename Op::Named* keep;
+};
+
+template <class Op>
+static SplitWs<Op> split_carve(Carver& cv, uint64_t T, uint32_t parts)
+{
+    SplitWs<Op> w = {nullptr, nullptr};
+    if (parts > 1) {
+        w.stat = cv.take<RowStat>(T * parts);
+        w.keep = cv.take<typename Op::Named>(T);
+    }
+    return w;
+}
+
+// a listed row, or its part, has its bitmap in LDS (32 KiB): longer rows are split whatever their number
+constexpr uint64_t RL_MAX_BITS = 1u << 18;
+template <class Op>
+static uint32_t op_parts(uint64_t T, uint64_t V, sg_dtype dt)
+{
+    uint32_t parts = row_parts(T, V, row_esize(dt));
+    if (Op::kListed && V > RL_MAX_BITS * parts) parts = (uint32_t)ceil_div(V, RL_MAX_BITS);
+    return parts;
+}
+
+template <class Op>
+static size_t split_bytes(uint64_t T, uint64_t V, sg_dtype dt)
+{
+    if (T >= (1ull << 31) || V == 0 || V >= (1ull << 31) || (dt != SG_F32 && dt != SG_BF16)) return 0;
+    const uint32_t parts = op_parts<Op>(T, V, dt);
+    Carver cv(nullptr);
+    split_carve<Op>(cv, T, parts);
+    return parts > 1 ? cv.bytes() : 0;
+}
+
+template <typename E, int NT, int J, int WAVES, class Op>
 static int launch_rows(const RowCheck& c, const Op& op, size_t lds, void* grad, uint64_t ldg, hipStream_t st)
 {
     Rows r = c.r;
@@ -544,35 +795,82 @@ static int launch_rows(const RowCheck& c, const Op& op, size_t lds, void* grad, 
         const uint64_t left = r.T - r.row0;
         const unsigned grid = (unsigned)(left < ROWS_PER_LAUNCH ? left : ROWS_PER_LAUNCH);
         if constexpr (Op::kGrad)
-            if (grad) row_loss_kernel<E, NT, J, Op, true><<<grid, NT, lds, st>>>(r, op, grad, ldg);
-        if (!grad) row_loss_kernel<E, NT, 4, Op, false><<<grid, NT, lds, st>>>(r, op, grad, ldg);
+            if (grad) row_loss_kernel<E, NT, J, Op, true, WAVES><<<grid, NT, lds, st>>>(r, op, grad, ldg);
+        if (!grad) row_loss_kernel<E, NT, 2, Op, false, 8><<<grid, NT, lds, st>>>(r, op, grad, ldg);
         SG_TRY_LAUNCH();
     }
     return SG_OK;
 }
 
 template <typename E, class Op>
-static int launch_row_loss_of(const RowCheck& c, const Op& op, size_t lds, void* grad, uint64_t ldg, hipStream_t st)
+static int launch_split(const RowCheck& c, const Op& op, uint32_t parts, void* grad, uint64_t ldg, void* ws,
+                        hipStream_t st)
 {
+    Carver cv(ws);
+    const SplitWs<Op> w = split_carve<Op>(cv, c.r.T, parts);
+    SplitArgs s = {w.stat, parts, 0};
+    s.len = part_len(c.r.V, &s.parts);
+    const size_t lds = Op::kListed ? ceil_div(s.len + 8, 32) * 4 : 0;
+    Rows r = c.r;
+    typename Op::Named* keep = w.keep;
+    for (r.row0 = 0; r.row0 < c.r.T; r.row0 += GRID_Y) {
+        const unsigned rows = (unsigned)(c.r.T - r.row0 < GRID_Y ? c.r.T - r.row0 : GRID_Y);
+        row_part_kernel<E, Op><<<dim3(s.parts, rows), SP_NT, lds, st>>>(r, op, s, keep);
+        SG_TRY_LAUNCH();
+        if constexpr (Op::kGrad)
+            if (grad) row_join_kernel<E, Op, true><<<dim3(s.parts, rows), SP_NT, 0, st>>>(r, op, s, keep, grad, ldg);
+        if (!grad) row_join_kernel<E, Op, false><<<dim3(1, rows), SG_WAVE, 0, st>>>(r, op, s, keep, nullptr, 0);
+        SG_TRY_LAUNCH();
+    }
+    return SG_OK;
+}
+
+// Threads, chunks kept and waves per SIMD by the row's bytes, measured on
+// rows of bf16 with a policy gradient (TB/s read and written): 8 KB 4.6 with
+// 256 threads, 2.8 with 512; 32 KB 5.2 with 512, 4.8 with 256; 100 KB 5.1
+// with 512 threads that keep 16 chunks, 4.5 with 1024; 200 KB 5.05 with 1024,
+// 4.7 with 512 (which keep half of it and read the rest again).
+template <typename E, class Op>
+static int launch_row_loss_of(const RowCheck& c, const Op& op, void* grad, uint64_t ldg, void* ws, sg_dtype dt,
+                              hipStream_t st)
+{
+    const uint32_t parts = op_parts<Op>(c.r.T, c.r.V, dt);
+    if (parts > 1) return launch_split<E>(c, op, parts, grad, ldg, ws, st);
     const uint64_t bytes = (uint64_t)c.r.V * sizeof(E);
-    if (bytes <= 256 * 8 * 16) return launch_rows<E, 256, 8>(c, op, lds, grad, ldg, st);
-    if (bytes <= 512 * 16 * 16) return launch_rows<E, 512, 16>(c, op, lds, grad, ldg, st);
-    return launch_rows<E, 1024, 16>(c, op, lds, grad, ldg, st);
+    const size_t lds = Op::kListed ? ceil_div((uint64_t)c.r.V + 8, 32) * 4 : 0;
+    constexpr bool L = Op::kListed; // one wave less for the row
+    if (bytes <= 4 * 1024) return launch_rows<E, L ? 128 : 64, 4, L ? 6 : 8>(c, op, lds, grad, ldg, st);
+    if (bytes <= 16 * 1024) return launch_rows<E, 256, L ? 6 : 4, L ? 6 : 8>(c, op, lds, grad, ldg, st);
+    if (bytes <= 64 * 1024) return launch_rows<E, 512, L ? 9 : 8, L ? 4 : 8>(c, op, lds, grad, ldg, st);
+    if (bytes <= 128 * 1024) return launch_rows<E, 512, L ? 18 : 16, 4>(c, op, lds, grad, ldg, st);
+    return launch_rows<E, 1024, L ? 17 : 16, 4>(c, op, lds, grad, ldg, st);
 }
 
 template <class Op>
-static int launch_row_loss(const RowCheck& c, sg_dtype dt, const Op& op, size_t lds, void* grad, uint64_t ldg,
+static int launch_row_loss(const RowCheck& c, sg_dtype dt, const Op& op, void* grad, uint64_t ldg, void* ws,
                            hipStream_t st)
 {
-    if (dt == SG_BF16) return launch_row_loss_of<bf16_bits>(c, op, lds, grad, ldg, st);
-    return launch_row_loss_of<float>(c, op, lds, grad, ldg, st);
+    if (dt == SG_BF16) return launch_row_loss_of<bf16_bits>(c, op, grad, ldg, ws, dt, st);
+    return launch_row_loss_of<float>(c, op, grad, ldg, ws, dt, st);
+}
+
+// a split call's workspace
+template <class Op>
+static int check_split_ws(uint64_t T, uint64_t V, sg_dtype dt, const void* ws, size_t ws_bytes)
+{
+    const size_t need = split_bytes<Op>(T, V, dt);
+    if (need > 0 && !ws) return SG_EINVAL;
+    return ws_bytes < need ? SG_ECAPACITY : SG_OK;
 }
 
 } // namespace sg
 
 using namespace sg;
 
-extern "C" size_t sg_distill_workspace_bytes(uint64_t T, uint64_t V, uint32_t k, sg_dtype dt) { return 0; }
+extern "C" size_t sg_distill_workspace_bytes(uint64_t T, uint64_t V, uint32_t k, sg_dtype dt)
+{
+    return split_bytes<DistillOp>(T, V, dt);
+}
 
 extern "C" int sg_distill_loss(const void* d_logits, sg_dtype dt, uint64_t T, uint64_t V, uint64_t ld,
                                double inv_temp, const uint32_t* d_idx, const float* d_logp, uint32_t k,
@@ -586,13 +884,17 @@ extern "C" int sg_distill_loss(const void* d_logits, sg_dtype dt, uint64_t T, ui
     if (mode != SG_DISTILL_PLAIN && mode != SG_DISTILL_RENORM && mode != SG_DISTILL_TAIL) return SG_EINVAL;
     if ((rc = grad_args(d_logits, ld, d_grad, dt, V, ld_grad))) return rc;
     if (T > 0 && (!d_idx || !d_logp || !d_loss)) return SG_EINVAL;
-    if (k > SG_ROWS_MAX_K || V > 14 * 32768u) return SG_EUNSUPPORTED;
+    if (k > SG_ROWS_MAX_K || V > RL_MAX_BITS * RL_MAX_PARTS) return SG_EUNSUPPORTED;
     if (T == 0) return SG_OK;
+    if ((rc = check_split_ws<DistillOp>(T, V, dt, d_ws, ws_bytes))) return rc;
     DistillOp op = {d_idx, d_logp, d_weight, d_loss, k, (uint32_t)V, (int)mode};
-    return launch_row_loss(c, dt, op, ceil_div(V + 8, 32) * 4, d_grad, ld_grad, as_stream(stream));
+    return launch_row_loss(c, dt, op, d_grad, ld_grad, d_ws, as_stream(stream));
 }
 
-extern "C" size_t sg_policy_workspace_bytes(uint64_t T, uint64_t V, sg_dtype dt) { return 0; }
+extern "C" size_t sg_policy_workspace_bytes(uint64_t T, uint64_t V, sg_dtype dt)
+{
+    return split_bytes<PolicyOp>(T, V, dt);
+}
 
 extern "C" int sg_policy_loss(const void* d_logits, sg_dtype dt, uint64_t T, uint64_t V, uint64_t ld, double inv_temp,
                               const int32_t* d_action, const float* d_old_logp, const float* d_ref_logp,
@@ -608,19 +910,22 @@ extern "C" int sg_policy_loss(const void* d_logits, sg_dtype dt, uint64_t T, uin
     if ((rc = grad_args(d_logits, ld, d_grad, dt, V, ld_grad))) return rc;
     if (T > 0 && (!d_action || !d_loss)) return SG_EINVAL;
     if (T == 0) return SG_OK;
+    if ((rc = check_split_ws<PolicyOp>(T, V, dt, d_ws, ws_bytes))) return rc;
     PolicyOp op = {d_action, d_old_logp, kl_coef != 0.0 ? d_ref_logp : nullptr, d_adv, d_weight, d_loss, d_logp,
                    1.0 - clip_low, 1.0 + clip_high, kl_coef, (uint32_t)V};
-    return launch_row_loss(c, dt, op, 0, d_grad, ld_grad, as_stream(stream));
+    return launch_row_loss(c, dt, op, d_grad, ld_grad, d_ws, as_stream(stream));
 }
 
 namespace sg {
 struct PrefWs {
     double* logp;
     float *m, *inv, *slope;
+    void* split; // of the token pass
 };
-static PrefWs pref_carve(Carver& cv, uint64_t T)
+static PrefWs pref_carve(Carver& cv, uint64_t T, uint64_t V, sg_dtype dt)
 {
     PrefWs w;
+    w.split = cv.take<char>(split_bytes<TokenOp>(T, V, dt));
     w.logp = cv.take<double>(T);
     w.m = cv.take<float>(T);
     w.inv = cv.take<float>(T);
@@ -631,9 +936,9 @@ static PrefWs pref_carve(Carver& cv, uint64_t T)
 
 extern "C" size_t sg_preference_workspace_bytes(uint64_t T, uint64_t V, sg_dtype dt)
 {
-    if (T >= (1ull << 31) || V == 0 || V >= (1ull << 31)) return 0;
+    if (T >= (1ull << 31) || V == 0 || V >= (1ull << 31) || (dt != SG_F32 && dt != SG_BF16)) return 0;
     Carver cv(nullptr);
-    pref_carve(cv, T);
+    pref_carve(cv, T, V, dt);
     return cv.bytes();
 }
 
@@ -655,9 +960,9 @@ extern "C" int sg_preference_loss(const void* d_logits, sg_dtype dt, uint64_t T,
     if (ws_bytes < sg_preference_workspace_bytes(T, V, dt)) return SG_ECAPACITY;
     hipStream_t st = as_stream(stream);
     Carver cv(d_ws);
-    const PrefWs w = pref_carve(cv, T);
+    const PrefWs w = pref_carve(cv, T, V, dt);
     TokenOp op = {d_label, w.logp, w.m, w.inv, w.slope, (uint32_t)V};
-    if (T > 0 && (rc = launch_row_loss(c, dt, op, 0, nullptr, 0, st))) return rc;
+    if (T > 0 && (rc = launch_row_loss(c, dt, op, nullptr, 0, w.split, st))) return rc;
     if (pairs > 0) {
         PairArgs p = {d_seq_off, d_ref_logp, d_weight, d_label, w.logp, w.slope, d_loss, d_logp, T, pairs,
                       (uint32_t)V, (int)kind, average ? 1 : 0, d_grad ? 1 : 0, beta, smoothing};
@@ -665,8 +970,13 @@ extern "C" int sg_preference_loss(const void* d_logits, sg_dtype dt, uint64_t T,
         SG_TRY_LAUNCH();
     }
     if (T > 0 && d_grad) {
-        if (dt == SG_BF16) pref_grad_kernel<bf16_bits><<<c.grid, RL_NT, 0, st>>>(c.r, op, d_grad, ld_grad);
-        else pref_grad_kernel<float><<<c.grid, RL_NT, 0, st>>>(c.r, op, d_grad, ld_grad);
+        // enough blocks to fill the chip, at least 16 KiB of row to each
+        const uint64_t most = ceil_div(V * row_esize(dt), 16 * 1024), want = ceil_div(1024, T);
+        uint32_t parts = (uint32_t)(want < most ? want : most);
+        const uint32_t len = part_len(V, &parts);
+        const dim3 grid(parts, (unsigned)(T < GRID_Y ? T : GRID_Y));
+        if (dt == SG_BF16) pref_grad_kernel<bf16_bits><<<grid, PF_NT, 0, st>>>(c.r, op, len, d_grad, ld_grad);
+        else pref_grad_kernel<float><<<grid, PF_NT, 0, st>>>(c.r, op, len, d_grad, ld_grad);
         SG_TRY_LAUNCH();
     }
     return SG_OK;

@@ -148,13 +148,18 @@ __device__ __forceinline__ P* chunk_at(P* x, uint32_t j, uint32_t j0)
     return x + (uint64_t)j * RowIO<E>::VEC + j0 * RowIO<E>::VEC;
 }
 
-// chunks j0, j0 + NT, ... of a row
+// Chunks j0, j0 + NT, ... of a row with nc > 0 chunks.  Past the row's end the
+// last chunk is loaded again: with every load issued on every path, the wait
+// for one of them need not be a wait for all (a load in a branch may or may
+// not be among those in flight, so the compiler waits until none is).
 template <int J, int NT, typename E>
 __device__ __forceinline__ void load_chunks(u32x4* w, const E* x, uint32_t j0, uint32_t nc)
 {
 #pragma unroll
-    for (int j = 0; j < J; ++j)
-        if (j0 + j * NT < nc) w[j] = load_chunk(chunk_at<E>(x, j * NT, j0));
+    for (int j = 0; j < J; ++j) {
+        const uint32_t c = j0 + j * NT < nc ? j0 + j * NT : nc - 1;
+        w[j] = load_chunk(chunk_at<E>(x, 0, c));
+    }
 }
 
 __device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
@@ -197,6 +202,13 @@ __device__ __forceinline__ RowStat wave_stat(RowStat r, float c)
         r = (lane_id() & d) ? stat_join(o, r, c) : stat_join(r, o, c);
     }
     return r;
+}
+
+constexpr int next_pow2(int n)
+{
+    int p = 1;
+    while (p < n) p *= 2;
+    return p;
 }
 
 __device__ __forceinline__ double wave_sum_f64(double v)

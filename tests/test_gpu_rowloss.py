@@ -105,10 +105,12 @@ def run_distill(x, xs, idx, logp, w, temp, mode, dtype, grad=None):
 # registers and the whole-row limit
 SIZES = [(1, 1), (3, 2), (2, 7), (5, 8), (4, 9), (3, 255), (7, 1000), (5, 2048), (6, 4099), (3, 16384), (4, 32000),
          (2, 65536), (3, 70001), (2, 131072), (2, 131083), (2, 262144), (1, 262153), (300, 1030), (270, 9001)]
+# the same limits with enough rows that none is split over blocks
+MANY = [(200, 2048), (200, 2051), (150, 8200), (140, 16390), (130, 33000), (129, 66001)]
 
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
-@pytest.mark.parametrize("T,V", SIZES)
+@pytest.mark.parametrize("T,V", SIZES + MANY)
 def test_distill_sizes(T, V, dtype):
     need_gpu()
     k = min(V, 1 + (T * 7 + V) % 40)
@@ -238,7 +240,7 @@ def run_policy(x, xs, a, old, rf, adv, w, temp, lo, hi, kl, dtype, grad=None, st
 
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
-@pytest.mark.parametrize("T,V", SIZES)
+@pytest.mark.parametrize("T,V", SIZES + MANY)
 def test_policy_sizes(T, V, dtype):
     need_gpu()
     temp = (1.0, 0.7, 2.0)[(T + V) % 3]
@@ -494,6 +496,41 @@ def test_offsets_beyond_32_bits():
     loss, _ = sg.sg_distill_loss(x, idx, lp, weight=w, want_grad=False)
     loss1, _ = sg.sg_distill_loss(tail[2:], idx[-1:], lp[-1:], want_grad=False)
     check(host(loss[-1:]), host(loss1), tol * (1 + np.abs(host(loss1))), "distill")
+
+
+def test_many_rows_longer_than_a_bitmap():
+    """Lists over rows of more than 2^18 tokens, in parts whatever the number of rows."""
+    need_gpu()
+    T, V, k = 130, 262200, 9
+    x = torch.randn((T, V), device="cuda").bfloat16()
+    idx, logp = make_lists(72, T, V, k)
+    idx, logp = dev(idx, torch.int32), dev(logp, torch.float32)
+    loss, g = sg.sg_distill_loss(x, idx, logp)
+    for r in (0, 64, 127):
+        loss3, g3 = sg.sg_distill_loss(x[r:r + 3], idx[r:r + 3], logp[r:r + 3])
+        L, G, tl, tg = distill_reference(host(x[r:r + 1]), idx[r:r + 1].cpu().numpy(), logp[r:r + 1].cpu().numpy(),
+                                         np.ones(1), 1.0, "tail")
+        for a, b in ((loss[r:r + 1], g[r:r + 1]), (loss3[:1], g3[:1])):
+            check(host(a), L, tl, "loss")
+            check(host(b), G, tg + ref.HALF["bf16"] * np.abs(G) + 1e-38, "gradient")
+
+
+def test_split_rows_beyond_a_grid_dimension():
+    """65540 rows in parts: the last ones are those of a short call."""
+    need_gpu()
+    T, V = 65540, 262200
+    x = torch.empty((T, V), dtype=torch.bfloat16, device="cuda")  # rows of weight 0 are not read
+    tail, _ = make_logits(73, 3, V, "bf16")
+    x[-3:] = tail
+    idx = torch.full((T, 2), -1, dtype=torch.int32, device="cuda")
+    idx[-3:] = torch.tensor([7, V - 2], dtype=torch.int32)
+    lp = torch.full((T, 2), -1.5, device="cuda")
+    w = torch.zeros(T, device="cuda")
+    w[-3:] = 1.0
+    loss, _ = sg.sg_distill_loss(x, idx, lp, weight=w, want_grad=False)
+    loss3, _ = sg.sg_distill_loss(tail, idx[-3:], lp[-3:], want_grad=False)
+    check(host(loss[-3:]), host(loss3), 8 * ref.sum_error(V), "loss")
+    assert not loss[:-3].any()
 
 
 def test_on_another_stream_and_in_a_graph():
