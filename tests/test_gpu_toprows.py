@@ -7,7 +7,7 @@ import torch
 import rowloss_ref as ref
 import sparse_gradient_synchronization_amd as sg
 from gpu_util import need_gpu
-from test_gpu_rowloss import SIZES, TDT, check, host, make_logits
+from test_gpu_rowloss import MANY, SIZES, TDT, check, host, make_logits
 
 pytestmark = pytest.mark.gpu
 
@@ -23,13 +23,20 @@ def run(x, xs, k, temp=1.0):
     return idx, logp, lse
 
 
+# the longest row of a wave and the next one, the longest whose line maxima fit
+# (one line more takes the whole-row select), with and without parts
+EDGES = [(3, 4095), (3, 4096), (3, 4097), (130, 4096), (130, 2048), (130, 2049), (1, 300001), (1, 1 << 20),
+         (129, 262144), (129, 262145), (2, 524287), (2, 524288)]
+
+
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
-@pytest.mark.parametrize("T,V", SIZES + [(1, 300001), (1, 1 << 20)])
+@pytest.mark.parametrize("T,V", SIZES + MANY + EDGES)
 def test_sizes(T, V, dtype):
     need_gpu()
     x, xs = make_logits(T + 2 * V, T, V, dtype)
     for k in sorted({1, min(V, 1 + (V * 3 + T) % 60), min(V, 256)}):
-        run(x, xs, k, (1.0, 2.0, 0.7)[V % 3])
+        if T * V < 10000000 or k > 1:
+            run(x, xs, k, (1.0, 2.0, 0.7)[V % 3])
 
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
@@ -37,8 +44,9 @@ def test_sizes(T, V, dtype):
 @pytest.mark.parametrize("k", [1, 2, 63, 64, 65, 511, 512, 513, 1023, 1024])
 def test_list_lengths(k, T, dtype):
     need_gpu()
-    x, xs = make_logits(k, T, 4001, dtype)
-    run(x, xs, k)
+    for V in (1100, 4001, 9001) if T > 2 else (1100, 4001, 9001, 140001):
+        x, xs = make_logits(k, T, V, dtype)
+        run(x, xs, k)
 
 
 @pytest.mark.parametrize("T", [1, 260])
