@@ -605,7 +605,10 @@ def _grad_of(logits, want_grad, grad):
     if grad is None:
         if not want_grad:
             return None, None, 0
-        grad = torch.empty(logits.shape, dtype=logits.dtype, device=logits.device)
+        if logits.is_contiguous():
+            grad = torch.empty_like(logits)
+        else:
+            grad = torch.empty(logits.shape, dtype=logits.dtype, device=logits.device)
         return grad, grad.data_ptr(), logits.shape[1]
     T, V = logits.shape
     if grad.dtype != logits.dtype or grad.shape != logits.shape or grad.get_device() != logits.get_device():
@@ -656,7 +659,7 @@ def sg_distill_loss(logits: torch.Tensor, idx: torch.Tensor, logp: torch.Tensor,
     logits [T, V], idx [T, k] int32, logp [T, k] float32, weight [T] float32
     -> (loss [T] float32, weighted; grad [T, V] of loss.sum(), or None).
     grad: where to write the gradient, logits itself included."""
-    _need_cuda(logits, idx, logp, weight, grad)
+    _need_cuda(logits)
     L, dev, f = lib(), logits.device, torch.float32
     grad, p_grad, ldg = _grad_of(logits, want_grad, grad)
     logits, dt, T, V, ld = _rows(logits)
@@ -679,7 +682,7 @@ def sg_policy_loss(logits: torch.Tensor, action: torch.Tensor, old_logp=None, ad
     old_logp, adv, ref_logp, weight [T] float32 or None -> (loss [T] float32,
     weighted; logp [T] float32 of the actions; grad [T, V] of loss.sum(), or
     None).  grad: where to write the gradient, logits itself included."""
-    _need_cuda(logits, action, old_logp, adv, ref_logp, weight, grad)
+    _need_cuda(logits)
     L, dev, f = lib(), logits.device, torch.float32
     grad, p_grad, ldg = _grad_of(logits, want_grad, grad)
     logits, dt, T, V, ld = _rows(logits)
@@ -710,7 +713,7 @@ def sg_preference_loss(logits: torch.Tensor, label: torch.Tensor, seq_off: torch
     grad [T, V] of loss.sum(), or None).  smoothing applies to
     SG_PREF_SIGMOID.  grad: where to write the gradient, logits itself
     included."""
-    _need_cuda(logits, label, seq_off, ref_logp, weight, grad)
+    _need_cuda(logits)
     L, dev, f = lib(), logits.device, torch.float32
     grad, p_grad, ldg = _grad_of(logits, want_grad, grad)
     logits, dt, T, V, ld = _rows(logits)

@@ -14,6 +14,7 @@
 namespace sg {
 
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x4_at2 __attribute__((ext_vector_type(4), aligned(2))); // anywhere an element may be
 
 struct Rows {
     const void* x; // [T] rows, ld elements apart
@@ -29,12 +30,13 @@ struct RowSpan {
     uint32_t head, nc, V; // first element of chunk 0, whole chunks, elements
 };
 
-template <typename E>
+// BYTES: where the chunks start, 16 or a cache line's 128
+template <int BYTES = 16, typename E>
 __device__ __forceinline__ RowSpan span_of(const E* x, uint32_t V)
 {
     constexpr uint32_t VEC = 16 / sizeof(E);
     RowSpan s;
-    s.head = (uint32_t)(-(reinterpret_cast<uintptr_t>(x) / sizeof(E))) % VEC;
+    s.head = (uint32_t)(-(reinterpret_cast<uintptr_t>(x) / sizeof(E))) % (BYTES / sizeof(E));
     s.head = s.head < V ? s.head : V;
     s.nc = (V - s.head) / VEC;
     s.V = V;
@@ -134,10 +136,13 @@ __device__ __forceinline__ u32x4 load_chunk(const E* p)
     return r;
 }
 
-template <typename E>
+// PAST: the store goes past the caches (a template, since the compiler makes
+// one ordinary store of two in branches)
+template <bool PAST, typename E>
 __device__ __forceinline__ void store_chunk(E* p, u32x4 v)
 {
-    __builtin_memcpy(p, &v, 16);
+    if (PAST) __builtin_nontemporal_store(v, reinterpret_cast<u32x4_at2*>(p));
+    else __builtin_memcpy(p, &v, 16);
 }
 
 // address of chunk j + j0: j is the same for all lanes, so it goes into a
