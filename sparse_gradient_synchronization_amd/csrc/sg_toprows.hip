@@ -463,8 +463,9 @@ __global__ __launch_bounds__(NT, 8) void top_rows_kernel(TopArgs p)
         const uint32_t wv = uniform(t / SG_WAVE);
         const uint32_t l0 = (uint32_t)((uint64_t)nl * wv / NW), l1 = (uint32_t)((uint64_t)nl * (wv + 1) / NW);
         const uint32_t want = (k + NW - 1) / NW;
-        const float reach = nl <= 2 * SG_WAVE * NW - NW ? lines_reach<2>(lines, l0, l1, want)
-                                                        : lines_reach<RMAX>(lines, l0, l1, want);
+        const float reach = l1 - l0 <= 2 * SG_WAVE   ? lines_reach<2>(lines, l0, l1, want)
+                            : l1 - l0 <= 4 * SG_WAVE ? lines_reach<4>(lines, l0, l1, want)
+                                                     : lines_reach<RMAX>(lines, l0, l1, want);
         if (lane_id() == 0) sh.low[wv] = reach;
         __syncthreads();
         float low = sh.low[0];
@@ -488,45 +489,62 @@ __global__ __launch_bounds__(NT, 8) void top_rows_kernel(TopArgs p)
                 uint32_t* list = reinterpret_cast<uint32_t*>(lines);
                 for (uint32_t i = t; i < nlc; i += NT) list[i] = cidx[i];
                 __syncthreads();
-                const uint32_t items = 8 * nlc + 2, each = (items + NT - 1) / NT;
-                const auto item = [&](uint32_t q, float* v, uint32_t* first) {
-                    uint32_t len = 0;
-                    *first = 0;
-                    if (q == 0) {
-                        len = sp.head;
-                    } else if (q == items - 1) {
-                        *first = sp.head + sp.nc * VEC;
-                        len = V - *first;
-                    } else {
-                        const uint32_t ch = list[(q - 1) / 8] * TR_LINE + (q - 1) % 8;
-                        *first = sp.head + ch * VEC;
-                        if (ch < sp.nc) len = VEC;
-                    }
-                    if (len == VEC) {
-                        RowIO<E>::unpack(load_chunk(x + *first), v);
-                    } else {
+                const uint32_t items = 8 * nlc + 2;
+                constexpr int B = 4; // neighbours to a thread, loaded together
+                for (uint32_t q0 = 0; q0 < items; q0 += B * NT) {
+                    u32x4 it[B];
+                    uint32_t first[B], e = 0, total;
 #pragma unroll
-                        for (int i = 0; i < VEC; ++i) v[i] = i < (int)len ? RowIO<E>::get(x + *first + i) : -INFINITY;
-                    }
-                };
-                float v[VEC];
-                uint32_t first, e = 0;
-                for (uint32_t q = t * each; q < (t + 1) * each && q < items; ++q) {
-                    item(q, v, &first);
+                    for (int i = 0; i < B; ++i) {
+                        const uint32_t q = q0 + t * B + i;
+                        uint32_t len = 0;
+                        first[i] = 0;
+                        if (q == 0) {
+                            len = sp.head;
+                        } else if (q == items - 1) {
+                            first[i] = sp.head + sp.nc * VEC;
+                            len = V - first[i];
+                        } else if (q < items) {
+                            const uint32_t ch = list[(q - 1) / 8] * TR_LINE + (q - 1) % 8;
+                            first[i] = sp.head + ch * VEC;
+                            if (ch < sp.nc) len = VEC;
+                        }
+                        if (len == VEC) {
+                            it[i] = load_chunk(x + first[i]);
+                        } else {
+                            float v[VEC];
 #pragma unroll
-                    for (int i = 0; i < VEC; ++i) e += v[i] >= low ? 1u : 0u;
+                            for (int c = 0; c < VEC; ++c) v[c] = c < (int)len ? RowIO<E>::get(x + first[i] + c) : -INFINITY;
+                            it[i] = RowIO<E>::pack(v);
+                        }
+                    }
+#pragma unroll
+                    for (int i = 0; i < B; ++i) {
+                        float v[VEC];
+                        RowIO<E>::unpack(it[i], v);
+#pragma unroll
+                        for (int c = 0; c < VEC; ++c) e += v[c] >= low ? 1u : 0u;
+                        __builtin_amdgcn_sched_barrier(0);
+                    }
+                    uint32_t to = n + block_excl_scan<NT>(e, sh.scan, &total);
+                    if (e)
+#pragma unroll
+                        for (int i = 0; i < B; ++i) {
+                            float v[VEC];
+                            RowIO<E>::unpack(it[i], v);
+#pragma unroll
+                            for (int c = 0; c < VEC; ++c)
+                                if (v[c] >= low) {
+                                    if (to < cap) {
+                                        ckey[to] = order_key(v[c]);
+                                        cidx[to] = first[i] + c;
+                                    }
+                                    ++to;
+                                }
+                        }
+                    n += total;
+                    __syncthreads(); // the scan's words
                 }
-                uint32_t to = block_excl_scan<NT>(e, sh.scan, &n);
-                if (n <= cap && e)
-                    for (uint32_t q = t * each; q < (t + 1) * each && q < items; ++q) {
-                        if (each > 1) item(q, v, &first);
-#pragma unroll
-                        for (int i = 0; i < VEC; ++i)
-                            if (v[i] >= low) {
-                                ckey[to] = order_key(v[i]);
-                                cidx[to++] = first + i;
-                            }
-                    }
                 if (t < 4 && n + t < cap) ckey[n + t] = 0;
                 if (n > cap) n = 0;
             }
