@@ -71,7 +71,8 @@ __device__ __forceinline__ float top_logp(float v, float m, double log_s, double
 // short rows: a wave per row
 // ---------------------------------------------------------------------------
 constexpr int TW_R = 8;             // chunks of a lane
-constexpr uint32_t TW_CAP = 512;    // candidates
+constexpr uint32_t TW_CAP = 1024;   // candidates
+constexpr uint32_t TW_MAX_K = 256;  // longer lists leave too many candidates
 
 // the k-th largest of the keys a wave holds: count(c) says how many are at
 // least c; from bit 31 down to low_bit
@@ -111,7 +112,8 @@ __global__ __launch_bounds__(SG_WAVE, 6) void top_wave_kernel(TopArgs p)
 {
     constexpr int VEC = RowIO<E>::VEC, R = TW_R;
     constexpr int low_shift = sizeof(E) == 2 ? 16 : 0;
-    __shared__ uint32_t ckey[TW_CAP], cidx[TW_CAP];
+    __shared__ uint32_t ckey[TW_CAP];
+    __shared__ uint16_t cidx[TW_CAP]; // a row here has at most 4096 elements
     const uint32_t l = threadIdx.x, V = p.r.V, k = p.k;
     const uint64_t row = p.r.row0 + blockIdx.x;
     const E* x = static_cast<const E*>(p.r.x) + row * p.r.ld;
@@ -179,7 +181,7 @@ __global__ __launch_bounds__(SG_WAVE, 6) void top_wave_kernel(TopArgs p)
                         if (v[i] >= low && first + i < V) {
                             if (pos < TW_CAP) {
                                 ckey[pos] = order_key(v[i]);
-                                cidx[pos] = first + i;
+                                cidx[pos] = (uint16_t)(first + i);
                             }
                             ++pos;
                         }
@@ -195,7 +197,7 @@ __global__ __launch_bounds__(SG_WAVE, 6) void top_wave_kernel(TopArgs p)
     };
     if (n <= TW_CAP) {
         wave_sync();
-        // a lane holds candidates l, l + 64, ...: up to two in nearly all rows
+        // a lane holds candidates l, l + 64, ...: two or four in nearly all rows
         uint32_t key[TW_CAP / SG_WAVE];
         const uint32_t rounds = (n + SG_WAVE - 1) / SG_WAVE;
 #pragma unroll
@@ -209,8 +211,10 @@ __global__ __launch_bounds__(SG_WAVE, 6) void top_wave_kernel(TopArgs p)
                 return h;
             });
         };
-        const uint32_t kth = whole_key(rounds <= 2 ? kth_of(std::integral_constant<int, 2>())
-                                                   : kth_of(std::integral_constant<int, TW_CAP / SG_WAVE>()), low_shift);
+        const uint32_t kth = whole_key(rounds <= 2   ? kth_of(std::integral_constant<int, 2>())
+                                       : rounds <= 4 ? kth_of(std::integral_constant<int, 4>())
+                                                     : kth_of(std::integral_constant<int, TW_CAP / SG_WAVE>()),
+                                       low_shift);
         uint32_t gt = 0;
 #pragma unroll
         for (uint32_t q = 0; q < TW_CAP / SG_WAVE; ++q) gt += popc64(ballot(key[q] > kth));
@@ -383,8 +387,8 @@ __device__ __forceinline__ float lines_reach(const float* lines, uint32_t lo, ui
     return cut_value(t);
 }
 
-// room for candidates: four times k, at least 1024
-__host__ __device__ constexpr uint32_t top_cap(uint32_t k) { return k <= 256 ? 1024 : 4 * k; }
+// room for candidates: four times k, at least 1024; 4096 take any row of so many elements as it is
+__host__ __device__ constexpr uint32_t top_cap(uint32_t k) { return k <= 256 ? 1024 : 4096; }
 
 // Dynamic LDS: candidates' keys and indices [cap], then the maximum of every
 // line, whose place the list of candidate lines takes once it is made.
@@ -471,7 +475,7 @@ __global__ __launch_bounds__(NT, 8) void top_rows_kernel(TopArgs p)
         float low = sh.low[0];
 #pragma unroll
         for (int i = 1; i < NW; ++i) low = fminf(low, sh.low[i]);
-        if (low > -INFINITY) {
+        if (low > -INFINITY || V <= cap) {
             // the lines that reach it, in order: a thread takes `per` neighbours
             const uint32_t per = (nl + NT - 1) / NT, b0 = t * per < nl ? t * per : nl, b1 = b0 + per < nl ? b0 + per : nl;
             uint32_t c = 0, nlc;
@@ -490,13 +494,14 @@ __global__ __launch_bounds__(NT, 8) void top_rows_kernel(TopArgs p)
                 for (uint32_t i = t; i < nlc; i += NT) list[i] = cidx[i];
                 __syncthreads();
                 const uint32_t items = 8 * nlc + 2;
-                constexpr int B = 4; // neighbours to a thread, loaded together
-                for (uint32_t q0 = 0; q0 < items; q0 += B * NT) {
+                constexpr int B = 4; // neighbours to a thread, loaded together; one if that is enough
+                const uint32_t per_t = items <= NT ? 1 : B;
+                for (uint32_t q0 = 0; q0 < items; q0 += per_t * NT) {
                     u32x4 it[B];
                     uint32_t first[B], e = 0, total;
 #pragma unroll
                     for (int i = 0; i < B; ++i) {
-                        const uint32_t q = q0 + t * B + i;
+                        const uint32_t q = (uint32_t)i < per_t ? q0 + t * per_t + i : items;
                         uint32_t len = 0;
                         first[i] = 0;
                         if (q == 0) {
@@ -514,7 +519,8 @@ __global__ __launch_bounds__(NT, 8) void top_rows_kernel(TopArgs p)
                         } else {
                             float v[VEC];
 #pragma unroll
-                            for (int c = 0; c < VEC; ++c) v[c] = c < (int)len ? RowIO<E>::get(x + first[i] + c) : -INFINITY;
+                            for (int c = 0; c < VEC; ++c) // a NaN is no candidate
+                                v[c] = c < (int)len ? RowIO<E>::get(x + first[i] + c) : __builtin_nanf("");
                             it[i] = RowIO<E>::pack(v);
                         }
                     }
@@ -676,7 +682,7 @@ static int launch_top_of(TopArgs p, void* ws, hipStream_t st)
         SG_TRY_LAUNCH();
         return SG_OK;
     }
-    if (bytes <= (uint64_t)SG_WAVE * TW_R * 16) {
+    if (bytes <= (uint64_t)SG_WAVE * TW_R * 16 && (p.k <= TW_MAX_K || p.r.V <= TW_CAP)) {
         for (p.r.row0 = 0; p.r.row0 < p.r.T; p.r.row0 += ROWS_PER_LAUNCH) {
             const uint64_t left = p.r.T - p.r.row0;
             top_wave_kernel<E><<<(unsigned)(left < ROWS_PER_LAUNCH ? left : ROWS_PER_LAUNCH), SG_WAVE, 0, st>>>(p);
@@ -687,8 +693,9 @@ static int launch_top_of(TopArgs p, void* ws, hipStream_t st)
     // Four blocks of 512 on a compute unit hide each other's selection better
     // than two of 1024 (8192 x 131072 bf16: 513 us against 566 for k = 128),
     // until the lists are so long that the threads of one block count (950
-    // against 705 us for k = 500).
-    if (bytes <= 128 * 1024 || p.k <= 256) return launch_top<E, 512>(p, st);
+    // against 705 us for k = 500); with few rows there is one block on a
+    // compute unit anyway (200 x 262144 fp32: 58 against 49 us).
+    if (bytes <= 128 * 1024 || (p.k <= 256 && p.r.T >= 512)) return launch_top<E, 512>(p, st);
     return launch_top<E, 1024>(p, st);
 }
 
