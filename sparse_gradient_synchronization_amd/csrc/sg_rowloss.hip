@@ -154,7 +154,7 @@ struct TokenOp {
     __device__ __forceinline__ RowCoef finish(const Rows& r, uint64_t row, RowStat st, Named za, bool write) const
     {
         if (write && lane_id() == 0) {
-            logp[row] = za == -INFINITY ? -(double)INFINITY : ((double)za - st.m) * r.it - row_log((double)st.s);
+            logp[row] = za == -INFINITY ? -(double)INFINITY : ((double)za - st.m) * r.it - row_log(st.s);
             m[row] = st.m;
             inv[row] = (float)inverse_of(st.s);
             slope[row] = 0.f;
@@ -219,7 +219,7 @@ struct DistillOp {
                                                      const uint32_t* bm, float c) const
     {
         constexpr uint32_t VEC = RowIO<E>::VEC;
-        RowStat st = {-INFINITY, 0.f};
+        RowStat st = {-INFINITY, 0.0};
         for (uint32_t j = lane_id(); j < k; j += SG_WAVE) {
             const uint32_t ch = ls.chunk[j];
             if (ch == ~0u) continue;
@@ -481,7 +481,7 @@ __global__ __launch_bounds__(NT, WAVES) void row_loss_kernel(Rows r, Op op, Grad
         }
     }
     if (!LISTED || t < ND) {
-        RowStat st = {-INFINITY, 0.f};
+        RowStat st = {-INFINITY, 0.0};
         if constexpr (GRAD) stat_chunks<E, J, ND, LISTED>(st, kept, flags, t, sp.nc, r.c);
         stat_more<E, GRAD ? 2 : J, ND, LISTED>(st, xc, flags, rl_bitmap, b0, t, KEPT, sp.nc, r.c);
         stat_loose<E, ND, LISTED>(st, x, sp, rl_bitmap, t, r.c);
@@ -491,7 +491,7 @@ __global__ __launch_bounds__(NT, WAVES) void row_loss_kernel(Rows r, Op op, Grad
     __syncthreads();
     if (own) {
         const uint32_t l = lane_id();
-        const RowStat a = wave_stat(l < NT / SG_WAVE ? part[l] : RowStat{-INFINITY, 0.f}, r.c);
+        const RowStat a = wave_stat(l < NT / SG_WAVE ? part[l] : RowStat{-INFINITY, 0.0}, r.c);
         const RowCoef k = op.finish(r, row, a, nm, true);
         if (l == 0) coef = k;
     }
@@ -565,7 +565,7 @@ __global__ __launch_bounds__(SP_NT, 4) void row_part_kernel(Rows r, Op op, Split
         if (lane_id() == 0) keep[row] = nm;
     }
     if (t < ND) {
-        RowStat st = {-INFINITY, 0.f};
+        RowStat st = {-INFINITY, 0.0};
         stat_more<E, 4, ND, LISTED>(st, x + sp.head, flags, rl_bitmap, sp.head + mark_pad<E>(sp), t, 0, sp.nc, r.c);
         stat_loose<E, ND, LISTED>(st, x, sp, rl_bitmap, t, r.c);
         st = wave_stat(st, r.c);
@@ -573,7 +573,7 @@ __global__ __launch_bounds__(SP_NT, 4) void row_part_kernel(Rows r, Op op, Split
     }
     __syncthreads();
     if (t < SG_WAVE) {
-        const RowStat a = wave_stat(t < SP_NT / SG_WAVE ? part[t] : RowStat{-INFINITY, 0.f}, r.c);
+        const RowStat a = wave_stat(t < SP_NT / SG_WAVE ? part[t] : RowStat{-INFINITY, 0.0}, r.c);
         if (t == 0) s.stat[row * s.parts + blockIdx.x] = a;
     }
 }
@@ -597,7 +597,7 @@ __global__ __launch_bounds__(SP_NT, 4) void row_join_kernel(Rows r, Op op, Split
         return;
     }
     if (t < SG_WAVE) {
-        const RowStat a = wave_stat(t < s.parts ? s.stat[row * s.parts + t] : RowStat{-INFINITY, 0.f}, r.c);
+        const RowStat a = wave_stat(t < s.parts ? s.stat[row * s.parts + t] : RowStat{-INFINITY, 0.0}, r.c);
         const RowCoef k = op.finish(r, row, a, keep[row], blockIdx.x == 0);
         if (t == 0) coef = k;
         if constexpr (GRAD && Op::kListed) // the part's listed logits, before the gradient may overwrite them
@@ -825,8 +825,8 @@ static int rows_args(const void* x, sg_dtype dt, uint64_t T, uint64_t V, uint64_
     out->r.row0 = 0;
     out->r.ld = ld;
     out->r.V = (uint32_t)V;
-    out->r.it = inv_temp;
     out->r.c = (float)(inv_temp * 1.4426950408889634074); // log2(e)
+    out->r.it = out->r.c * kLn2;
     return SG_OK;
 }
 

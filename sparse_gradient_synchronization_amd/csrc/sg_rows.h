@@ -22,7 +22,7 @@ struct Rows {
     uint64_t row0; // first row of this launch
     uint32_t V;
     float c;   // exp(inv_temp * d) = exp2(c * d)
-    double it; // inv_temp
+    double it; // c log 2: inv_temp up to the rounding of c, so that both agree
 };
 
 // the chunks of one row
@@ -49,12 +49,15 @@ __device__ __forceinline__ uint32_t loose_element(const RowSpan& s, uint32_t vec
     return i < s.head ? i : i + s.nc * vec;
 }
 
-// what one pass over (a part of) a row gives: maximum of the raw logits and
-// sum of exp2(c * (x - m)); {-inf, 0} for nothing.  fp32: every thread adds
-// at most a few thousand terms of at most 1, and the threads' sums are joined
-// as a tree, so the relative error stays near 1e-7.
+// What one pass over (a part of) a row gives: maximum of the raw logits and
+// sum of exp2(c * (x - m)); {-inf, 0} for nothing.  The exponentials of a chunk
+// are added in fp32 as a tree, chunks and lanes in fp64: a preference loss adds
+// the log-probabilities of thousands of tokens, and what fp32 sums lose in a
+// row whose largest term dominates is of one sign (1.7e-7 a token).  It costs
+// nothing measurable beside the loads.
 struct RowStat {
-    float m, s;
+    float m;
+    double s;
 };
 
 template <typename E>
@@ -182,31 +185,28 @@ __device__ __forceinline__ void stat_add(RowStat& r, const float* v, float c)
 #pragma unroll
     for (int i = 0; i < N; ++i) m = fmaxf(m, v[i]);
     const float sh = shift_of(m);
-    float s = r.s * exp2_fast((r.m - sh) * c);
+    float e[N];
 #pragma unroll
-    for (int i = 0; i < N; ++i) s += exp2_fast((v[i] - sh) * c);
+    for (int i = 0; i < N; ++i) e[i] = exp2_fast((v[i] - sh) * c);
+#pragma unroll
+    for (int w = N / 2; w > 0; w /= 2)
+#pragma unroll
+        for (int i = 0; i < w; ++i) e[i] += e[i + w];
+    r.s = r.s * (double)exp2_fast((r.m - sh) * c) + (double)e[0];
     r.m = m;
-    r.s = s;
 }
 
-__device__ __forceinline__ RowStat stat_join(RowStat a, RowStat b, float c)
-{
-    const float m = fmaxf(a.m, b.m), sh = shift_of(m);
-    return {m, a.s * exp2_fast((a.m - sh) * c) + b.s * exp2_fast((b.m - sh) * c)};
-}
-
-// the parts of the first N lanes (of every N) joined in a fixed order; every
-// lane holds its result
+// the parts of every N lanes joined in a fixed order; each of them holds the result
 template <int N = SG_WAVE>
 __device__ __forceinline__ RowStat wave_stat(RowStat r, float c)
 {
+    float m = r.m;
 #pragma unroll
-    for (int d = 1; d < N; d <<= 1) {
-        RowStat o = {__shfl_xor(r.m, d, SG_WAVE), __shfl_xor(r.s, d, SG_WAVE)};
-        // the lower lane's part first on both sides, so both hold the same bits
-        r = (lane_id() & d) ? stat_join(o, r, c) : stat_join(r, o, c);
-    }
-    return r;
+    for (int d = 1; d < N; d <<= 1) m = fmaxf(m, __shfl_xor(m, d, SG_WAVE));
+    double s = r.s * (double)exp2_fast((r.m - shift_of(m)) * c);
+#pragma unroll
+    for (int d = 1; d < N; d <<= 1) s += __shfl_xor(s, d, SG_WAVE);
+    return {m, s};
 }
 
 constexpr int next_pow2(int n)

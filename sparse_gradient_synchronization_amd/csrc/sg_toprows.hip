@@ -131,7 +131,7 @@ __global__ __launch_bounds__(SG_WAVE, 6) void top_wave_kernel(TopArgs p)
             w[r] = RowIO<E>::pack(v);
         }
     }
-    RowStat st = {-INFINITY, 0.f};
+    RowStat st = {-INFINITY, 0.0};
     uint32_t top[R]; // upper half of the key of each chunk's maximum
 #pragma unroll
     for (int r = 0; r < R; ++r) {
@@ -147,7 +147,7 @@ __global__ __launch_bounds__(SG_WAVE, 6) void top_wave_kernel(TopArgs p)
         __builtin_amdgcn_sched_barrier(0);
     }
     st = wave_stat(st, p.r.c);
-    const double log_s = row_log((double)st.s);
+    const double log_s = row_log(st.s);
     const float m = shift_of(st.m);
     if (l == 0 && p.lse) p.lse[row] = (float)(m * p.r.it + log_s);
 
@@ -413,7 +413,7 @@ __global__ __launch_bounds__(NT, 8) void top_rows_kernel(TopArgs p)
     const uint32_t nl = (sp.nc + TR_LINE - 1) / TR_LINE;
     const bool lined = nl <= TR_MAX_LINES;
 
-    RowStat st = {-INFINITY, 0.f};
+    RowStat st = {-INFINITY, 0.0};
     const auto take = [&](u32x4 w, uint32_t c) { // chunk c < nl * TR_LINE: whole lines, so that their 8 lanes stay together
         float m = -INFINITY;
         if (c < sp.nc) {
@@ -457,7 +457,7 @@ __global__ __launch_bounds__(NT, 8) void top_rows_kernel(TopArgs p)
         if (PART) {
             p.part_stat[row * p.parts + blockIdx.x] = st;
         } else {
-            sh.log_s = row_log((double)st.s);
+            sh.log_s = row_log(st.s);
             sh.max = shift_of(st.m);
             if (p.lse) p.lse[row] = (float)(sh.max * p.r.it + sh.log_s);
         }
@@ -601,9 +601,9 @@ __global__ __launch_bounds__(TJ_NT, 4) void top_join_kernel(TopArgs p)
     }
     if (t < 4 && n + t < TJ_CAP) ckey[n + t] = 0;
     if (t < SG_WAVE) {
-        const RowStat st = wave_stat(t < p.parts ? p.part_stat[row * p.parts + t] : RowStat{-INFINITY, 0.f}, p.r.c);
+        const RowStat st = wave_stat(t < p.parts ? p.part_stat[row * p.parts + t] : RowStat{-INFINITY, 0.0}, p.r.c);
         if (t == 0) {
-            sh.log_s = row_log((double)st.s);
+            sh.log_s = row_log(st.s);
             sh.max = shift_of(st.m);
             if (p.lse) p.lse[row] = (float)(sh.max * p.r.it + sh.log_s);
         }
