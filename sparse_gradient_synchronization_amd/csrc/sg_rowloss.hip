@@ -71,7 +71,7 @@ struct PolicyOp {
     double lo, hi, kl;
     uint32_t V;
 
-    static constexpr bool kListed = false, kGrad = true;
+    static constexpr bool kListed = false, kGrad = true, kFine = false;
     typedef float Named; // the action's logit
     typedef NoList List;
 
@@ -136,7 +136,7 @@ struct TokenOp {
     float* slope; // cleared here, set by the pair pass for rows of a sequence
     uint32_t V;
 
-    static constexpr bool kListed = false, kGrad = false;
+    static constexpr bool kListed = false, kGrad = false, kFine = true;
     typedef float Named;
     typedef NoList List;
 
@@ -178,7 +178,7 @@ struct DistillOp {
     uint32_t k, V;
     int mode;
 
-    static constexpr bool kListed = true, kGrad = true;
+    static constexpr bool kListed = true, kGrad = true, kFine = false;
     typedef RowList List;
     struct Named {
         double P, A, S; // mass, sum p (log p - (z - m)), sum exp(z - m), z scaled by inv_temp
@@ -216,7 +216,7 @@ struct DistillOp {
     // the other tokens of the marked chunks
     template <typename E>
     __device__ __forceinline__ RowStat marked_chunks(const E* xc, const RowSpan& sp, const RowList& ls,
-                                                     const uint32_t* bm, float c) const
+                                                     const uint32_t* bm, Scale c) const
     {
         constexpr uint32_t VEC = RowIO<E>::VEC;
         RowStat st = {-INFINITY, 0.0};
@@ -300,7 +300,7 @@ struct DistillOp {
     __device__ __forceinline__ void named_grad(const Rows& r, const RowCoef& co, RowList& ls) const
     {
         for (uint32_t j = lane_id(); j < k; j += SG_WAVE)
-            ls.z[j] = co.a * exp2_fast((ls.z[j] - shift_of(co.m)) * r.c) - co.b * ls.p[j];
+            ls.z[j] = co.a * exp2_scaled<false>(ls.z[j] - shift_of(co.m), r.c) - co.b * ls.p[j];
     }
     template <typename E>
     __device__ __forceinline__ void put_named(uint64_t, E* g, const RowCoef&, const RowList& ls, uint32_t lo,
@@ -328,32 +328,32 @@ __device__ __forceinline__ void zero_row(E* g, uint32_t V, uint32_t t, uint32_t 
 }
 
 template <bool PAST, typename E>
-__device__ __forceinline__ void grad_chunk(u32x4 w, E* g, float coef, float sh, float c)
+__device__ __forceinline__ void grad_chunk(u32x4 w, E* g, float coef, float sh, Scale c)
 {
     constexpr int VEC = RowIO<E>::VEC;
     float v[VEC];
     RowIO<E>::unpack(w, v);
 #pragma unroll
-    for (int i = 0; i < VEC; ++i) v[i] = coef * exp2_fast((v[i] - sh) * c);
+    for (int i = 0; i < VEC; ++i) v[i] = coef * exp2_scaled<false>(v[i] - sh, c);
     store_chunk<PAST>(g, RowIO<E>::pack(v));
 }
 
 // the elements outside the chunks
 template <typename E>
-__device__ __forceinline__ void grad_loose(const E* x, E* g, const RowSpan& sp, float coef, float sh, float c,
+__device__ __forceinline__ void grad_loose(const E* x, E* g, const RowSpan& sp, float coef, float sh, Scale c,
                                            uint32_t t, uint32_t nt)
 {
     constexpr int VEC = RowIO<E>::VEC;
 #pragma unroll 1
     for (uint32_t i = loose_element(sp, VEC, t); i < sp.V; i = loose_element(sp, VEC, t += nt))
-        RowIO<E>::put(g + i, coef * exp2_fast((RowIO<E>::get(x + i) - sh) * c));
+        RowIO<E>::put(g + i, coef * exp2_scaled<false>(RowIO<E>::get(x + i) - sh, c));
 }
 
 // gradient of V elements: coef * exp2(c (x - m)).  x and g may be the same
 // memory: every thread reads an element before it writes it, and nobody else
 // touches it.
 template <bool PAST, typename E>
-__device__ __forceinline__ void grad_row(const E* x, E* g, uint32_t V, float coef, float m, float c, uint32_t t,
+__device__ __forceinline__ void grad_row(const E* x, E* g, uint32_t V, float coef, float m, Scale c, uint32_t t,
                                          uint32_t nt)
 {
     const RowSpan sp = span_of<128>(g, V);
@@ -367,17 +367,17 @@ __device__ __forceinline__ void grad_row(const E* x, E* g, uint32_t V, float coe
 // Chunks j0, j0 + ND, ... whose loads are in w.  LISTED: chunks with listed
 // tokens are left out (the list's wave takes them); bit j of `flags` says
 // whether chunk j0 + j * ND is one.
-template <typename E, int J, int ND, bool LISTED>
+template <typename E, int J, int ND, class Op>
 __device__ __forceinline__ void stat_chunks(RowStat& st, const u32x4* w, uint32_t flags, uint32_t j0, uint32_t nc,
-                                            float c)
+                                            Scale c)
 {
     constexpr int VEC = RowIO<E>::VEC;
 #pragma unroll
     for (int j = 0; j < J; ++j) {
-        if (j0 + j * ND < nc && !(LISTED && (flags >> j & 1u))) {
+        if (j0 + j * ND < nc && !(Op::kListed && (flags >> j & 1u))) {
             float v[VEC];
             RowIO<E>::unpack(w[j], v);
-            stat_add<VEC>(st, v, c);
+            stat_add<VEC, Op::kFine>(st, v, c);
         }
         __builtin_amdgcn_sched_barrier(0); // a chunk at a time: unpacked, a chunk takes twice its registers
     }
@@ -386,38 +386,38 @@ __device__ __forceinline__ void stat_chunks(RowStat& st, const u32x4* w, uint32_
 // The chunks from round `first` on (thread t takes chunk t + round * ND), M
 // loads in flight.  Rounds beyond the 32 that the flags hold look the chunk up
 // in the bitmap, b0 the bit of chunk 0.
-template <typename E, int M, int ND, bool LISTED>
+template <typename E, int M, int ND, class Op>
 __device__ __forceinline__ void stat_more(RowStat& st, const E* xc, uint32_t flags, const uint32_t* bm, uint32_t b0,
-                                          uint32_t t, uint32_t first, uint32_t nc, float c)
+                                          uint32_t t, uint32_t first, uint32_t nc, Scale c)
 {
     constexpr int VEC = RowIO<E>::VEC;
     uint32_t round = first;
     u32x4 more[M];
 #pragma unroll 1
-    for (; (round + M) * ND <= nc && (!LISTED || round + M <= 32); round += M) { // the whole block has chunks in these rounds
+    for (; (round + M) * ND <= nc && (!Op::kListed || round + M <= 32); round += M) { // the whole block has chunks in these rounds
 #pragma unroll
         for (int j = 0; j < M; ++j) more[j] = load_chunk(chunk_at<E>(xc, (round + j) * ND, t));
-        stat_chunks<E, M, ND, LISTED>(st, more, flags >> round, t + round * ND, nc, c);
+        stat_chunks<E, M, ND, Op>(st, more, flags >> round, t + round * ND, nc, c);
     }
 #pragma unroll 1
     for (; t + round * ND < nc; ++round) {
         more[0] = load_chunk(chunk_at<E>(xc, round * ND, t));
         uint32_t f = 0;
-        if (LISTED) f = round < 32 ? flags >> round : (marked(bm, b0 + (t + round * ND) * VEC, VEC) ? 1u : 0u);
-        stat_chunks<E, 1, ND, LISTED>(st, more, f, t + round * ND, nc, c);
+        if (Op::kListed) f = round < 32 ? flags >> round : (marked(bm, b0 + (t + round * ND) * VEC, VEC) ? 1u : 0u);
+        stat_chunks<E, 1, ND, Op>(st, more, f, t + round * ND, nc, c);
     }
 }
 
-template <typename E, int ND, bool LISTED>
+template <typename E, int ND, class Op>
 __device__ __forceinline__ void stat_loose(RowStat& st, const E* x, const RowSpan& sp, const uint32_t* bm, uint32_t t,
-                                           float c)
+                                           Scale c)
 {
     constexpr int VEC = RowIO<E>::VEC;
 #pragma unroll 1
     for (uint32_t i = loose_element(sp, VEC, t); i < sp.V; i = loose_element(sp, VEC, t += ND)) {
         float v = RowIO<E>::get(x + i);
-        if (LISTED && marked(bm, i + mark_pad<E>(sp), 1)) v = -INFINITY;
-        stat_add<1>(st, &v, c);
+        if (Op::kListed && marked(bm, i + mark_pad<E>(sp), 1)) v = -INFINITY;
+        stat_add<1, Op::kFine>(st, &v, c);
     }
 }
 
@@ -482,16 +482,16 @@ __global__ __launch_bounds__(NT, WAVES) void row_loss_kernel(Rows r, Op op, Grad
     }
     if (!LISTED || t < ND) {
         RowStat st = {-INFINITY, 0.0};
-        if constexpr (GRAD) stat_chunks<E, J, ND, LISTED>(st, kept, flags, t, sp.nc, r.c);
-        stat_more<E, GRAD ? 2 : J, ND, LISTED>(st, xc, flags, rl_bitmap, b0, t, KEPT, sp.nc, r.c);
-        stat_loose<E, ND, LISTED>(st, x, sp, rl_bitmap, t, r.c);
-        st = wave_stat(st, r.c);
+        if constexpr (GRAD) stat_chunks<E, J, ND, Op>(st, kept, flags, t, sp.nc, r.c);
+        stat_more<E, GRAD ? 2 : J, ND, Op>(st, xc, flags, rl_bitmap, b0, t, KEPT, sp.nc, r.c);
+        stat_loose<E, ND, Op>(st, x, sp, rl_bitmap, t, r.c);
+        st = wave_stat<SG_WAVE, Op::kFine>(st, r.c);
         if (lane_id() == 0) part[t / SG_WAVE] = st;
     }
     __syncthreads();
     if (own) {
         const uint32_t l = lane_id();
-        const RowStat a = wave_stat(l < NT / SG_WAVE ? part[l] : RowStat{-INFINITY, 0.0}, r.c);
+        const RowStat a = wave_stat<SG_WAVE, Op::kFine>(l < NT / SG_WAVE ? part[l] : RowStat{-INFINITY, 0.0}, r.c);
         const RowCoef k = op.finish(r, row, a, nm, true);
         if (l == 0) coef = k;
     }
@@ -566,14 +566,14 @@ __global__ __launch_bounds__(SP_NT, 4) void row_part_kernel(Rows r, Op op, Split
     }
     if (t < ND) {
         RowStat st = {-INFINITY, 0.0};
-        stat_more<E, 4, ND, LISTED>(st, x + sp.head, flags, rl_bitmap, sp.head + mark_pad<E>(sp), t, 0, sp.nc, r.c);
-        stat_loose<E, ND, LISTED>(st, x, sp, rl_bitmap, t, r.c);
-        st = wave_stat(st, r.c);
+        stat_more<E, 4, ND, Op>(st, x + sp.head, flags, rl_bitmap, sp.head + mark_pad<E>(sp), t, 0, sp.nc, r.c);
+        stat_loose<E, ND, Op>(st, x, sp, rl_bitmap, t, r.c);
+        st = wave_stat<SG_WAVE, Op::kFine>(st, r.c);
         if (lane_id() == 0) part[t / SG_WAVE] = st;
     }
     __syncthreads();
     if (t < SG_WAVE) {
-        const RowStat a = wave_stat(t < SP_NT / SG_WAVE ? part[t] : RowStat{-INFINITY, 0.0}, r.c);
+        const RowStat a = wave_stat<SG_WAVE, Op::kFine>(t < SP_NT / SG_WAVE ? part[t] : RowStat{-INFINITY, 0.0}, r.c);
         if (t == 0) s.stat[row * s.parts + blockIdx.x] = a;
     }
 }
@@ -597,7 +597,7 @@ __global__ __launch_bounds__(SP_NT, 4) void row_join_kernel(Rows r, Op op, Split
         return;
     }
     if (t < SG_WAVE) {
-        const RowStat a = wave_stat(t < s.parts ? s.stat[row * s.parts + t] : RowStat{-INFINITY, 0.0}, r.c);
+        const RowStat a = wave_stat<SG_WAVE, Op::kFine>(t < s.parts ? s.stat[row * s.parts + t] : RowStat{-INFINITY, 0.0}, r.c);
         const RowCoef k = op.finish(r, row, a, keep[row], blockIdx.x == 0);
         if (t == 0) coef = k;
         if constexpr (GRAD && Op::kListed) // the part's listed logits, before the gradient may overwrite them
@@ -814,7 +814,8 @@ struct RowCheck {
 static uint64_t row_esize(sg_dtype dt) { return dt == SG_BF16 ? 2 : 4; }
 
 // the checks every rows call shares
-static int rows_args(const void* x, sg_dtype dt, uint64_t T, uint64_t V, uint64_t ld, double inv_temp, RowCheck* out)
+static int rows_args(const void* x, sg_dtype dt, uint64_t T, uint64_t V, uint64_t ld, double inv_temp, RowCheck* out,
+                     bool fine = false)
 {
     if (dt != SG_F32 && dt != SG_BF16) return SG_EINVAL;
     if (V == 0 || V >= (1ull << 31) || T >= (1ull << 31) || ld < V || ld >= (1ull << 40)) return SG_EINVAL;
@@ -825,8 +826,15 @@ static int rows_args(const void* x, sg_dtype dt, uint64_t T, uint64_t V, uint64_
     out->r.row0 = 0;
     out->r.ld = ld;
     out->r.V = (uint32_t)V;
-    out->r.c = (float)(inv_temp * 1.4426950408889634074); // log2(e)
-    out->r.it = out->r.c * kLn2;
+    const double c = inv_temp * 1.4426950408889634074; // log2(e)
+    out->r.c.hi = (float)c;
+    out->r.c.lo = 0.f;
+    out->r.it = out->r.c.hi * kLn2;
+    if (fine) {
+        if (out->r.c.hi >= c) out->r.c.hi = nextafterf(out->r.c.hi, 0.0f);
+        out->r.c.lo = (float)(c - out->r.c.hi);
+        out->r.it = inv_temp;
+    }
     return SG_OK;
 }
 
@@ -1072,7 +1080,7 @@ extern "C" int sg_preference_loss(const void* d_logits, sg_dtype dt, uint64_t T,
                                   uint64_t ld_grad, void* d_ws, size_t ws_bytes, void* stream)
 {
     RowCheck c;
-    int rc = rows_args(d_logits, dt, T, V, ld, 1.0, &c);
+    int rc = rows_args(d_logits, dt, T, V, ld, 1.0, &c, TokenOp::kFine);
     if (rc) return rc;
     if (kind != SG_PREF_SIGMOID && kind != SG_PREF_HINGE && kind != SG_PREF_IPO) return SG_EINVAL;
     if (!(beta > 0.0) || !(beta <= 1e6) || !(smoothing >= 0.0) || !(smoothing < 0.5)) return SG_EINVAL;

@@ -16,13 +16,24 @@ namespace sg {
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x4_at2 __attribute__((ext_vector_type(4), aligned(2))); // anywhere an element may be
 
+// log2(e) * inv_temp in fp32, and the rest of it.  With the first alone every
+// log-probability of a batch is off by the same small share (1.3e-8 at
+// temperature 1) of its distance from the row's mean.  That is lost in the
+// rounding of a result per token, and there the row's scalars take the
+// temperature that hi stands for; but the preference loss adds thousands of
+// them and takes differences (an IPO loss of 12000 tokens was 3e-4 off), so
+// its sums are FINE and use both parts, an fma more a term.
+struct Scale {
+    float hi, lo; // FINE: lo > 0, so that -inf times it stays -inf
+};
+
 struct Rows {
     const void* x; // [T] rows, ld elements apart
     uint64_t T, ld;
     uint64_t row0; // first row of this launch
     uint32_t V;
-    float c;   // exp(inv_temp * d) = exp2(c * d)
-    double it; // c log 2: inv_temp up to the rounding of c, so that both agree
+    Scale c;   // exp(inv_temp * d) = exp2(c * d)
+    double it; // inv_temp; not FINE: that of c.hi
 };
 
 // the chunks of one row
@@ -171,6 +182,13 @@ __device__ __forceinline__ void load_chunks(u32x4* w, const E* x, uint32_t j0, u
 }
 
 __device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
+// exp2(c * d), d <= 0; -inf gives 0.  The small product goes first: added to
+// a rounded d * hi it would be rounded away.
+template <bool FINE>
+__device__ __forceinline__ float exp2_scaled(float d, Scale c)
+{
+    return exp2_fast(FINE ? fmaf(d, c.hi, d * c.lo) : d * c.hi);
+}
 
 // the maximum as it is subtracted: a row (or part) of nothing but -inf has
 // exp(-inf - 0) = 0 terms, not exp(-inf + inf)
@@ -178,8 +196,8 @@ __device__ __forceinline__ float shift_of(float m) { return m == -INFINITY ? 0.f
 
 // Adds N values to a running (maximum, sum).  A NaN among them, or a +inf,
 // makes the sum NaN; -inf adds nothing.
-template <int N>
-__device__ __forceinline__ void stat_add(RowStat& r, const float* v, float c)
+template <int N, bool FINE = false>
+__device__ __forceinline__ void stat_add(RowStat& r, const float* v, Scale c)
 {
     float m = r.m;
 #pragma unroll
@@ -187,23 +205,23 @@ __device__ __forceinline__ void stat_add(RowStat& r, const float* v, float c)
     const float sh = shift_of(m);
     float e[N];
 #pragma unroll
-    for (int i = 0; i < N; ++i) e[i] = exp2_fast((v[i] - sh) * c);
+    for (int i = 0; i < N; ++i) e[i] = exp2_scaled<FINE>(v[i] - sh, c);
 #pragma unroll
     for (int w = N / 2; w > 0; w /= 2)
 #pragma unroll
         for (int i = 0; i < w; ++i) e[i] += e[i + w];
-    r.s = r.s * (double)exp2_fast((r.m - sh) * c) + (double)e[0];
+    r.s = r.s * (double)exp2_scaled<FINE>(r.m - sh, c) + (double)e[0];
     r.m = m;
 }
 
 // the parts of every N lanes joined in a fixed order; each of them holds the result
-template <int N = SG_WAVE>
-__device__ __forceinline__ RowStat wave_stat(RowStat r, float c)
+template <int N = SG_WAVE, bool FINE = false>
+__device__ __forceinline__ RowStat wave_stat(RowStat r, Scale c)
 {
     float m = r.m;
 #pragma unroll
     for (int d = 1; d < N; d <<= 1) m = fmaxf(m, __shfl_xor(m, d, SG_WAVE));
-    double s = r.s * (double)exp2_fast((r.m - shift_of(m)) * c);
+    double s = r.s * (double)exp2_scaled<FINE>(r.m - shift_of(m), c);
 #pragma unroll
     for (int d = 1; d < N; d <<= 1) s += __shfl_xor(s, d, SG_WAVE);
     return {m, s};
