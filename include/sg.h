@@ -539,8 +539,8 @@ int sg_stats_collect(const void* h_block, uint32_t n, uint64_t M, uint64_t total
  *            Elements between V and ld_grad are left untouched.
  *   d_ws     of at least the size the call's *_workspace_bytes returns; it
  *            may be NULL where that is 0.
- * Sums, row scalars: fp32 terms of at most 1 per lane, joined in fp32, the
- * row's scalars in fp64.  Results do not depend on timing (no float atomics).
+ * Sums: fp32 exponentials, 4 or 8 added in fp32, the rest and the row's
+ * scalars in fp64.  Results do not depend on timing (no float atomics).
  * Limits: T < 2^31, 1 <= V < 2^31, ld and ld_grad < 2^40, 0 < inv_temp <= 1e6.
  * T = 0 is a no-op.
  * ------------------------------------------------------------------------ */

@@ -533,11 +533,12 @@ def test_split_rows_beyond_a_grid_dimension():
     assert not loss[:-3].any()
 
 
-def test_on_another_stream_and_in_a_graph():
+@pytest.mark.parametrize("V", [33000, 140001])
+def test_on_another_stream_and_in_a_graph(V):
     """Queued on a side stream; captured once and replayed with new inputs,
-    eager work between the replays."""
+    eager work between the replays.  The longer rows are split."""
     need_gpu()
-    T, V, k = 12, 33000, 16
+    T, k = 12, 16
     x, _ = make_logits(80, T, V, "bf16")
     idx, logp = make_lists(81, T, V, k)
     idx, logp = dev(idx, torch.int32), dev(logp, torch.float32)
@@ -581,6 +582,27 @@ def test_results_repeat():
         for _ in range(3):
             again = sg.sg_distill_loss(x, idx, logp)
             assert all(torch.equal(p, q) for p, q in zip(first, again))
+
+
+def test_long_sequences_keep_their_differences():
+    """One pair of thousands of tokens: the sequences' sums are differences of
+    thousands, so what every token is off by must not be of one sign."""
+    need_gpu()
+    T, V = 6000, 1500
+    x, xs = make_logits(97, T, V, "f32")
+    label = np.random.default_rng(98).integers(0, V, T)
+    off = np.array([0, 1000, T])
+    lq = np.array([ref.log_softmax(xs[t], 1.0)[0][label[t]] for t in range(T)])
+    S = np.array([lq[:1000].sum(), lq[1000:].sum()])
+    rf = (S - np.array([3.0, -2.0])).astype(np.float32)
+    loss, got, g = sg.sg_preference_loss(x, dev(label, torch.int32), dev(off, torch.int64),
+                                         ref_logp=dev(rf, torch.float32), kind=sg.SG_PREF_IPO, beta=0.1)
+    d = (S[0] - float(rf[0])) - (S[1] - float(rf[1]))
+    want = (d - 5.0) ** 2
+    # a token's log-probability is off by a random 1e-7 (an exponential's 2^-23, one sign or the other) and by 1e-8
+    # of one sign: 8e-6 + 6e-5 for 6000 of them, and the loss moves by 2 |d - 5| times that
+    off_by = np.sqrt(T) * 1e-7 + T * 1e-8
+    assert abs(float(loss[0]) - want) <= 2 * abs(d - 5.0) * off_by + off_by ** 2 + 2.0 ** -24 * want
 
 
 # ---------------------------------------------------------------------------

@@ -95,6 +95,20 @@ def test_orders_and_ties(V, T, kind):
 
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("T", [2, 130])
+def test_long_lists_of_the_longest_lined_rows(T, dtype):
+    """The most line maxima and the most candidates at once (66 KB of LDS), in parts and in one block."""
+    need_gpu()
+    V = 262144 if dtype == "f32" else 524288
+    x = torch.randn((T, V), device="cuda").to(TDT[dtype])
+    idx, logp, lse = sg.sg_topk_rows(x, 1000)
+    for t in (0, T - 1):
+        ri, rp, rl = ref.topk_rows(host(x[t:t + 1]), 1000, 1.0)
+        assert np.array_equal(idx[t:t + 1].cpu().numpy(), ri)
+        check(host(logp)[t:t + 1], rp, ref.sum_error(V) + 2.0 ** -24 * np.abs(rp), "logp")
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
 def test_strided_rows(dtype):
     need_gpu()
     for V, ld, shift in ((1001, 1009, 1), (70001, 70004, 3)):
