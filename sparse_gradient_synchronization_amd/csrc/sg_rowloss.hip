@@ -32,13 +32,18 @@ struct GradOut {
     bool past;
 };
 
-// What an operator with a list keeps of it in LDS.
+// What an operator with a list keeps of it, in dynamic LDS of the list's size:
+// room for the longest list (20 KiB) left 7 blocks of short rows on a compute
+// unit, where the registers allow 12.
 struct RowList {
-    float z[RL_MAX_K], p[RL_MAX_K]; // logits, masses
-    uint32_t id[RL_MAX_K], chunk[RL_MAX_K]; // tokens; the chunks that the list's wave adds
-    uint32_t flag[1024]; // bit r of flag[t]: the chunk that data thread t takes in round r has listed tokens
+    float *z, *p;         // [k] logits, masses
+    uint32_t *id, *chunk; // [k] tokens; the chunks that the list's wave adds
+    uint32_t* flag;       // [threads] bit r: the chunk that data thread t takes in round r has listed tokens
+    uint32_t* bitmap;     // of the row or part
 };
-struct NoList {};
+struct NoList {
+    uint32_t* bitmap;
+};
 
 // An element's bit of the bitmap is its place plus this, so that the bits of
 // a chunk start at a multiple of the chunk's size.
@@ -74,6 +79,7 @@ struct PolicyOp {
     static constexpr bool kListed = false, kGrad = true, kFine = false;
     typedef float Named; // the action's logit
     typedef NoList List;
+    __device__ __forceinline__ NoList list(uint32_t*, uint32_t) const { return {nullptr}; }
 
     __device__ __forceinline__ bool live(uint64_t row) const
     {
@@ -139,6 +145,7 @@ struct TokenOp {
     static constexpr bool kListed = false, kGrad = false, kFine = true;
     typedef float Named;
     typedef NoList List;
+    __device__ __forceinline__ NoList list(uint32_t*, uint32_t) const { return {nullptr}; }
 
     __device__ __forceinline__ bool live(uint64_t row) const { return (uint32_t)label[row] < V; }
     __device__ __forceinline__ void skip(uint64_t row) const
@@ -180,6 +187,19 @@ struct DistillOp {
 
     static constexpr bool kListed = true, kGrad = true, kFine = false;
     typedef RowList List;
+
+    static __host__ __device__ constexpr uint32_t list_words(uint32_t k, uint32_t threads) { return 4 * k + threads; }
+    __device__ __forceinline__ RowList list(uint32_t* lds, uint32_t threads) const
+    {
+        RowList ls;
+        ls.z = reinterpret_cast<float*>(lds);
+        ls.p = ls.z + k;
+        ls.id = lds + 2 * k;
+        ls.chunk = lds + 3 * k;
+        ls.flag = lds + 4 * k;
+        ls.bitmap = ls.flag + threads;
+        return ls;
+    }
     struct Named {
         double P, A, S; // mass, sum p (log p - (z - m)), sum exp(z - m), z scaled by inv_temp
         float m;        // maximum of the listed logits
@@ -439,8 +459,9 @@ __global__ __launch_bounds__(NT, WAVES) void row_loss_kernel(Rows r, Op op, Grad
     constexpr bool LISTED = Op::kListed;
     constexpr int ND = LISTED ? NT - SG_WAVE : NT, NW = ND / SG_WAVE; // data threads
     constexpr int VEC = RowIO<E>::VEC;
-    extern __shared__ uint32_t rl_bitmap[];
-    __shared__ typename Op::List ls;
+    extern __shared__ uint32_t rl_lds[];
+    typename Op::List ls = op.list(rl_lds, ND);
+    uint32_t* const rl_bitmap = ls.bitmap;
     __shared__ RowStat part[NT / SG_WAVE];
     __shared__ RowCoef coef;
     const uint32_t t = threadIdx.x;
@@ -534,8 +555,9 @@ __global__ __launch_bounds__(SP_NT, 4) void row_part_kernel(Rows r, Op op, Split
 {
     constexpr bool LISTED = Op::kListed;
     constexpr int ND = LISTED ? SP_NT - SG_WAVE : SP_NT, NW = ND / SG_WAVE, VEC = RowIO<E>::VEC;
-    extern __shared__ uint32_t rl_bitmap[];
-    __shared__ typename Op::List ls;
+    extern __shared__ uint32_t rl_lds[];
+    typename Op::List ls = op.list(rl_lds, ND);
+    uint32_t* const rl_bitmap = ls.bitmap;
     __shared__ RowStat part[SP_NT / SG_WAVE];
     const uint32_t t = threadIdx.x, lo = blockIdx.x * s.len;
     const uint64_t row = r.row0 + blockIdx.y;
@@ -584,7 +606,8 @@ template <typename E, class Op, bool GRAD>
 __global__ __launch_bounds__(SP_NT, 4) void row_join_kernel(Rows r, Op op, SplitArgs s, const typename Op::Named* keep,
                                                             GradOut out)
 {
-    __shared__ typename Op::List ls;
+    extern __shared__ uint32_t rl_lds[];
+    typename Op::List ls = op.list(rl_lds, 0);
     __shared__ RowCoef coef;
     const uint32_t t = threadIdx.x;
     const uint64_t row = r.row0 + blockIdx.y;
@@ -633,7 +656,7 @@ struct PairArgs {
     double beta, eps;
 };
 
-constexpr int PF_NT = 256;
+constexpr int PF_NT = 256, PF_PAIR_NT = 1024;
 
 struct PairTerm {
     uint64_t lo[2], hi[2]; // the rows of both sequences
@@ -659,6 +682,7 @@ __device__ __forceinline__ PairTerm pair_term(const PairArgs& p, uint32_t b, boo
         if (report && (o1 > p.T || o0 > o1) && threadIdx.x == 0) report_error(kDevErrBadOffsets);
         if (q.hi[c] < q.lo[c]) q.hi[c] = q.lo[c];
         double a = 0.0, k = 0.0;
+#pragma unroll 4
         for (uint64_t t = q.lo[c] + threadIdx.x; t < q.hi[c]; t += NT) {
             a += p.row_logp[t]; // 0 where the label does not count
             k += (uint32_t)p.label[t] < p.V ? 1.0 : 0.0;
@@ -724,15 +748,15 @@ __device__ __forceinline__ void put_pair(const PairArgs& p, uint32_t b, const Pa
 }
 
 // one block per pair: its loss, and the slope of every row of its sequences
-__global__ __launch_bounds__(PF_NT) void pref_pair_kernel(PairArgs p)
+__global__ __launch_bounds__(PF_PAIR_NT) void pref_pair_kernel(PairArgs p)
 {
     for (uint32_t b = blockIdx.x; b < p.pairs; b += gridDim.x) {
-        const PairTerm q = pair_term<PF_NT>(p, b, true);
+        const PairTerm q = pair_term<PF_PAIR_NT>(p, b, true);
         if (threadIdx.x == 0) put_pair(p, b, q);
         if (p.grad)
 #pragma unroll
             for (int c = 0; c < 2; ++c)
-                for (uint64_t t = q.lo[c] + threadIdx.x; t < q.hi[c]; t += PF_NT)
+                for (uint64_t t = q.lo[c] + threadIdx.x; t < q.hi[c]; t += PF_PAIR_NT)
                     p.slope[t] = (uint32_t)p.label[t] < p.V ? (float)q.each[c] : 0.f;
         __syncthreads();
     }
@@ -740,32 +764,32 @@ __global__ __launch_bounds__(PF_NT) void pref_pair_kernel(PairArgs p)
 
 // gradient rows from the kept maximum and 1/sum: slope * (1[i = y] - q_i).
 // gridDim.x parts of len elements to a row.
-template <typename E, bool PAST>
+template <typename E, bool PAST, int NT>
 __device__ __forceinline__ void pref_grad_part(const Rows& r, const TokenOp& op, uint64_t row, uint32_t lo, uint32_t n,
                                                float slope, const GradOut& out)
 {
     const E* x = static_cast<const E*>(r.x) + row * r.ld + lo;
     E* g = static_cast<E*>(out.g) + row * out.ld + lo;
     if (slope == 0.f) {
-        zero_row<PAST>(g, n, threadIdx.x, PF_NT);
+        zero_row<PAST>(g, n, threadIdx.x, NT);
         return;
     }
-    grad_row<PAST>(x, g, n, -slope * op.inv[row], op.m[row], r.c, threadIdx.x, PF_NT);
+    grad_row<PAST>(x, g, n, -slope * op.inv[row], op.m[row], r.c, threadIdx.x, NT);
     __syncthreads();
     const uint32_t y = (uint32_t)op.label[row];
     if (threadIdx.x == 0 && y >= lo && y < lo + n)
         RowIO<E>::put(g + (y - lo), (float)((double)slope * -row_expm1(op.logp[row])));
 }
 
-template <typename E, bool PAST>
-__global__ __launch_bounds__(PF_NT) void pref_grad_kernel(Rows r, TokenOp op, uint32_t len, GradOut out)
+template <typename E, bool PAST, int NT>
+__global__ __launch_bounds__(NT) void pref_grad_kernel(Rows r, TokenOp op, uint32_t len, GradOut out)
 {
     const uint32_t lo = blockIdx.x * len, n = r.V - lo < len ? r.V - lo : len;
     // last row first: the token pass has just read the last rows, which are
     // still in the last-level cache (6000 x 131072 bf16: 731 -> 706 us)
     for (uint64_t y = blockIdx.y; y < r.T; y += gridDim.y) {
         const uint64_t row = r.T - 1 - y;
-        pref_grad_part<E, PAST>(r, op, row, lo, n, op.slope[row], out);
+        pref_grad_part<E, PAST, NT>(r, op, row, lo, n, op.slope[row], out);
     }
 }
 
@@ -798,7 +822,7 @@ __global__ __launch_bounds__(PF_NT) void pref_both_kernel(Rows r, TokenOp op, Pa
         const PairTerm q = pair_term<PF_NT>(p, chosen ? s : s - p.pairs, false);
         slope = (float)(chosen ? q.each[0] : q.each[1]);
     }
-    pref_grad_part<E, false>(r, op, row, lo, n, slope, out);
+    pref_grad_part<E, false, PF_NT>(r, op, row, lo, n, slope, out);
 }
 
 // ---------------------------------------------------------------------------
@@ -916,9 +940,18 @@ static size_t split_bytes(uint64_t T, uint64_t V, sg_dtype dt)
     return parts > 1 ? cv.bytes() : 0;
 }
 
-template <typename E, int NT, int J, int WAVES, class Op>
-static int launch_rows(const RowCheck& c, const Op& op, size_t lds, const GradOut& out, hipStream_t st)
+// dynamic LDS of a kernel whose blocks take V elements: the list and its bitmap
+template <class Op>
+static size_t list_lds(const Op& op, uint32_t threads, uint64_t V)
 {
+    if constexpr (Op::kListed) return 4 * (Op::list_words(op.k, threads) + (V > 0 ? ceil_div(V + 8, 32) : 0));
+    return 0;
+}
+
+template <typename E, int NT, int J, int WAVES, class Op>
+static int launch_rows(const RowCheck& c, const Op& op, const GradOut& out, hipStream_t st)
+{
+    const size_t lds = list_lds(op, NT - SG_WAVE, c.r.V);
     Rows r = c.r;
     for (r.row0 = 0; r.row0 < r.T; r.row0 += ROWS_PER_LAUNCH) {
         const uint64_t left = r.T - r.row0;
@@ -941,7 +974,7 @@ static int launch_split(const RowCheck& c, const Op& op, uint32_t parts, const G
     const SplitWs<Op> w = split_carve<Op>(cv, c.r.T, parts);
     SplitArgs s = {w.stat, parts, 0};
     s.len = part_len(c.r.V, &s.parts);
-    const size_t lds = Op::kListed ? ceil_div(s.len + 8, 32) * 4 : 0;
+    const size_t lds = list_lds(op, SP_NT - SG_WAVE, s.len), lds_join = list_lds(op, 0, 0);
     Rows r = c.r;
     typename Op::Named* keep = w.keep;
     for (r.row0 = 0; r.row0 < c.r.T; r.row0 += GRID_Y) {
@@ -949,7 +982,7 @@ static int launch_split(const RowCheck& c, const Op& op, uint32_t parts, const G
         row_part_kernel<E, Op><<<dim3(s.parts, rows), SP_NT, lds, st>>>(r, op, s, keep);
         SG_TRY_LAUNCH();
         if constexpr (Op::kGrad)
-            if (out.g) row_join_kernel<E, Op, true><<<dim3(s.parts, rows), SP_NT, 0, st>>>(r, op, s, keep, out);
+            if (out.g) row_join_kernel<E, Op, true><<<dim3(s.parts, rows), SP_NT, lds_join, st>>>(r, op, s, keep, out);
         if (!out.g) row_join_kernel<E, Op, false><<<dim3(1, rows), SG_WAVE, 0, st>>>(r, op, s, keep, out);
         SG_TRY_LAUNCH();
     }
@@ -968,13 +1001,12 @@ static int launch_row_loss_of(const RowCheck& c, const Op& op, const GradOut& ou
     const uint32_t parts = op_parts<Op>(c.r.T, c.r.V, dt);
     if (parts > 1) return launch_split<E>(c, op, parts, out, ws, st);
     const uint64_t bytes = (uint64_t)c.r.V * sizeof(E);
-    const size_t lds = Op::kListed ? ceil_div((uint64_t)c.r.V + 8, 32) * 4 : 0;
     constexpr bool L = Op::kListed; // one wave less for the row
-    if (bytes <= 4 * 1024) return launch_rows<E, L ? 128 : 64, 4, L ? 6 : 8>(c, op, lds, out, st);
-    if (bytes <= 16 * 1024) return launch_rows<E, 256, L ? 6 : 4, L ? 6 : 8>(c, op, lds, out, st);
-    if (bytes <= 64 * 1024) return launch_rows<E, 512, L ? 9 : 8, L ? 4 : 8>(c, op, lds, out, st);
-    if (bytes <= 128 * 1024) return launch_rows<E, 512, L ? 18 : 16, 4>(c, op, lds, out, st);
-    return launch_rows<E, 1024, L ? 17 : 16, 4>(c, op, lds, out, st);
+    if (bytes <= 4 * 1024) return launch_rows<E, L ? 128 : 64, 4, L ? 6 : 8>(c, op, out, st);
+    if (bytes <= 16 * 1024) return launch_rows<E, 256, L ? 6 : 4, L ? 6 : 8>(c, op, out, st);
+    if (bytes <= 64 * 1024) return launch_rows<E, 512, L ? 9 : 8, L ? 4 : 8>(c, op, out, st);
+    if (bytes <= 128 * 1024) return launch_rows<E, 512, L ? 18 : 16, 4>(c, op, out, st);
+    return launch_rows<E, 1024, L ? 17 : 16, 4>(c, op, out, st);
 }
 
 template <class Op>
@@ -1114,15 +1146,20 @@ extern "C" int sg_preference_loss(const void* d_logits, sg_dtype dt, uint64_t T,
         return SG_OK;
     }
     if (pairs > 0) {
-        pref_pair_kernel<<<pairs < 65536u ? pairs : 65536u, PF_NT, 0, st>>>(p);
+        pref_pair_kernel<<<pairs < 65536u ? pairs : 65536u, PF_PAIR_NT, 0, st>>>(p);
         SG_TRY_LAUNCH();
     }
     if (T > 0 && d_grad) {
         const dim3 grid(parts, (unsigned)(T < GRID_Y ? T : GRID_Y));
-        if (dt == SG_BF16 && out.past) pref_grad_kernel<bf16_bits, true><<<grid, PF_NT, 0, st>>>(c.r, op, len, out);
-        else if (dt == SG_BF16) pref_grad_kernel<bf16_bits, false><<<grid, PF_NT, 0, st>>>(c.r, op, len, out);
-        else if (out.past) pref_grad_kernel<float, true><<<grid, PF_NT, 0, st>>>(c.r, op, len, out);
-        else pref_grad_kernel<float, false><<<grid, PF_NT, 0, st>>>(c.r, op, len, out);
+        const bool narrow = V * row_esize(dt) <= 4 * 1024; // a wave a row
+        const auto go = [&](auto e) {
+            typedef decltype(e) E;
+            if (out.past) pref_grad_kernel<E, true, PF_NT><<<grid, PF_NT, 0, st>>>(c.r, op, len, out);
+            else if (narrow) pref_grad_kernel<E, false, SG_WAVE><<<grid, SG_WAVE, 0, st>>>(c.r, op, len, out);
+            else pref_grad_kernel<E, false, PF_NT><<<grid, PF_NT, 0, st>>>(c.r, op, len, out);
+        };
+        if (dt == SG_BF16) go(bf16_bits());
+        else go(float());
         SG_TRY_LAUNCH();
     }
     return SG_OK;
