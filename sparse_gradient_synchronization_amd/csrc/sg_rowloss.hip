@@ -656,7 +656,7 @@ struct PairArgs {
     double beta, eps;
 };
 
-constexpr int PF_NT = 256, PF_PAIR_NT = 1024;
+constexpr int PF_NT = 256;
 
 struct PairTerm {
     uint64_t lo[2], hi[2]; // the rows of both sequences
@@ -748,15 +748,16 @@ __device__ __forceinline__ void put_pair(const PairArgs& p, uint32_t b, const Pa
 }
 
 // one block per pair: its loss, and the slope of every row of its sequences
-__global__ __launch_bounds__(PF_PAIR_NT) void pref_pair_kernel(PairArgs p)
+template <int NT>
+__global__ __launch_bounds__(NT) void pref_pair_kernel(PairArgs p)
 {
     for (uint32_t b = blockIdx.x; b < p.pairs; b += gridDim.x) {
-        const PairTerm q = pair_term<PF_PAIR_NT>(p, b, true);
+        const PairTerm q = pair_term<NT>(p, b, true);
         if (threadIdx.x == 0) put_pair(p, b, q);
         if (p.grad)
 #pragma unroll
             for (int c = 0; c < 2; ++c)
-                for (uint64_t t = q.lo[c] + threadIdx.x; t < q.hi[c]; t += PF_PAIR_NT)
+                for (uint64_t t = q.lo[c] + threadIdx.x; t < q.hi[c]; t += NT)
                     p.slope[t] = (uint32_t)p.label[t] < p.V ? (float)q.each[c] : 0.f;
         __syncthreads();
     }
@@ -1149,7 +1150,10 @@ extern "C" int sg_preference_loss(const void* d_logits, sg_dtype dt, uint64_t T,
         return SG_OK;
     }
     if (pairs > 0) {
-        pref_pair_kernel<<<pairs < 65536u ? pairs : 65536u, PF_PAIR_NT, 0, st>>>(p);
+        const unsigned blocks = pairs < 65536u ? pairs : 65536u;
+        // long sequences: more loads in flight; short ones: fewer waves to join (2 us of 83 for 24 pairs of 5000 rows)
+        if (T / pairs > 2048) pref_pair_kernel<1024><<<blocks, 1024, 0, st>>>(p);
+        else pref_pair_kernel<PF_NT><<<blocks, PF_NT, 0, st>>>(p);
         SG_TRY_LAUNCH();
     }
     if (T > 0 && d_grad) {
