@@ -695,6 +695,7 @@ static int launch_top_of(TopArgs p, void* ws, hipStream_t st)
     // until the lists are so long that the threads of one block count (950
     // against 705 us for k = 500); with few rows there is one block on a
     // compute unit anyway (200 x 262144 fp32: 58 against 49 us).
+    if (bytes <= 32 * 1024 && p.k <= 256) return launch_top<E, 256>(p, st);
     if (bytes <= 128 * 1024 || (p.k <= 256 && p.r.T >= 512)) return launch_top<E, 512>(p, st);
     return launch_top<E, 1024>(p, st);
 }
