@@ -25,7 +25,7 @@
 
 namespace sg {
 
-constexpr uint32_t TR_LINE = 8;          // chunks of a line
+constexpr uint32_t TR_LINE = 8;          // chunks of a line (1 where the row has few lines for its k)
 constexpr uint32_t TR_MAX_LINES = 8192;  // lines of a row (1 MiB)
 
 // unsigned order of the values: -inf < ... < -0 = +0 < ... < +inf < NaN
@@ -55,6 +55,7 @@ struct TopArgs {
     uint32_t k;
     uint32_t* idx;
     float *logp, *lse;
+    uint32_t shift; // a line is 1 << shift chunks
     // parts of a row: candidates and sums of each part
     uint32_t parts, len;
     uint32_t *part_key, *part_idx; // [rows][parts][k]
@@ -322,14 +323,16 @@ __device__ __forceinline__ void emit_rows(S& sh, uint32_t n, uint32_t kth, uint3
     }
 }
 
-// The k of n candidates (ascending in index) in LDS.  For up to NT of them a
-// thread counts what its own is below, four keys a read: one round instead of
-// a radix round of three barriers for every 8 bits.
+// The k of n candidates (ascending in index) in LDS.  For up to 64 of them a
+// lane of one wave counts what its own is below, four keys a read; for more
+// the radix rounds of three barriers for every 8 bits are shorter.  8000 x
+// 8000 bf16 with counting up to 512, 128 and 64: top 128 83, 57 and 58 us,
+// top 64 65, 66 and 55 us.
 template <int NT, class S, class Put>
 __device__ __forceinline__ void select_candidates(S& sh, const uint32_t* ckey, const uint32_t* cidx, uint32_t n,
                                                   uint32_t k, int low_shift, Put put)
 {
-    if (n <= NT && n <= 512) {
+    if (n <= SG_WAVE) {
         const uint32_t i = threadIdx.x, key = i < n ? ckey[i] : 0u;
         uint32_t rank = 0;
         if (uniform(i) < n) // waves without a candidate have nothing to count
@@ -410,11 +413,11 @@ __global__ __launch_bounds__(NT, 8) void top_rows_kernel(TopArgs p)
     const E* x = static_cast<const E*>(p.r.x) + row * p.r.ld + lo;
     const RowSpan sp = span_of(x, V);
     const E* xc = x + sp.head;
-    const uint32_t nl = (sp.nc + TR_LINE - 1) / TR_LINE;
+    const uint32_t shift = p.shift, per_line = 1u << shift, nl = (sp.nc + per_line - 1) >> shift;
     const bool lined = nl <= TR_MAX_LINES;
 
     RowStat st = {-INFINITY, 0.0};
-    const auto take = [&](u32x4 w, uint32_t c) { // chunk c < nl * TR_LINE: whole lines, so that their 8 lanes stay together
+    const auto take = [&](u32x4 w, uint32_t c) { // chunk c of a line: whole lines, so that their 8 lanes stay together
         float m = -INFINITY;
         if (c < sp.nc) {
             float v[VEC];
@@ -423,8 +426,8 @@ __global__ __launch_bounds__(NT, 8) void top_rows_kernel(TopArgs p)
             for (int i = 0; i < VEC; ++i) m = fmaxf(m, v[i]);
             stat_add<VEC>(st, v, p.r.c);
         }
-        m = line_max(m);
-        if (lined && c % TR_LINE == 0) lines[c / TR_LINE] = m;
+        if (shift) m = line_max(m);
+        if (lined && (c & (per_line - 1)) == 0) lines[c >> shift] = m;
         __builtin_amdgcn_sched_barrier(0);
     };
     uint32_t j0 = 0;
@@ -440,7 +443,7 @@ __global__ __launch_bounds__(NT, 8) void top_rows_kernel(TopArgs p)
         load_chunks<J, NT>(w, xc, t + j0, sp.nc);
 #pragma unroll
         for (int j = 0; j < J; ++j)
-            if (t + j0 + j * NT < nl * TR_LINE) take(w[j], t + j0 + j * NT);
+            if (t + j0 + j * NT < nl << shift) take(w[j], t + j0 + j * NT);
     }
     if (t < 2 * VEC) {
         const uint32_t i = loose_element(sp, VEC, t);
@@ -469,6 +472,7 @@ __global__ __launch_bounds__(NT, 8) void top_rows_kernel(TopArgs p)
         const uint32_t want = (k + NW - 1) / NW;
         const float reach = l1 - l0 <= 2 * SG_WAVE   ? lines_reach<2>(lines, l0, l1, want)
                             : l1 - l0 <= 4 * SG_WAVE ? lines_reach<4>(lines, l0, l1, want)
+                            : l1 - l0 <= 8 * SG_WAVE ? lines_reach<8>(lines, l0, l1, want)
                                                      : lines_reach<RMAX>(lines, l0, l1, want);
         if (lane_id() == 0) sh.low[wv] = reach;
         __syncthreads();
@@ -487,13 +491,13 @@ __global__ __launch_bounds__(NT, 8) void top_rows_kernel(TopArgs p)
                     if (lines[b] >= low) cidx[pos++] = b;
             __syncthreads();
             if (nlc <= cap) {
-                // their elements that reach it, with those outside the chunks, in order: 8 items to a
-                // line, before them the elements ahead of the chunks and after them those behind; a
+                // their elements that reach it, with those outside the chunks, in order: an item a
+                // chunk, before them the elements ahead of the chunks and after them those behind; a
                 // thread takes neighbours again.  The list of lines moves over the line maxima.
                 uint32_t* list = reinterpret_cast<uint32_t*>(lines);
                 for (uint32_t i = t; i < nlc; i += NT) list[i] = cidx[i];
                 __syncthreads();
-                const uint32_t items = 8 * nlc + 2;
+                const uint32_t items = (nlc << shift) + 2;
                 constexpr int B = 4; // neighbours to a thread, loaded together; one if that is enough
                 const uint32_t per_t = items <= NT ? 1 : B;
                 for (uint32_t q0 = 0; q0 < items; q0 += per_t * NT) {
@@ -510,7 +514,7 @@ __global__ __launch_bounds__(NT, 8) void top_rows_kernel(TopArgs p)
                             first[i] = sp.head + sp.nc * VEC;
                             len = V - first[i];
                         } else if (q < items) {
-                            const uint32_t ch = list[(q - 1) / 8] * TR_LINE + (q - 1) % 8;
+                            const uint32_t ch = (list[(q - 1) >> shift] << shift) + ((q - 1) & (per_line - 1));
                             first[i] = sp.head + ch * VEC;
                             if (ch < sp.nc) len = VEC;
                         }
@@ -644,10 +648,21 @@ static TopWs top_carve(Carver& cv, uint64_t T, uint32_t parts, uint32_t k)
     return w;
 }
 
+// A row with fewer than three lines to each of its k gives a threshold far
+// below the k-th largest, or none: its groups are single chunks, as long as
+// their maxima fit (top 128 of 8000 x 8000 bf16, 125 lines: 307 us with
+// lines of 8, 84 us so).
+template <typename E>
+static uint32_t top_shift(uint64_t V, uint32_t k)
+{
+    const uint64_t chunks = V / RowIO<E>::VEC;
+    return chunks / TR_LINE < 3ull * k && chunks <= TR_MAX_LINES ? 0 : 3;
+}
+
 template <typename E>
 static size_t top_lds(uint64_t V, uint32_t k)
 {
-    const uint64_t lines = ceil_div(V / RowIO<E>::VEC, TR_LINE), cap = top_cap(k);
+    const uint64_t lines = ceil_div(V / RowIO<E>::VEC, 1u << top_shift<E>(V, k)), cap = top_cap(k);
     // the lines' maxima, or the list of up to cap candidate lines in their place
     return cap * 8 + (lines <= TR_MAX_LINES && lines > cap ? lines : cap) * 4;
 }
@@ -656,6 +671,7 @@ template <typename E, int NT>
 static int launch_top(TopArgs p, hipStream_t st)
 {
     const size_t lds = top_lds<E>(p.r.V, p.k);
+    p.shift = top_shift<E>(p.r.V, p.k);
     for (p.r.row0 = 0; p.r.row0 < p.r.T; p.r.row0 += ROWS_PER_LAUNCH) {
         const uint64_t left = p.r.T - p.r.row0;
         top_rows_kernel<E, NT, false><<<(unsigned)(left < ROWS_PER_LAUNCH ? left : ROWS_PER_LAUNCH), NT, lds, st>>>(p);
@@ -676,6 +692,7 @@ static int launch_top_of(TopArgs p, void* ws, hipStream_t st)
         p.part_idx = w.idx;
         p.part_stat = w.stat;
         p.len = part_len(p.r.V, &p.parts);
+        p.shift = top_shift<E>(p.len, p.k);
         top_rows_kernel<E, 512, true><<<dim3(p.parts, (unsigned)p.r.T), 512, top_lds<E>(p.len, p.k), st>>>(p);
         SG_TRY_LAUNCH();
         top_join_kernel<E><<<(unsigned)p.r.T, TJ_NT, 0, st>>>(p);
@@ -695,6 +712,9 @@ static int launch_top_of(TopArgs p, void* ws, hipStream_t st)
     // until the lists are so long that the threads of one block count (950
     // against 705 us for k = 500); with few rows there is one block on a
     // compute unit anyway (200 x 262144 fp32: 58 against 49 us).
+    // Rows of up to 32 KB: 256 threads, twice the blocks of 512 on a compute unit, so that one
+    // selects while another reads (512 -> 256: top 20 of 8000 x 8000 bf16 92 -> 54 us, top 64 of
+    // 8000 x 16000 133 -> 90 us).  Longer lists keep 512 for their selection.
     if (bytes <= 32 * 1024 && p.k <= 256) return launch_top<E, 256>(p, st);
     if (bytes <= 128 * 1024 || (p.k <= 256 && p.r.T >= 512)) return launch_top<E, 512>(p, st);
     return launch_top<E, 1024>(p, st);
