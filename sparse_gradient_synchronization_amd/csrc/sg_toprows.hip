@@ -56,6 +56,7 @@ struct TopArgs {
     uint32_t* idx;
     float *logp, *lse;
     uint32_t shift; // a line is 1 << shift chunks
+    bool lined;     // the LDS has room for the maxima of the lines of V elements, or of len
     // parts of a row: candidates and sums of each part
     uint32_t parts, len;
     uint32_t *part_key, *part_idx; // [rows][parts][k]
@@ -414,7 +415,9 @@ __global__ __launch_bounds__(NT, 8) void top_rows_kernel(TopArgs p)
     const RowSpan sp = span_of(x, V);
     const E* xc = x + sp.head;
     const uint32_t shift = p.shift, per_line = 1u << shift, nl = (sp.nc + per_line - 1) >> shift;
-    const bool lined = nl <= TR_MAX_LINES;
+    // Not nl <= TR_MAX_LINES: an unaligned row has a chunk less than the room was
+    // sized for and the last part is shorter, so nl can pass a limit that they did not.
+    const bool lined = p.lined;
 
     RowStat st = {-INFINITY, 0.0};
     const auto take = [&](u32x4 w, uint32_t c) { // chunk c of a line: whole lines, so that their 8 lanes stay together
@@ -659,19 +662,21 @@ static uint32_t top_shift(uint64_t V, uint32_t k)
     return chunks / TR_LINE < 3ull * k && chunks <= TR_MAX_LINES ? 0 : 3;
 }
 
+// Lines and LDS of blocks that take up to V elements each.
 template <typename E>
-static size_t top_lds(uint64_t V, uint32_t k)
+static size_t top_lines(TopArgs* p, uint64_t V)
 {
-    const uint64_t lines = ceil_div(V / RowIO<E>::VEC, 1u << top_shift<E>(V, k)), cap = top_cap(k);
+    p->shift = top_shift<E>(V, p->k);
+    const uint64_t lines = ceil_div(V / RowIO<E>::VEC, 1u << p->shift), cap = top_cap(p->k);
+    p->lined = lines <= TR_MAX_LINES;
     // the lines' maxima, or the list of up to cap candidate lines in their place
-    return cap * 8 + (lines <= TR_MAX_LINES && lines > cap ? lines : cap) * 4;
+    return cap * 8 + (p->lined && lines > cap ? lines : cap) * 4;
 }
 
 template <typename E, int NT>
 static int launch_top(TopArgs p, hipStream_t st)
 {
-    const size_t lds = top_lds<E>(p.r.V, p.k);
-    p.shift = top_shift<E>(p.r.V, p.k);
+    const size_t lds = top_lines<E>(&p, p.r.V);
     for (p.r.row0 = 0; p.r.row0 < p.r.T; p.r.row0 += ROWS_PER_LAUNCH) {
         const uint64_t left = p.r.T - p.r.row0;
         top_rows_kernel<E, NT, false><<<(unsigned)(left < ROWS_PER_LAUNCH ? left : ROWS_PER_LAUNCH), NT, lds, st>>>(p);
@@ -692,8 +697,8 @@ static int launch_top_of(TopArgs p, void* ws, hipStream_t st)
         p.part_idx = w.idx;
         p.part_stat = w.stat;
         p.len = part_len(p.r.V, &p.parts);
-        p.shift = top_shift<E>(p.len, p.k);
-        top_rows_kernel<E, 512, true><<<dim3(p.parts, (unsigned)p.r.T), 512, top_lds<E>(p.len, p.k), st>>>(p);
+        const size_t lds = top_lines<E>(&p, p.len);
+        top_rows_kernel<E, 512, true><<<dim3(p.parts, (unsigned)p.r.T), 512, lds, st>>>(p);
         SG_TRY_LAUNCH();
         top_join_kernel<E><<<(unsigned)p.r.T, TJ_NT, 0, st>>>(p);
         SG_TRY_LAUNCH();
