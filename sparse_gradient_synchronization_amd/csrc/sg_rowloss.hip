@@ -20,9 +20,9 @@ constexpr uint32_t RL_MAX_K = SG_ROWS_MAX_K;
 constexpr uint32_t RL_MAX_PARTS = 64;
 
 // A row's gradient: coef * exp2(c * (x_i - m)) for the tokens it does not
-// name; a and b are what the operator needs for those it names.
+// name; a, b and named_m are what the operator needs for those it names.
 struct RowCoef {
-    float m, coef, a, b;
+    float m, coef, a, b, named_m;
 };
 
 // Where the gradient goes.  past: its stores go past the caches.
@@ -119,7 +119,7 @@ struct PolicyOp {
         }
         const double g = w * slope * r.it;
         // at the action 1 - q without the cancellation
-        return {st.m, (float)(-g * inverse_of(S)), (float)(g * -row_expm1(lp)), 0.f};
+        return {st.m, (float)(-g * inverse_of(S)), (float)(g * -row_expm1(lp)), 0.f, 0.f};
     }
     __device__ __forceinline__ void named_grad(const Rows&, const RowCoef&, NoList&) const {}
     template <typename E>
@@ -313,14 +313,17 @@ struct DistillOp {
         }
         if (write && l == 0) loss[row] = (float)(w * L);
         const double g = w * r.it;
-        const double all = (P + R) * per_S;
-        return {m, (float)(g * (R != 0.0 ? all - R * per_rest : all)), (float)(g * all), (float)(g * gp)};
+        const double all = (P + R) * per_S, near = all * __shfl(scale, 0);
+        // The unlisted tokens' exponentials are taken from their own maximum.
+        // From the row's they would be 0 in fp32 88 below it, and R / rest
+        // beyond fp32's range, where together they are up to R.
+        return {st.m, (float)(g * (R != 0.0 ? near - R / st.s : near)), (float)(g * all), (float)(g * gp), m};
     }
     // ls.z[j] becomes the gradient of listed token j
     __device__ __forceinline__ void named_grad(const Rows& r, const RowCoef& co, RowList& ls) const
     {
         for (uint32_t j = lane_id(); j < k; j += SG_WAVE)
-            ls.z[j] = co.a * exp2_scaled<false>(ls.z[j] - shift_of(co.m), r.c) - co.b * ls.p[j];
+            ls.z[j] = co.a * exp2_scaled<false>(ls.z[j] - shift_of(co.named_m), r.c) - co.b * ls.p[j];
     }
     template <typename E>
     __device__ __forceinline__ void put_named(uint64_t, E* g, const RowCoef&, const RowList& ls, uint32_t lo,

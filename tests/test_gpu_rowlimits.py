@@ -41,3 +41,106 @@ def test_top_rows_around_the_most_lines(T, V, k, dtype, ld, shift):
         z = host(rows.gather(1, first) - want[:, None])
         check(host(logp[a:a + 16]), z, ref.sum_error(V) + 2.0 ** -24 * np.abs(z), "logp")
     assert sg.sg_device_error() == 0
+
+
+# ---------------------------------------------------------------------------
+# distillation
+# ---------------------------------------------------------------------------
+MODES = {"plain": sg.SG_DISTILL_PLAIN, "renorm": sg.SG_DISTILL_RENORM, "tail": sg.SG_DISTILL_TAIL}
+
+
+def sum_bound(V):
+    """Bound of the relative error of a row's sum of exponentials, as the
+    kernels add it.  A term's exponent is rounded twice (the difference to the
+    maximum, its product with the scale): 2^-23 of the term's depth, and the
+    depth weighted by the terms' shares is at most log V; the instruction is
+    off by 2^-23, the tree of a chunk adds three half units.  All else is added in
+    fp64, but where a lane's maximum rises its sum is scaled by an fp32
+    exponential: 2^-23 each time (of n chunks in random order that is log n + 1
+    times on average; 16 here), and 2^-23 of the rises, which add up to the
+    maximum's depth again.  Waves, blocks and parts join with one such scaling each."""
+    return 2.0 ** -23 * (2 * max(1.0, np.log(V)) + 1 + 1.5 + 16 + 3)
+
+
+def distill_bounds(x, idx, logp, w, it, mode):
+    """Loss and gradient of the definition, and what the kernel's may be off
+    by: the sums' errors; scalars take the temperature as fp32 rounds it, half a
+    unit of the distances they multiply; a gradient's factors, exponential and
+    product are rounded once each, and its exponent by 3 half units of its own depth
+    below the maximum of the listed or of the unlisted tokens."""
+    T, V = x.shape
+    se = sum_bound(V)
+    L, G, tl, tg = np.zeros(T), np.zeros((T, V)), np.zeros(T), np.zeros((T, V))
+    for t in range(T):
+        l, g, scale = ref.distill_row(x[t], idx[t], logp[t].astype(np.float64), it, mode)
+        ok = (idx[t] >= 0) & (idx[t] < V)
+        listed = np.zeros(V, bool)
+        listed[idx[t][ok]] = True
+        depth = np.zeros(V)
+        for part, top in ((listed, x[t].max()), (~listed, x[t][~listed].max() if (~listed).any() else 0.0)):
+            with np.errstate(invalid="ignore"):
+                d = (top - x[t][part]) * it
+            depth[part] = np.where(np.isfinite(d), d, 0.0)
+        finite = x[t][np.isfinite(x[t])]
+        apart = (finite.max() - finite.min()) * it if finite.size else 0.0
+        L[t], G[t] = w[t] * l, w[t] * g
+        tl[t] = abs(w[t]) * (3 * se + 2.0 ** -24 * 2 * apart) + 2.0 ** -24 * abs(w[t] * l)
+        tg[t] = abs(w[t]) * scale * (2 * se + 2.0 ** -22 + 3 * 2.0 ** -24 * np.minimum(depth, 110))
+    return L, G, tl, tg
+
+
+def check_distill(x, idx, logp, mode, dtype, temp=1.0, weight=None):
+    T = x.shape[0]
+    w = np.ones(T) if weight is None else np.asarray(weight, np.float64)
+    args = (dev(idx, torch.int32), dev(logp, torch.float32))
+    kw = dict(temperature=temp, mode=MODES[mode], weight=None if weight is None else dev(weight, torch.float32))
+    loss, g = sg.sg_distill_loss(x, *args, **kw)
+    L, G, tl, tg = distill_bounds(host(x), idx, logp, w, 1.0 / temp, mode)
+    check(host(loss), L, tl, "loss")
+    # what an exponential below 2^-126 gives is lost
+    check(host(g), G, tg + ref.HALF[dtype] * np.abs(G) + 2.0 ** -126 * 16, "gradient")
+    alone, _ = sg.sg_distill_loss(x, *args, want_grad=False, **kw)
+    check(host(alone), L, tl, "loss without the gradient")
+    assert sg.sg_device_error() == 0
+    return host(loss), host(g)
+
+
+# in one block (rows kept in registers, and longer ones) and in parts
+GAP_ROWS = [(3, 100), (3, 1000), (3, 5003), (130, 33000), (2, 70001), (1, 262200)]
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("T,V", GAP_ROWS)
+@pytest.mark.parametrize("gap,temp", [(80, 1.0), (87, 1.0), (88, 1.0), (95, 1.0), (120, 2.0), (200, 1.0), (600, 1.0),
+                                      (60, 0.1)])
+def test_tail_gradient_far_below_the_list(gap, temp, T, V, dtype):
+    """The unlisted tokens share R however far below the listed ones they lie:
+    each of them has a gradient of R times its share among them."""
+    need_gpu()
+    rng = np.random.default_rng(gap + V)
+    g = torch.Generator().manual_seed(gap + V)
+    x = (torch.rand((T, V), generator=g) * 0.5 - gap).to(TDT[dtype])
+    idx = np.stack([rng.choice(V, 5, replace=False) for _ in range(T)])
+    x[torch.arange(T)[:, None], torch.from_numpy(idx)] = torch.randn((T, 5), generator=g).to(TDT[dtype])
+    logp = np.log(np.full((T, 5), 0.16)).astype(np.float32)
+    _, grad = check_distill(x.cuda(), idx, logp, "tail", dtype, temp)
+    listed = np.zeros((T, V), bool)
+    np.put_along_axis(listed, idx, True, 1)
+    assert np.isfinite(grad).all() and (grad[~listed] < 0).all()
+    unlisted = np.where(listed, 0.0, grad).sum(1) * temp
+    # R = 0.2 less what q of them adds (e^-80 and less), each rounded to the type
+    assert np.abs(unlisted + 0.2).max() < 0.2 * (ref.HALF[dtype] + 2.0 ** -17)
+
+
+@pytest.mark.parametrize("mode", ["plain", "renorm", "tail"])
+@pytest.mark.parametrize("T,V", [(2, 700), (2, 70001)])
+def test_distill_listed_far_below_the_others(T, V, mode):
+    """The other way round: a list that the student gives no weight to."""
+    need_gpu()
+    rng = np.random.default_rng(V)
+    for gap in (50, 95, 300):
+        x = torch.randn((T, V), generator=torch.Generator().manual_seed(gap))
+        idx = np.stack([rng.choice(V, 6, replace=False) for _ in range(T)])
+        x[torch.arange(T)[:, None], torch.from_numpy(idx)] -= gap
+        logp = np.log(rng.dirichlet(np.ones(6), T) * 0.7).astype(np.float32)
+        check_distill(x.cuda(), idx, logp, mode, "f32")
