@@ -567,7 +567,8 @@ typedef enum sg_distill_mode {
 /* Distillation from a teacher's listed log-probabilities.  With p = exp(logp)
  * over the row's list, P = sum p and Q = sum q over the list:
  *   PLAIN   L = sum p (log p - log q)
- *   RENORM  the same with p / P (a list of no mass: L = 0)
+ *   RENORM  the same with p / P, however small P (a list of nothing but
+ *           padding and log-probabilities of -inf: L = 0)
  *   TAIL    PLAIN + R (log R - log(1 - Q)), R = max(0, 1 - P); 1 - Q is summed
  *           over the unlisted tokens, not subtracted; where they hold nothing
  *           (all masked, or a share of the row below 1e-300) the bucket is

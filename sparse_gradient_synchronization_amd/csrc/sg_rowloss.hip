@@ -203,6 +203,10 @@ struct DistillOp {
     struct Named {
         double P, A, S; // mass, sum p (log p - (z - m)), sum exp(z - m), z scaled by inv_temp
         float m;        // maximum of the listed logits
+        // RENORM: the maximum of the listed log-probabilities, otherwise 0.  p / P
+        // is the same for p = exp(logp - top), and masses far below 1 keep 1 / P in
+        // fp32's range.
+        float top;
     };
 
     __device__ __forceinline__ bool live(uint64_t row) const { return !weight || weight[row] != 0.f; }
@@ -255,22 +259,27 @@ struct DistillOp {
     __device__ __forceinline__ Named named(const Rows& r, uint64_t row, const E* x, RowList& ls) const
     {
         const float* lp = logp + row * k;
-        float m = -INFINITY;
+        float m = -INFINITY, top = -INFINITY;
         for (uint32_t j = lane_id(); j < k; j += SG_WAVE) {
             const uint32_t i = ls.id[j];
             const float v = i < V ? RowIO<E>::get(x + i) : -INFINITY;
             ls.z[j] = v;
             m = fmaxf(m, v);
+            if (mode == SG_DISTILL_RENORM && i < V) top = fmaxf(top, lp[j]);
         }
 #pragma unroll
-        for (int d = 1; d < SG_WAVE; d <<= 1) m = fmaxf(m, __shfl_xor(m, d, SG_WAVE));
+        for (int d = 1; d < SG_WAVE; d <<= 1) {
+            m = fmaxf(m, __shfl_xor(m, d, SG_WAVE));
+            top = fmaxf(top, __shfl_xor(top, d, SG_WAVE));
+        }
+        top = shift_of(top);
         const double shift = shift_of(m);
         double P = 0.0, A = 0.0, S = 0.0;
 #pragma unroll 1
         for (uint32_t j = lane_id(); j < k; j += SG_WAVE) {
             double p = 0.0;
             if (ls.id[j] < V) {
-                const double t = lp[j], d = (ls.z[j] - shift) * r.it;
+                const double t = (double)lp[j] - top, d = (ls.z[j] - shift) * r.it;
                 p = row_exp(t);
                 P += p;
                 if (p != 0.0) A += p * (t - d);
@@ -278,7 +287,7 @@ struct DistillOp {
             }
             ls.p[j] = (float)p;
         }
-        return {wave_sum_f64(P), wave_sum_f64(A), wave_sum_f64(S), m};
+        return {wave_sum_f64(P), wave_sum_f64(A), wave_sum_f64(S), m, top};
     }
     // finish: by the whole wave, so that the functions of several numbers run
     // side by side in its lanes
@@ -631,7 +640,7 @@ __global__ __launch_bounds__(SP_NT, 4) void row_join_kernel(Rows r, Op op, Split
                 const uint32_t i = op.idx[row * op.k + j];
                 ls.id[j] = i;
                 ls.z[j] = i >= lo && i < lo + n ? RowIO<E>::get(x + (i - lo)) : 0.f;
-                ls.p[j] = (float)row_exp((double)op.logp[row * op.k + j]);
+                ls.p[j] = (float)row_exp((double)op.logp[row * op.k + j] - keep[row].top);
             }
     }
     if constexpr (GRAD) {

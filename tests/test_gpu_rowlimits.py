@@ -144,3 +144,40 @@ def test_distill_listed_far_below_the_others(T, V, mode):
         x[torch.arange(T)[:, None], torch.from_numpy(idx)] -= gap
         logp = np.log(rng.dirichlet(np.ones(6), T) * 0.7).astype(np.float32)
         check_distill(x.cuda(), idx, logp, mode, "f32")
+
+
+@pytest.mark.parametrize("T,V", [(4, 900), (130, 33000), (2, 70001)])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("level", [-3, -60, -90, -100, -104, -300, -700, -5000])
+def test_renormalised_lists_of_little_mass(level, T, V, dtype):
+    """p / P does not depend on the level of the list's log-probabilities:
+    the definition is taken from the list lifted to 0, where its sums are ordinary."""
+    need_gpu()
+    rng = np.random.default_rng(V - level)
+    x, xs = make_logits(V - level, T, V, dtype)
+    idx = np.stack([rng.choice(V, 70, replace=False) for _ in range(T)])
+    idx[::3, 40:] = -1
+    logp = (level + rng.normal(0, 1.0, (T, 70))).astype(np.float32)
+    logp[1::3, 5] = -np.inf
+    loss, g = sg.sg_distill_loss(x, dev(idx, torch.int32), dev(logp, torch.float32), mode=sg.SG_DISTILL_RENORM)
+    lifted = logp.astype(np.float64) - level
+    L, G, tl, tg = np.zeros(T), np.zeros((T, V)), np.zeros(T), np.zeros((T, V))
+    for t in range(T):
+        a = distill_bounds(xs[t:t + 1], idx[t:t + 1], lifted[t:t + 1], np.ones(1), 1.0, "renorm")
+        L[t], G[t], tl[t], tg[t] = a[0][0], a[1][0], a[2][0], a[3][0]
+    check(host(loss), L, tl, "loss")
+    check(host(g), G, tg + ref.HALF[dtype] * np.abs(G) + 2.0 ** -126 * 16, "gradient")
+    y = x.clone()
+    loss2, g2 = sg.sg_distill_loss(y, dev(idx, torch.int32), dev(logp, torch.float32), mode=sg.SG_DISTILL_RENORM, grad=y)
+    assert torch.equal(loss, loss2) and torch.equal(g, g2)
+
+
+@pytest.mark.parametrize("T,V", [(3, 900), (2, 70001)])
+def test_renormalised_list_without_mass(T, V):
+    need_gpu()
+    x, _ = make_logits(V, T, V, "f32")
+    idx = np.stack([np.arange(8) for _ in range(T)])
+    idx[0] = -1
+    logp = np.full((T, 8), -np.inf, np.float32)
+    loss, g = sg.sg_distill_loss(x, dev(idx, torch.int32), dev(logp, torch.float32), mode=sg.SG_DISTILL_RENORM)
+    assert not loss.any() and not g.any()
