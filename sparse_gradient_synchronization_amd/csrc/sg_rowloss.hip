@@ -303,14 +303,14 @@ struct DistillOp {
         const double lg = row_log(l == 0 ? S : (l == 1 ? R0 * S * per_rest : nm.P));
         // lse less the listed maximum (a row may lie at the type's lowest
         // value, where lse itself holds no digit of log S); of a row of
-        // nothing but -inf, A decides
-        const double lse = m == -INFINITY ? 0.0 : (shift - shift_of(nm.m)) * r.it + __shfl(lg, 0);
+        // nothing but -inf, A decides: S is 0, or NaN if the row has one
+        const double lse = m == -INFINITY ? S : (shift - shift_of(nm.m)) * r.it + __shfl(lg, 0);
         const double log_tail = __shfl(lg, 1), log_mass = __shfl(lg, 2);
         const double w = weight ? (double)weight[row] : 1.0;
         double P = nm.P, R = 0.0, gp = 1.0, L;
         if (mode == SG_DISTILL_RENORM) {
-            gp = P > 0.0 ? 1.0 / P : P; // nothing listed: no mass, no loss (a NaN stays)
-            L = P > 0.0 ? nm.A * gp - log_mass + lse : P;
+            gp = P > 0.0 ? 1.0 / P : P; // nothing listed: no mass, no loss (a NaN stays, the row's too)
+            L = P > 0.0 ? nm.A * gp - log_mass + lse : P * lse;
             P = P > 0.0 ? 1.0 : P;
         } else {
             L = nm.A + P * lse;

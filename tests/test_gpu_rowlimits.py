@@ -181,3 +181,42 @@ def test_renormalised_list_without_mass(T, V):
     logp = np.full((T, 8), -np.inf, np.float32)
     loss, g = sg.sg_distill_loss(x, dev(idx, torch.int32), dev(logp, torch.float32), mode=sg.SG_DISTILL_RENORM)
     assert not loss.any() and not g.any()
+
+
+# ---------------------------------------------------------------------------
+# rows that hold a NaN or +inf
+# ---------------------------------------------------------------------------
+def poison(x, t, kind, keep=()):
+    """Row t gets a NaN or +inf; 'only': NaN beside nothing but -inf.  The tokens of `keep` become -inf."""
+    keep = list(keep)
+    if kind == "only":
+        x[t] = -float("inf")
+    x[t, keep] = -float("inf")
+    at = next(i for i in range(x.shape[1] - 3, -1, -1) if i not in keep)
+    x[t, at] = float("inf") if kind == "inf" else float("nan")
+
+
+NAN_ROWS = [(4, 60), (4, 5003), (130, 33000), (3, 70001)]
+
+
+@pytest.mark.parametrize("mode", ["plain", "renorm", "tail"])
+@pytest.mark.parametrize("kind", ["nan", "inf", "only"])
+@pytest.mark.parametrize("T,V", NAN_ROWS)
+def test_distill_rows_with_a_nan(T, V, kind, mode):
+    """NaN results, whatever the list: tokens that are -inf, of no mass, or padding only."""
+    need_gpu()
+    rng = np.random.default_rng(V)
+    x, xs = make_logits(V, T, V, "f32")
+    idx = np.stack([rng.choice(V, 6, replace=False) for _ in range(T)])
+    logp = np.log(rng.dirichlet(np.ones(6), T) * 0.8).astype(np.float32)
+    poison(x, 0, kind, idx[0])
+    idx[1] = -1
+    poison(x, 1, kind)
+    logp[2] = -np.inf
+    poison(x, 2, kind, idx[2])
+    for want_grad in (True, False):
+        loss, g = sg.sg_distill_loss(x, dev(idx, torch.int32), dev(logp, torch.float32), mode=MODES[mode],
+                                     want_grad=want_grad)
+        assert list(np.flatnonzero(np.isnan(host(loss)))) == [0, 1, 2]
+        if want_grad:
+            assert np.isnan(host(g)[:3]).all() and np.isfinite(host(g)[3:]).all()
