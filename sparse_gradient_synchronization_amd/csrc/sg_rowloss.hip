@@ -66,6 +66,12 @@ __device__ __forceinline__ uint32_t marked(const uint32_t* bm, uint32_t i0, int 
 // g is element lo).  kListed: tokens are listed, and left out of the
 // streaming pass's sum; a wave of its own handles the list.
 
+// log-probability of the logit za; a NaN in the row (its sum is NaN then) stays
+__device__ __forceinline__ double token_logp(const Rows& r, RowStat st, float za)
+{
+    return za == -INFINITY && st.s == st.s ? -(double)INFINITY : ((double)za - st.m) * r.it - row_log(st.s);
+}
+
 // ---------------------------------------------------------------------------
 // the clipped policy loss
 // ---------------------------------------------------------------------------
@@ -98,10 +104,10 @@ struct PolicyOp {
     __device__ __forceinline__ RowCoef finish(const Rows& r, uint64_t row, RowStat st, Named za, bool write) const
     {
         const double S = st.s;
-        const double lp = za == -INFINITY ? -(double)INFINITY : ((double)za - st.m) * r.it - row_log(S);
+        const double lp = token_logp(r, st, za);
         const double w = weight ? (double)weight[row] : 1.0;
         const double A = adv ? (double)adv[row] : 0.0;
-        const double ratio = old_logp ? row_exp(lp - (double)old_logp[row]) : 1.0;
+        const double ratio = old_logp ? row_exp(lp - (double)old_logp[row]) : (S == S ? 1.0 : S);
         const double bounded = ratio < lo ? lo : (ratio > hi ? hi : ratio);
         const double a = ratio * A, b = bounded * A;
         double L = a <= b ? -a : (b <= a ? -b : a + b); // a NaN stays
@@ -161,7 +167,7 @@ struct TokenOp {
     __device__ __forceinline__ RowCoef finish(const Rows& r, uint64_t row, RowStat st, Named za, bool write) const
     {
         if (write && lane_id() == 0) {
-            logp[row] = za == -INFINITY ? -(double)INFINITY : ((double)za - st.m) * r.it - row_log(st.s);
+            logp[row] = token_logp(r, st, za);
             m[row] = st.m;
             inv[row] = (float)inverse_of(st.s);
             slope[row] = 0.f;

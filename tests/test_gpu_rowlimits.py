@@ -220,3 +220,40 @@ def test_distill_rows_with_a_nan(T, V, kind, mode):
         assert list(np.flatnonzero(np.isnan(host(loss)))) == [0, 1, 2]
         if want_grad:
             assert np.isnan(host(g)[:3]).all() and np.isfinite(host(g)[3:]).all()
+
+
+@pytest.mark.parametrize("kind", ["nan", "inf", "only"])
+@pytest.mark.parametrize("T,V", NAN_ROWS)
+def test_policy_rows_with_a_nan(T, V, kind):
+    """An action of -inf, and a policy that is its own old one: NaN all the same."""
+    need_gpu()
+    x, xs = make_logits(V + 1, T, V, "bf16")
+    action = np.arange(T) % V
+    poison(x, 0, kind, [0])
+    poison(x, 1, kind)
+    adv = dev(np.linspace(-1, 1, T), torch.float32)
+    some = dev(np.full(T, -3.0), torch.float32)
+    for old, rf, kl in ((None, None, 0.0), (some, None, 0.0), (None, some, 0.1), (some, some, 0.1)):
+        for want_grad in (True, False):
+            loss, logp, g = sg.sg_policy_loss(x, dev(action, torch.int32), old, adv, ref_logp=rf, kl_coef=kl,
+                                              want_grad=want_grad)
+            assert list(np.flatnonzero(np.isnan(host(loss)))) == [0, 1]
+            assert list(np.flatnonzero(np.isnan(host(logp)))) == [0, 1]
+            if want_grad:
+                g = host(g)
+                assert np.isnan(g[:2]).all() and np.isfinite(g[2:]).all()
+
+
+@pytest.mark.parametrize("kind", ["nan", "inf", "only"])
+@pytest.mark.parametrize("T,V", NAN_ROWS)
+def test_preference_rows_with_a_nan(T, V, kind):
+    """A label of -inf in a row with a NaN: the sequence's sum is NaN, not -inf."""
+    need_gpu()
+    x, xs = make_logits(V + 2, T, V, "f32")
+    label = np.arange(T) % V
+    poison(x, 1, kind, [1])
+    off = np.array([0, 1, 2, T, T])  # the chosen: row 0, row 1; the rejected: the others, none
+    loss, S, g = sg.sg_preference_loss(x, dev(label, torch.int32), dev(off, torch.int64))
+    assert list(np.isnan(host(loss))) == [False, True]
+    assert list(np.isnan(host(S))) == [False, True, False, False]
+    assert np.isnan(host(g)[1]).all() and np.isfinite(np.delete(host(g), 1, 0)).all()
