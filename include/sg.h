@@ -625,6 +625,7 @@ typedef enum sg_pref_kind {
  *   d_ref_logp [2 * pairs] fp32, or NULL: 0 (no reference model)
  *   d_weight   [pairs] fp32, or NULL: every pair 1
  *   d_loss [pairs], d_logp [2 * pairs] (S, may be NULL) fp32 out
+ * A NaN in a row that counts makes its whole pair's results NaN.
  * The temperature is 1.  Limits: pairs < 2^30, 0 < beta <= 1e6,
  * 0 <= smoothing < 0.5 (other than 0 with SG_PREF_SIGMOID only). */
 size_t sg_preference_workspace_bytes(uint64_t T, uint64_t V, sg_dtype dt);

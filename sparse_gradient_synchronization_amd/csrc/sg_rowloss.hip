@@ -734,8 +734,8 @@ __device__ __forceinline__ PairTerm pair_term(const PairArgs& p, uint32_t b, boo
             g = 2.0 * gap;
         } else if (p.kind == SG_PREF_HINGE) {
             const double gap = 1.0 - p.beta * d;
-            L = gap <= 0.0 ? 0.0 : gap; // a NaN stays
-            g = gap <= 0.0 ? 0.0 : -p.beta;
+            L = gap <= 0.0 ? 0.0 : gap; // a NaN stays, in the gradient too
+            g = gap <= 0.0 ? 0.0 : (gap > 0.0 ? -p.beta : gap);
         } else {
             const double h = p.beta * d, u = row_exp(-fabs(h)), l = row_log1p(u);
             const double up = l + (h < 0.0 ? -h : 0.0), down = l + (h > 0.0 ? h : 0.0);

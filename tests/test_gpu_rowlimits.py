@@ -257,3 +257,21 @@ def test_preference_rows_with_a_nan(T, V, kind):
     assert list(np.isnan(host(loss))) == [False, True]
     assert list(np.isnan(host(S))) == [False, True, False, False]
     assert np.isnan(host(g)[1]).all() and np.isfinite(np.delete(host(g), 1, 0)).all()
+
+
+@pytest.mark.parametrize("kind", ["sigmoid", "hinge", "ipo"])
+@pytest.mark.parametrize("T,V", [(6, 700), (1100, 700), (6, 70001)])
+def test_a_nan_reaches_its_whole_pair(T, V, kind):
+    """And no other: both sequences' gradients, in every kind of loss."""
+    need_gpu()
+    x, xs = make_logits(V + 3, T, V, "f32")
+    label = np.arange(T) % V
+    label[3] = -1
+    x[1, V - 1] = float("nan")
+    off = np.array([0, 2, 3, 5, T])  # rows 0, 1 against 3, 4; row 2 against the rest
+    loss, S, g = sg.sg_preference_loss(x, dev(label, torch.int32), dev(off, torch.int64),
+                                       kind={"sigmoid": 0, "hinge": 1, "ipo": 2}[kind])
+    assert list(np.isnan(host(loss))) == [True, False]
+    assert list(np.isnan(host(S))) == [True, False, False, False]
+    g = host(g)
+    assert np.isnan(g[[0, 1, 4]]).all() and not g[3].any() and np.isfinite(g[2]).all() and np.isfinite(g[5:]).all()
