@@ -63,10 +63,10 @@ struct TopArgs {
     RowStat* part_stat;            // [rows][parts]
 };
 
-// log-probability of a value
+// log-probability of a value; a NaN in the row (log_s is NaN then) stays
 __device__ __forceinline__ float top_logp(float v, float m, double log_s, double it)
 {
-    return v == -INFINITY ? v : (float)(((double)v - m) * it - log_s);
+    return v == -INFINITY && log_s == log_s ? v : (float)(((double)v - m) * it - log_s);
 }
 
 // ---------------------------------------------------------------------------

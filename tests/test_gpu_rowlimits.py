@@ -275,3 +275,22 @@ def test_a_nan_reaches_its_whole_pair(T, V, kind):
     assert list(np.isnan(host(S))) == [True, False, False, False]
     g = host(g)
     assert np.isnan(g[[0, 1, 4]]).all() and not g[3].any() and np.isfinite(g[2]).all() and np.isfinite(g[5:]).all()
+
+
+@pytest.mark.parametrize("kind", ["nan", "inf", "only"])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("T,V", NAN_ROWS)
+def test_top_rows_with_a_nan(T, V, dtype, kind):
+    """Every log-probability of the row is NaN, those of listed -inf too."""
+    need_gpu()
+    x, xs = make_logits(V + 4, T, V, dtype)
+    k = 12
+    poison(x, 1, kind, range(V - 2 - k, V - 3))
+    x[1, :V - 2 - k] = -float("inf")  # so that -inf is among the k
+    x[1, V - 2:] = -float("inf")
+    x[2] = -float("inf")
+    idx, logp, lse = sg.sg_topk_rows(x, k)
+    assert list(np.flatnonzero(np.isnan(host(lse)))) == [1]
+    logp = host(logp)
+    assert np.isnan(logp[1]).all() and (logp[2] == -np.inf).all() and np.isfinite(np.delete(logp, [1, 2], 0)).all()
+    assert idx[2].tolist() == list(range(k)) and idx[1].tolist() == list(range(k - 1)) + [V - 3]
