@@ -597,7 +597,8 @@ int sg_distill_loss(const void* d_logits, sg_dtype dt, uint64_t T, uint64_t V, u
  *   d loss / d logit_i = weight * inv_temp * dL/dlp * (1[i = action] - q_i)
  *   d_action   [T] i32; a row whose action is outside [0, V) counts as weight 0
  *   d_old_logp [T] fp32, or NULL: the policy is its own old one (r = 1)
- *   d_ref_logp [T] fp32, or NULL: no KL term
+ *   d_ref_logp [T] fp32, or NULL: no KL term.  An action of probability 0 that
+ *              the reference may take has loss +inf and no finite gradient.
  *   d_adv      [T] fp32 advantages, or NULL: 0 (log-probabilities and KL only)
  *   d_loss [T], d_logp [T] fp32 out (d_logp may be NULL; 0 for rows of weight 0)
  * Limits: 0 <= clip_low <= 1, 0 <= clip_high <= 1e6, 0 <= kl_coef <= 1e6. */

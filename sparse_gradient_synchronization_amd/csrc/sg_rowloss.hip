@@ -116,7 +116,7 @@ struct PolicyOp {
         double slope = clipped ? 0.0 : -a;
         if (ref_logp) {
             const double d = (double)ref_logp[row] - lp, e = row_expm1(d);
-            L += kl * (e - d);
+            L += kl * (d == INFINITY ? d : e - d); // a token that the policy cannot take: +inf, not inf - inf
             slope -= kl * e;
         }
         if (write && lane_id() == 0) {

@@ -294,3 +294,27 @@ def test_top_rows_with_a_nan(T, V, dtype, kind):
     logp = host(logp)
     assert np.isnan(logp[1]).all() and (logp[2] == -np.inf).all() and np.isfinite(np.delete(logp, [1, 2], 0)).all()
     assert idx[2].tolist() == list(range(k)) and idx[1].tolist() == list(range(k - 1)) + [V - 3]
+
+
+# ---------------------------------------------------------------------------
+# policy
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("T,V", [(4, 300), (130, 33000), (3, 70001)])
+def test_kl_of_an_action_of_probability_zero(T, V):
+    """exp(d) - d - 1 goes to +inf with d = ref - logp; the other rows keep theirs."""
+    need_gpu()
+    x, xs = make_logits(V + 5, T, V, "f32")
+    action = np.arange(T) % V
+    rf = np.full(T, -2.0, np.float32)
+    kw = dict(old_logp=dev(rf, torch.float32), ref_logp=dev(rf, torch.float32), adv=dev(np.ones(T), torch.float32), kl_coef=0.1)
+    want, _, _ = sg.sg_policy_loss(x, dev(action, torch.int32), **kw)
+    x[1, 1] = -float("inf")
+    x[2] = -float("inf")
+    for want_grad in (True, False):
+        loss, logp, g = sg.sg_policy_loss(x, dev(action, torch.int32), want_grad=want_grad, **kw)
+        assert (host(loss)[1:3] == np.inf).all() and (host(logp)[1:3] == -np.inf).all()
+        # without the gradient other threads add a row's terms
+        check(np.delete(host(loss), [1, 2]), np.delete(host(want), [1, 2]),
+              2 * sum_bound(V) * 2 * (1 + np.abs(np.delete(host(want), [1, 2]))), "the others' loss")
+        if want_grad:
+            assert not np.isfinite(host(g)[1, 1]) and np.isfinite(np.delete(host(g), [1, 2], 0)).all()
