@@ -541,7 +541,7 @@ int sg_stats_collect(const void* h_block, uint32_t n, uint64_t M, uint64_t total
  *            may be NULL where that is 0.
  * Sums: fp32 exponentials, 4 or 8 added in fp32, the rest and the row's
  * scalars in fp64.  Results do not depend on timing (no float atomics).
- * Limits: T < 2^31, 1 <= V < 2^31, ld and ld_grad < 2^40, 0 < inv_temp <= 1e6.
+ * Limits: T < 2^31, 1 <= V < 2^31, ld and ld_grad < 2^40, 1e-37 <= inv_temp <= 1e6.
  * T = 0 is a no-op.
  * ------------------------------------------------------------------------ */
 #define SG_ROWS_MAX_K 1024 /* longest list per row of sg_topk_rows and sg_distill_loss */

@@ -862,7 +862,8 @@ static int rows_args(const void* x, sg_dtype dt, uint64_t T, uint64_t V, uint64_
 {
     if (dt != SG_F32 && dt != SG_BF16) return SG_EINVAL;
     if (V == 0 || V >= (1ull << 31) || T >= (1ull << 31) || ld < V || ld >= (1ull << 40)) return SG_EINVAL;
-    if (!(inv_temp > 0.0) || !(inv_temp <= 1e6)) return SG_EINVAL;
+    // below 1e-37 the fp32 scale would lose its digits, then be 0: -inf * 0 = NaN
+    if (!(inv_temp >= 1e-37) || !(inv_temp <= 1e6)) return SG_EINVAL;
     if (T > 0 && (!x || reinterpret_cast<uintptr_t>(x) % row_esize(dt) != 0)) return SG_EINVAL;
     out->r.x = x;
     out->r.T = T;

@@ -318,3 +318,24 @@ def test_kl_of_an_action_of_probability_zero(T, V):
               2 * sum_bound(V) * 2 * (1 + np.abs(np.delete(host(want), [1, 2]))), "the others' loss")
         if want_grad:
             assert not np.isfinite(host(g)[1, 1]) and np.isfinite(np.delete(host(g), [1, 2], 0)).all()
+
+
+# ---------------------------------------------------------------------------
+# temperatures
+# ---------------------------------------------------------------------------
+def test_highest_temperatures():
+    """A uniform distribution over what is not masked, up to the limit; beyond it the call is refused."""
+    need_gpu()
+    x, xs = make_logits(7, 3, 1000, "f32")
+    x[:, ::2] = -float("inf")
+    action = torch.tensor([1, 3, 4], device="cuda", dtype=torch.int32)
+    uniform = -np.log(500.0)
+    for temp in (1e20, 1e30, 1e37):
+        idx, logp, lse = sg.sg_topk_rows(x, 500, temperature=temp)
+        check(host(logp), np.full((3, 500), uniform), sum_bound(1000) + 2.0 ** -24 * abs(uniform), "logp")
+        loss, logp, g = sg.sg_policy_loss(x, action, None, torch.ones(3, device="cuda"), temperature=temp)
+        check(host(logp), [uniform, uniform, -np.inf], sum_bound(1000) + 2.0 ** -24 * abs(uniform), "logp")
+        assert torch.isfinite(g).all()
+    for temp in (1.2e37, 1e39, 1e300):
+        with pytest.raises(sg.SgError):
+            sg.sg_topk_rows(x, 5, temperature=temp)
