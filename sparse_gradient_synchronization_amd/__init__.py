@@ -632,6 +632,8 @@ def _scratch(need, workspace, device):
     if workspace is None or workspace.numel() * workspace.element_size() < need:
         workspace = torch.empty(need, dtype=torch.uint8, device=device)
         return workspace, workspace.data_ptr(), need
+    if workspace.device != device or not workspace.is_contiguous():
+        raise ValueError("the workspace must be contiguous and on %s, got one on %s" % (device, workspace.device))
     return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
 
 

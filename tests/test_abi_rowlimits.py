@@ -13,3 +13,16 @@ def test_temperatures_whose_scale_fp32_cannot_hold(op):
         assert f(it=it) == SG_EINVAL, it
     for it in (1e-37, 1e-30, 1e6):
         assert f(it=it, T=0) == SG_OK, it
+
+
+def test_binding_refuses_a_workspace_elsewhere():
+    """A large enough workspace of another device, or one whose elements lie apart, is not written to."""
+    gpu = torch.device("cuda", 0)
+    with pytest.raises(ValueError):
+        sg._scratch(100, torch.zeros(200, dtype=torch.uint8), gpu)
+    cpu = torch.device("cpu")
+    with pytest.raises(ValueError):
+        sg._scratch(100, torch.zeros(400, dtype=torch.uint8)[::2], cpu)
+    ws = torch.zeros(50, dtype=torch.float32)
+    assert sg._scratch(200, ws, cpu) == (ws, ws.data_ptr(), 200)
+    assert sg._scratch(0, torch.zeros(2), gpu) == (None, None, 0)
