@@ -66,10 +66,11 @@ __device__ __forceinline__ uint32_t marked(const uint32_t* bm, uint32_t i0, int 
 // g is element lo).  kListed: tokens are listed, and left out of the
 // streaming pass's sum; a wave of its own handles the list.
 
-// log-probability of the logit za; a NaN in the row (its sum is NaN then) stays
+// log-probability of the logit za; a NaN in the row stays (its sum is NaN then, and
+// S - S: a comparison more put registers of the widest kernels out to memory)
 __device__ __forceinline__ double token_logp(const Rows& r, RowStat st, float za)
 {
-    return za == -INFINITY && st.s == st.s ? -(double)INFINITY : ((double)za - st.m) * r.it - row_log(st.s);
+    return za == -INFINITY ? (st.s - st.s) - (double)INFINITY : ((double)za - st.m) * r.it - row_log(st.s);
 }
 
 // ---------------------------------------------------------------------------
@@ -107,7 +108,7 @@ struct PolicyOp {
         const double lp = token_logp(r, st, za);
         const double w = weight ? (double)weight[row] : 1.0;
         const double A = adv ? (double)adv[row] : 0.0;
-        const double ratio = old_logp ? row_exp(lp - (double)old_logp[row]) : (S == S ? 1.0 : S);
+        const double ratio = old_logp ? row_exp(lp - (double)old_logp[row]) : (S - S) + 1.0; // 1, or NaN
         const double bounded = ratio < lo ? lo : (ratio > hi ? hi : ratio);
         const double a = ratio * A, b = bounded * A;
         double L = a <= b ? -a : (b <= a ? -b : a + b); // a NaN stays
@@ -271,12 +272,20 @@ struct DistillOp {
             const float v = i < V ? RowIO<E>::get(x + i) : -INFINITY;
             ls.z[j] = v;
             m = fmaxf(m, v);
-            if (mode == SG_DISTILL_RENORM && i < V) top = fmaxf(top, lp[j]);
+            const float t = lp[j]; // beside the logit's load, not after it
+            ls.p[j] = t;
+            if (i < V) top = fmaxf(top, t);
         }
+        if (mode == SG_DISTILL_RENORM) {
 #pragma unroll
-        for (int d = 1; d < SG_WAVE; d <<= 1) {
-            m = fmaxf(m, __shfl_xor(m, d, SG_WAVE));
-            top = fmaxf(top, __shfl_xor(top, d, SG_WAVE));
+            for (int d = 1; d < SG_WAVE; d <<= 1) { // both at once: the lanes' exchange is latency
+                m = fmaxf(m, __shfl_xor(m, d, SG_WAVE));
+                top = fmaxf(top, __shfl_xor(top, d, SG_WAVE));
+            }
+        } else {
+            top = 0.f;
+#pragma unroll
+            for (int d = 1; d < SG_WAVE; d <<= 1) m = fmaxf(m, __shfl_xor(m, d, SG_WAVE));
         }
         top = shift_of(top);
         const double shift = shift_of(m);
@@ -285,7 +294,7 @@ struct DistillOp {
         for (uint32_t j = lane_id(); j < k; j += SG_WAVE) {
             double p = 0.0;
             if (ls.id[j] < V) {
-                const double t = (double)lp[j] - top, d = (ls.z[j] - shift) * r.it;
+                const double t = (double)ls.p[j] - top, d = (ls.z[j] - shift) * r.it;
                 p = row_exp(t);
                 P += p;
                 if (p != 0.0) A += p * (t - d);
@@ -328,11 +337,11 @@ struct DistillOp {
         }
         if (write && l == 0) loss[row] = (float)(w * L);
         const double g = w * r.it;
-        const double all = (P + R) * per_S, near = all * __shfl(scale, 0);
+        const double below = __shfl(scale, 0), all = (P + R) * per_S, near = all * below;
         // The unlisted tokens' exponentials are taken from their own maximum.
         // From the row's they would be 0 in fp32 88 below it, and R / rest
         // beyond fp32's range, where together they are up to R.
-        return {st.m, (float)(g * (R != 0.0 ? near - R / st.s : near)), (float)(g * all), (float)(g * gp), m};
+        return {st.m, (float)(g * (R != 0.0 ? near - R * per_rest * below : near)), (float)(g * all), (float)(g * gp), m};
     }
     // ls.z[j] becomes the gradient of listed token j
     __device__ __forceinline__ void named_grad(const Rows& r, const RowCoef& co, RowList& ls) const
