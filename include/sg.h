@@ -34,6 +34,11 @@
  *   sg_preference_loss      losses over a vocabulary with their gradients (the
  *                           dense gradients the path starts from), and the
  *                           teacher's top logits that distillation takes
+ *   sg_linear_ce_loss       cross entropy of hidden states against a vocabulary
+ *                           head with both gradients, without the logits
+ *   sg_balance_loss         balance loss of a router with its counts and gradient
+ *   sg_orthogonalize        Newton-Schulz orthogonalisation of the update that a
+ *                           synchronized gradient becomes
  *
  * Sources: "Zen: Empowering Distributed Training with Sparsity-driven Data
  * Synchronization" (OSDI'25) digest page [Zen]; "SkipReduce: (Interconnection)
@@ -634,6 +639,106 @@ int sg_preference_loss(const void* d_logits, sg_dtype dt, uint64_t T, uint64_t V
                        const uint64_t* d_seq_off, uint32_t pairs, const float* d_ref_logp, const float* d_weight,
                        sg_pref_kind kind, double beta, double smoothing, int average, float* d_loss, float* d_logp,
                        void* d_grad, uint64_t ld_grad, void* d_ws, size_t ws_bytes, void* stream);
+
+/* Softmax cross entropy of hidden states against a vocabulary head, with the
+ * gradients of both, without [T, V] logits in memory.  With x_t the hidden
+ * state and w_v the head's row, z_tv = inv_temp * (x_t . w_v) and
+ * lse_t = log sum_v exp(z_tv):
+ *   L_t = weight_t (lse_t - z_t,label + z_coef lse_t^2)
+ *   g_tv = weight_t inv_temp ((1 + 2 z_coef lse_t) exp(z_tv - lse_t) - 1[v = label])
+ *   grad_hidden_t = sum_v g_tv w_v,  grad_head_v = sum_t g_tv x_t
+ * (the gradients of the sum of the losses).
+ *   d_hidden [T] rows of H of dt, ld_hidden elements apart
+ *   d_head   [V] rows of H of dt, ld_head apart
+ *   d_label  [T] i32.  A row whose label is outside [0, V), or of weight 0, is
+ *            not read: its loss, lse and grad_hidden are 0, it adds nothing to
+ *            grad_head.
+ *   d_weight [T] fp32 or NULL (every row 1)
+ *   d_loss [T], d_lse [T] fp32 out (d_lse may be NULL)
+ *   d_grad_hidden [T] rows of H of dt, ld_grad_hidden apart, or NULL; may be
+ *            d_hidden itself
+ *   d_grad_head [V] rows of H of dt, ld_grad_head apart, or NULL; must not
+ *            overlap the head
+ *   keep_bytes  how much of the workspace may hold exponentials between the
+ *            two passes (2 bytes an element of the T x V logits, 4 for
+ *            SG_F32).  If they fit, every product runs once; otherwise the
+ *            vocabulary is taken in pieces that fit (at least 256 tokens), and the
+ *            logits' product runs twice.
+ * A NaN, or an infinity that makes a logit of a row that counts +inf or NaN,
+ * makes the row's results NaN, and with them the whole grad_head.
+ * With SG_F32 every infinity in the head or in such a row does.
+ * Sums: products and exponentials in fp32, a row's sums and scalars in fp64.
+ * SG_BF16: g is rounded to bf16 once between the products; SG_F32: operands
+ * keep 22 bits under one power of two per tensor.  Results do not depend on timing.
+ * Rows of the head that start on 16 bytes (bf16, H and ld_head multiples of 8) are
+ * used as they lie; others are copied to the workspace first.
+ * Limits: T <= 2^24, V < 2^31, 1 <= H <= 2^20, T * V / 2048 < 2^31 (SG_EUNSUPPORTED);
+ * ld's < 2^40, 1e-37 <= inv_temp <= 1e6, 0 <= z_coef <= 1e6 (SG_EINVAL).  The
+ * workspace depends on the arguments of its query alone (d_head: its address).
+ * T = 0 writes grad_head = 0 and nothing else. */
+size_t sg_linear_ce_workspace_bytes(uint64_t T, uint64_t V, uint64_t H, sg_dtype dt, const void* d_head,
+                                    uint64_t ld_head, int want_hidden, int want_head, uint64_t keep_bytes);
+int sg_linear_ce_loss(const void* d_hidden, uint64_t ld_hidden, const void* d_head, uint64_t ld_head, sg_dtype dt,
+                      uint64_t T, uint64_t V, uint64_t H, double inv_temp, const int32_t* d_label,
+                      const float* d_weight, double z_coef, float* d_loss, float* d_lse, void* d_grad_hidden,
+                      uint64_t ld_grad_hidden, void* d_grad_head, uint64_t ld_grad_head, uint64_t keep_bytes,
+                      void* d_ws, size_t ws_bytes, void* stream);
+
+/* Balance loss of a router over its E experts, with the counts a router's
+ * bias update or a monitor takes.  With p_t the softmax of row t, N the rows that
+ * count, c_e how often expert e is listed in them, f_e = c_e / (k N) and
+ * P_e = sum_t p_te / N:
+ *   loss = balance_coef E sum_e f_e P_e + z_coef / N sum_t lse_t^2
+ * and its gradient with respect to the logits (f_e is a constant of it).
+ *   d_logits [T] rows of E logits of dt, ld elements apart
+ *   d_idx    [T][k] i32, each row's chosen experts (sg_topk_rows gives them); an
+ *            index outside [0, E) is not counted, one listed twice counts twice
+ *   d_live   [T] u8 or NULL (every row counts).  A row of 0 is not read, its
+ *            gradient is 0.
+ *   d_loss [1] fp32, d_counts [E] i32, d_prob [E] fp32 (P) out
+ *   d_grad   [T] rows of E of dt, ld_grad apart, or NULL; may be d_logits itself
+ *            with ld_grad == ld, otherwise they must not overlap
+ * No row that counts: loss, counts, P and gradient are 0.  A NaN or +inf in a
+ * row makes its gradient, P and the loss NaN; a logit of -inf has probability 0, a
+ * row of nothing else no softmax (NaN).
+ * Sums: fp32 within a row and over a block's rows, fp64 over blocks.
+ * Results do not depend on timing.
+ * Limits: 1 <= E, 1 <= k, T < 2^31, coefficients in [0, 1e6] (SG_EINVAL); E <= 1024, k <= E,
+ * T * k < 2^31 (SG_EUNSUPPORTED). */
+size_t sg_balance_workspace_bytes(uint64_t T, uint32_t E, uint32_t k, sg_dtype dt);
+int sg_balance_loss(const void* d_logits, sg_dtype dt, uint64_t T, uint32_t E, uint64_t ld, const int32_t* d_idx,
+                    uint32_t k, const uint8_t* d_live, double balance_coef, double z_coef, float* d_loss,
+                    int32_t* d_counts, float* d_prob, void* d_grad, uint64_t ld_grad, void* d_ws, size_t ws_bytes,
+                    void* stream);
+
+/* ------------------------------------------------------------------------
+ * The update that a synchronized gradient becomes.
+ * ------------------------------------------------------------------------ */
+
+/* Orthogonalises matrices by Newton-Schulz products, as the Muon optimiser
+ * does with its update:
+ *   X_0 = U / (|U|_F + eps),  X <- a X + (b G + c G^2) X,  G = X X^T,
+ * `steps` times; for a matrix taller than wide X <- a X + X (b G + c G^2),
+ * G = X^T X (the same singular values).  With (a, b, c) = (3.4445, -4.7750,
+ * 2.0315) and five steps the singular values end near 1.
+ *   d_update B matrices of m rows of n elements of dt, rows ld (>= n) and
+ *            matrices `stride` elements apart (not used for B = 1)
+ *   d_out    the results, ld_out and stride_out apart; may be d_update itself
+ *            with the same ld and stride, otherwise they must not overlap.
+ *            Elements between n and ld_out are left untouched.
+ * A matrix of zeros gives zeros (eps > 0).  A NaN or an infinity in a matrix
+ * makes that matrix's result NaN.
+ * Products take operands of 11 bits (SG_BF16) or 22 (SG_F32) with fp32 sums;
+ * the norm is summed in fp64; the result is rounded once.  Results do not
+ * depend on timing.
+ * Limits: 1 <= steps <= 64, 0 <= eps <= 1e6, B < 2^16, m and n up to 2^21 - 64, and
+ * coefficients whose iterates stay in the scales' range: singular values s up to
+ * 3.9, |a + b s^2 + c s^4| up to 4 and |b| s^2 + |c| s^4 up to 128, starting from
+ * [0, 1] (SG_EUNSUPPORTED otherwise).  B, m or n = 0 is a no-op. */
+size_t sg_orthogonalize_workspace_bytes(uint32_t B, uint32_t m, uint32_t n, sg_dtype dt);
+int sg_orthogonalize(const void* d_update, sg_dtype dt, uint32_t B, uint32_t m, uint32_t n, uint64_t ld,
+                     uint64_t stride, uint32_t steps, double a, double b, double c, double eps, void* d_out,
+                     uint64_t ld_out, uint64_t stride_out, void* d_ws, size_t ws_bytes, void* stream);
 
 #ifdef __cplusplus
 }

@@ -106,6 +106,15 @@ SIGNATURES = {
     "sg_preference_workspace_bytes": (_sz, [_u64, _u64, _int]),
     "sg_preference_loss": (_int, [_vp, _int, _u64, _u64, _u64, _vp, _vp, _u32, _vp, _vp, _int, _dbl, _dbl, _int, _vp,
                                   _vp, _vp, _u64, _vp, _sz, _vp]),
+    "sg_linear_ce_workspace_bytes": (_sz, [_u64, _u64, _u64, _int, _vp, _u64, _int, _int, _u64]),
+    "sg_linear_ce_loss": (_int, [_vp, _u64, _vp, _u64, _int, _u64, _u64, _u64, _dbl, _vp, _vp, _dbl, _vp, _vp, _vp,
+                                 _u64, _vp, _u64, _u64, _vp, _sz, _vp]),
+    "sg_balance_workspace_bytes": (_sz, [_u64, _u32, _u32, _int]),
+    "sg_balance_loss": (_int, [_vp, _int, _u64, _u32, _u64, _vp, _u32, _vp, _dbl, _dbl, _vp, _vp, _vp, _vp, _u64, _vp,
+                               _sz, _vp]),
+    "sg_orthogonalize_workspace_bytes": (_sz, [_u32, _u32, _u32, _int]),
+    "sg_orthogonalize": (_int, [_vp, _int, _u32, _u32, _u32, _u64, _u64, _u32, _dbl, _dbl, _dbl, _dbl, _vp, _u64,
+                                _u64, _vp, _sz, _vp]),
 }
 
 _lib = None
@@ -734,6 +743,132 @@ def sg_preference_loss(logits: torch.Tensor, label: torch.Tensor, seq_off: torch
                                 smoothing if kind == SG_PREF_SIGMOID else 0.0, 1 if average else 0, loss.data_ptr(),
                                 seq_logp.data_ptr(), p_grad, ldg, p_ws, n_ws, stream), "sg_preference_loss")
     return loss, seq_logp, grad
+
+
+def _gradient_like(name, of, want, grad):
+    """A gradient's tensor, address and row stride: allocated, the caller's, or none."""
+    if grad is None:
+        if not want:
+            return None, None, 0
+        grad = torch.empty(of.shape, dtype=of.dtype, device=of.device)
+    elif grad.dtype != of.dtype or grad.shape != of.shape or grad.get_device() != of.get_device():
+        raise ValueError("%s must have the type, shape and device of what it is the gradient of" % name)
+    ld, step = grad.stride()
+    rows, n = grad.shape
+    if n > 1 and step != 1 or rows > 1 and ld < n:
+        raise ValueError("%s must have contiguous rows (it is written in place)" % name)
+    return grad, grad.data_ptr(), (ld if rows > 1 else n)
+
+
+def sg_linear_ce_loss(hidden: torch.Tensor, head: torch.Tensor, label: torch.Tensor, weight=None,
+                      temperature: float = 1.0, z_coef: float = 0.0, want_grad: bool = True,
+                      grad_hidden: torch.Tensor | None = None, grad_head: torch.Tensor | None = None,
+                      keep_bytes: int = 4 << 30, workspace: torch.Tensor | None = None):
+    """Softmax cross entropy of hidden [T, H] against a vocabulary head [V, H]
+    (both float32 or both bfloat16) without the logits: label [T] int32
+    (outside [0, V): does not count), weight [T] float32 or None -> (loss [T]
+    float32, weighted; lse [T] float32; grad_hidden [T, H], grad_head [V, H]
+    of loss.sum(), or None).  grad_hidden, grad_head: where to write them
+    (grad_hidden: hidden itself included); with want_grad False only those
+    given are computed.  keep_bytes: workspace for exponentials kept between
+    the passes."""
+    _need_cuda(hidden, head)
+    L, dev, f = lib(), hidden.device, torch.float32
+    if hidden.dim() != 2 or head.dim() != 2 or hidden.shape[1] != head.shape[1]:
+        raise ValueError("hidden and head must be [T, H] and [V, H], got %s and %s" % (list(hidden.shape), list(head.shape)))
+    if head.dtype != hidden.dtype or head.get_device() != hidden.get_device():
+        raise ValueError("hidden and head must have one type and device")
+    if keep_bytes < 0:
+        raise ValueError("keep_bytes must not be negative, got %d" % keep_bytes)
+    grad_hidden, p_gx, ld_gx = _gradient_like("grad_hidden", hidden, want_grad, grad_hidden)
+    grad_head, p_gw, ld_gw = _gradient_like("grad_head", head, want_grad, grad_head)
+    hidden, dt, T, H, ldx = _rows(hidden)
+    head, _, V, _, ldw = _rows(head)
+    stream = _raw_stream(hidden)
+    label, p_label = _beside(hidden, "label", label, torch.int32, (T,))
+    weight, p_weight = _beside(hidden, "weight", weight, f, (T,))
+    loss = torch.empty(T, dtype=f, device=dev)
+    lse = torch.empty(T, dtype=f, device=dev)
+    need = L.sg_linear_ce_workspace_bytes(T, V, H, dt, head.data_ptr(), ldw, p_gx is not None, p_gw is not None,
+                                          keep_bytes)
+    ws, p_ws, n_ws = _scratch(need, workspace, dev)
+    _check(L.sg_linear_ce_loss(hidden.data_ptr(), ldx, head.data_ptr(), ldw, dt, T, V, H, _inv_temp(temperature),
+                               p_label, p_weight, z_coef, loss.data_ptr(), lse.data_ptr(), p_gx, ld_gx, p_gw, ld_gw,
+                               keep_bytes, p_ws, n_ws, stream), "sg_linear_ce_loss")
+    return loss, lse, grad_hidden, grad_head
+
+
+def sg_balance_loss(logits: torch.Tensor, idx: torch.Tensor, live: torch.Tensor | None = None,
+                    balance_coef: float = 0.01, z_coef: float = 0.0, want_grad: bool = True,
+                    grad: torch.Tensor | None = None, workspace: torch.Tensor | None = None):
+    """Balance loss of a router: logits [T, E], idx [T, k] int32 (the chosen
+    experts; outside [0, E): not counted), live [T] bool or None -> (loss [1]
+    float32; counts [E] int32; prob [E] float32, the mean probabilities; grad
+    [T, E] of the loss, or None).  grad: where to write the gradient, logits
+    itself included."""
+    _need_cuda(logits)
+    L, dev = lib(), logits.device
+    grad, p_grad, ldg = _grad_of(logits, want_grad, grad)
+    logits, dt, T, E, ld = _rows(logits)
+    stream = _raw_stream(logits)
+    k = idx.shape[-1]
+    idx, p_idx = _beside(logits, "idx", idx, torch.int32, (T, k))
+    live, p_live = _beside(logits, "live", live, torch.bool, (T,))
+    loss = torch.empty(1, dtype=torch.float32, device=dev)
+    counts = torch.empty(E, dtype=torch.int32, device=dev)
+    prob = torch.empty(E, dtype=torch.float32, device=dev)
+    ws, p_ws, n_ws = _scratch(L.sg_balance_workspace_bytes(T, E, k, dt), workspace, dev)
+    _check(L.sg_balance_loss(logits.data_ptr(), dt, T, E, ld, p_idx, k, p_live, balance_coef, z_coef, loss.data_ptr(),
+                             counts.data_ptr(), prob.data_ptr(), p_grad, ldg, p_ws, n_ws, stream), "sg_balance_loss")
+    return loss, counts, prob, grad
+
+
+# --------------------------------------------------------------------------
+# the update that a synchronized gradient becomes
+# --------------------------------------------------------------------------
+
+def _matrices(t: torch.Tensor):
+    """(matrices, rows, columns, row stride, matrix stride) of a tensor of two
+    or three dimensions that the library can address, else None."""
+    B = t.shape[0] if t.dim() == 3 else 1
+    m, n = t.shape[-2:]
+    ld, step = t.stride()[-2:]
+    if m <= 1:
+        ld = max(n, 1)
+    apart = t.stride(0) if B > 1 else 0
+    if n > 1 and step != 1 or ld < n or B > 1 and apart < (m - 1) * ld + n:
+        return None
+    return B, m, n, ld, apart
+
+
+def sg_orthogonalize(update: torch.Tensor, steps: int = 5, coef=(3.4445, -4.7750, 2.0315), eps: float = 1e-7,
+                     out: torch.Tensor | None = None, workspace: torch.Tensor | None = None):
+    """Newton-Schulz orthogonalisation: update [m, n] or [B, m, n]
+    float32/bfloat16 -> out of the same type and shape.  out: where to write
+    the result, update itself included."""
+    _need_cuda(update)
+    L, dev = lib(), update.device
+    if update.dim() not in (2, 3):
+        raise ValueError("update must be [m, n] or [B, m, n], got %d dimensions" % update.dim())
+    if len(coef) != 3:
+        raise ValueError("coef must hold three coefficients, got %d" % len(coef))
+    dt = _dtype_code(update)
+    if out is None:
+        out = torch.empty(update.shape, dtype=update.dtype, device=dev)
+    elif out.dtype != update.dtype or out.shape != update.shape or out.get_device() != update.get_device():
+        raise ValueError("out must have the update's type, shape and device")
+    src, dst = _matrices(update), _matrices(out)
+    if dst is None:
+        raise ValueError("out must have contiguous rows (it is written in place)")
+    if src is None:
+        update = update.contiguous()
+        src = _matrices(update)
+    stream = _raw_stream(update)
+    B, m, n, ld, apart = src
+    ws, p_ws, n_ws = _scratch(L.sg_orthogonalize_workspace_bytes(B, m, n, dt), workspace, dev)
+    _check(L.sg_orthogonalize(update.data_ptr(), dt, B, m, n, ld, apart, steps, coef[0], coef[1], coef[2], eps,
+                              out.data_ptr(), dst[3], dst[4], p_ws, n_ws, stream), "sg_orthogonalize")
+    return out
 
 
 def sg_validate_coo(idx: torch.Tensor, in_off: torch.Tensor, M: int) -> int:

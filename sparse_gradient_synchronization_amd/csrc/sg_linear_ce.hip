@@ -1,0 +1,725 @@
+// sg_linear_ce.hip -- softmax cross entropy of hidden states against a
+// vocabulary head, with both gradients, without the logits in memory:
+//   z_tv = x_t . w_v / temperature,  lse_t = log sum_v exp z_tv
+//   loss_t = weight_t (lse_t - z_ty + zc lse_t^2)
+//   g_tv = weight_t / temperature ((1 + 2 zc lse_t) exp(z_tv - lse_t) - 1[v = y_t])
+//   dx = g w,  dw = g^T x
+//
+// Three products of 2 T V H operations bound it for more than a few hundred
+// rows; below that the head is read and its gradient written.
+//
+// The rows that count are gathered first, so every product runs over them
+// alone (their number stays on the device: a block past it ends at once).
+// What goes from the first product to the other two:
+//   - per row and tile of the vocabulary the maximum and the sum of the
+//     exponentials, from the sums in registers; a row's are joined in fp64
+//   - the exponentials themselves, relative to their tile's maximum, in 16
+//     bits, while T x V of them fit in keep_bytes; a pass over them then makes
+//     g in place.  Otherwise the vocabulary is taken in pieces that fit, each
+//     with a second product of the logits that ends in g: 8 T V H operations
+//     instead of 6.
+// 16 bits for a number in [0, 1]: no sign, 6 bits of exponent (down to
+// 2^-63) and 10 of mantissa, so that keeping them (2^-12) adds little to the
+// one rounding of g to bf16 (2^-9) that the matrix instructions ask for.
+//
+// fp32: hidden states, head and g are two fp16 planes each under one power of
+// two per tensor (sg_gemm.h), which loses 2^-22 of each element down to 2^-17
+// of the tensor's largest and an absolute 2^-39 of it below.  The kept
+// exponentials are whole fp32 there, in the two planes of g.
+#include "sg_gemm.h"
+#include "sg_rows.h"
+
+namespace sg {
+
+// what the joined sums leave for a live row
+struct CeRow {
+    float m;    // maximum logit, before the temperature
+    float ls;   // log2 of the sum of exp2(c (x - m))
+    float a, b; // g = top (a p - b 1[v = y])
+};
+
+struct CeScal { // power-of-two scales of the fp32 planes and their inverses
+    uint32_t max_x, max_w, max_g; // bits of the largest magnitudes
+    uint32_t live;                // rows that count
+    // largest |weight / temperature| of the live rows: g is kept relative to it,
+    // so that with equal weights the label's -1 is a bf16 number and not 1 / N rounded
+    double top;
+};
+
+// the power of two that brings a largest magnitude to [2^12, 2^13)
+__device__ __forceinline__ int ce_exponent(uint32_t bits)
+{
+    const int e = (int)(bits >> 23 & 255) - 127;
+    if (bits >= 0x7f800000u) return 0; // an infinity or NaN spoils its products anyway
+    return 12 - (e < -126 ? -126 : e);
+}
+
+struct CeArgs {
+    const int32_t* label;
+    const float* weight;
+    float *loss, *lse;
+    uint64_t T;
+    uint32_t V;
+    double it, zc;
+    float c; // log2(e) / temperature
+};
+
+// The rows that count, in order: row[j], and pos[t] = j or -1.  The others'
+// loss is 0.  One block: T labels are little.
+__global__ __launch_bounds__(1024) void ce_rows_kernel(CeArgs p, uint32_t* row, int32_t* pos, CeScal* scal)
+{
+    __shared__ uint32_t count[16];
+    __shared__ float most[16];
+    uint32_t done = 0;
+    float top = 0.f;
+    const uint32_t w = threadIdx.x / 64;
+    for (uint64_t t0 = 0; t0 < p.T; t0 += 1024) {
+        const uint64_t t = t0 + threadIdx.x;
+        bool live = false;
+        if (t < p.T) {
+            const int32_t y = p.label[t];
+            const float wt = p.weight ? p.weight[t] : 1.f;
+            live = y >= 0 && (uint32_t)y < p.V && wt != 0.f;
+            if (live) top = fmaxf(top, fabsf(wt));
+        }
+        const uint64_t b = ballot(live);
+        __syncthreads();
+        if (threadIdx.x % 64 == 0) count[w] = popc64(b);
+        __syncthreads();
+        uint32_t before = done, all = 0;
+        for (uint32_t i = 0; i < 16; ++i) {
+            before += i < w ? count[i] : 0;
+            all += count[i];
+        }
+        done += all;
+        const uint32_t j = before + count_below(b);
+        if (live) row[j] = (uint32_t)t;
+        if (t < p.T) {
+            pos[t] = live ? (int32_t)j : -1;
+            if (!live) {
+                p.loss[t] = 0.f;
+                if (p.lse) p.lse[t] = 0.f;
+            }
+        }
+    }
+#pragma unroll
+    for (int d = 1; d < 64; d *= 2) top = fmaxf(top, __shfl_xor(top, d));
+    if (threadIdx.x % 64 == 0) most[w] = top;
+    __syncthreads();
+    if (threadIdx.x) return;
+    for (int i = 0; i < 16; ++i) top = fmaxf(top, most[i]);
+    *scal = {0u, 0u, 0u, done, (double)top * p.it};
+}
+
+// rows of a user's matrix
+struct CeSrc {
+    const void* x;
+    uint64_t ld;
+    uint32_t n;   // elements of a row
+    bool wide;    // rows start on 16 bytes
+};
+template <typename E>
+__device__ __forceinline__ void ce_load8(const CeSrc& s, uint64_t r, uint32_t c, float* v)
+{
+    const E* x = static_cast<const E*>(s.x) + r * s.ld + c;
+    if (s.wide && c + 8 <= s.n) {
+        constexpr int VEC = RowIO<E>::VEC;
+#pragma unroll
+        for (int i = 0; i < 8; i += VEC) RowIO<E>::unpack(load_chunk(x + i), v + i);
+        return;
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = c + i < s.n ? RowIO<E>::get(x + i) : 0.f;
+}
+
+// the largest magnitude of the rows (of the live ones: row != NULL)
+__global__ __launch_bounds__(256) void ce_max_kernel(CeSrc s, uint64_t rows, const uint32_t* row, const CeScal* scal,
+                                                     uint32_t* out)
+{
+    const uint64_t n = row ? scal->live : rows;
+    const uint32_t per = (s.n + 7) / 8;
+    uint32_t m = 0;
+    for (uint64_t i = blockIdx.x * 256ull + threadIdx.x; i < n * per; i += gridDim.x * 256ull) {
+        float v[8];
+        const uint64_t r = i / per;
+        ce_load8<float>(s, row ? row[r] : r, (uint32_t)(i % per) * 8, v);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            const uint32_t b = __float_as_uint(v[k]) & 0x7fffffffu;
+            m = b > m ? b : m;
+        }
+    }
+#pragma unroll
+    for (int d = 1; d < 64; d *= 2) {
+        const uint32_t o = __shfl_xor(m, d);
+        m = o > m ? o : m;
+    }
+    // a maximum of whole numbers: the order of the blocks does not matter
+    if (threadIdx.x % 64 == 0 && m > *(volatile uint32_t*)out) atomicMax(out, m);
+}
+
+// Rows as planes: gathered (row != NULL; rows up to the next multiple of 64 are
+// zeros), columns padded with zeros to np.
+template <typename E>
+__global__ __launch_bounds__(256) void ce_pack_kernel(CeSrc s, uint64_t rows, const uint32_t* row, const CeScal* scal,
+                                                      const uint32_t* max_bits, uint16_t* hi, uint16_t* lo,
+                                                      uint32_t np)
+{
+    const uint64_t n = row ? scal->live : rows, padded = row ? (n + 63) / 64 * 64 : n;
+    const uint32_t per = np / 8;
+    const int e = lo ? ce_exponent(*max_bits) : 0;
+    for (uint64_t i = blockIdx.x * 256ull + threadIdx.x; i < padded * per; i += gridDim.x * 256ull) {
+        const uint64_t r = i / per;
+        const uint32_t c = (uint32_t)(i % per) * 8;
+        float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+        if (r < n && c < s.n) ce_load8<E>(s, row ? row[r] : r, c, v);
+        if (lo) {
+            s16x8 h, l;
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                uint16_t x, y;
+                split_f16(ldexpf(v[k], e), &x, &y);
+                h[k] = (short)x;
+                l[k] = (short)y;
+            }
+            *reinterpret_cast<s16x8*>(hi + r * np + c) = h;
+            *reinterpret_cast<s16x8*>(lo + r * np + c) = l;
+        } else {
+            *reinterpret_cast<u32x4*>(hi + r * np + c) = RowIO<bf16_bits>::pack(v);
+        }
+    }
+}
+
+// a number in [0, 1] in 16 bits, and back; below 2^-63 it is 0
+__device__ __forceinline__ uint16_t ce_code(float e)
+{
+    const uint32_t b = __float_as_uint(e);
+    return (uint16_t)((b < 0x20000000u ? 0u : b - 0x20000000u + 0x1000u) >> 13);
+}
+__device__ __forceinline__ float ce_decode(uint32_t code)
+{
+    return code ? __uint_as_float((code << 13) + 0x20000000u) : 0.f;
+}
+
+// g and the exponentials it comes from: rows of ld
+struct CeG {
+    uint16_t *hi, *lo;
+    uint64_t ld;
+};
+
+// where the logits' products end: statistics (and exponentials), or g
+struct CeLogitsEpi {
+    const uint32_t* row;
+    const int32_t* label;
+    const CeScal* scal;
+    float2* stat; // [rows][groups]
+    float* zy;    // [rows] the label's logit
+    const CeRow* info; // not NULL: g, from the joined sums
+    CeG g;        // hi NULL: keep nothing
+    uint32_t groups, v0, Vp; // v0: first token of this piece; Vp: its padded end in g
+    bool planes;
+    float c;
+
+    template <class Cfg>
+    __device__ __forceinline__ void run(f32x4 (&acc)[Cfg::MT][Cfg::NTT], const TileAt& at) const
+    {
+        const uint32_t l = threadIdx.x % 64;
+        const int unit = planes ? -ce_exponent(scal->max_x) - ce_exponent(scal->max_w) : 0;
+        const int gexp = planes && info ? ce_exponent(scal->max_g) : 0;
+        float mx[Cfg::MT], sum[Cfg::MT];
+        float* const lm = reinterpret_cast<float*>(at.lds);  // [WN][BM]
+        float* const ls = lm + Cfg::WN * Cfg::BM;
+#pragma unroll
+        for (int i = 0; i < Cfg::MT; ++i) {
+            const uint32_t m = at.m0 + i * 16 + l % 16;
+            const bool in = m < at.M;
+            const uint32_t y = in ? (uint32_t)label[row[m]] - v0 : 0xffffffffu; // in this piece, if below N
+            const CeRow r = in && info ? info[m] : CeRow{0.f, 0.f, 0.f, 0.f};
+            mx[i] = -INFINITY;
+#pragma unroll
+            for (int j = 0; j < Cfg::NTT; ++j) {
+                const uint32_t n = at.n0 + j * 16 + l / 16 * 4;
+                float v[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    v[k] = planes ? ldexpf(acc[i][j][k], unit) : acc[i][j][k];
+                    if (!info && n + k == y) zy[m] = v[k];
+                    if (n + k >= at.N) v[k] = -INFINITY;
+                    if (info) {
+                        v[k] = r.a * exp2_fast(c * (v[k] - r.m) - r.ls) - (n + k == y ? r.b : 0.f);
+                    }
+                    mx[i] = fmaxf(mx[i], v[k]);
+                    acc[i][j][k] = v[k];
+                }
+                if (info && in && n < Vp) put_g(m, n, v, gexp);
+            }
+        }
+        if (info) return;
+        // the rows' maxima over the block's columns
+#pragma unroll
+        for (int i = 0; i < Cfg::MT; ++i) {
+            mx[i] = fmaxf(mx[i], __shfl_xor(mx[i], 16));
+            mx[i] = fmaxf(mx[i], __shfl_xor(mx[i], 32));
+            if (l < 16) lm[at.wn * Cfg::BM + at.m0 - at.bm0 + i * 16 + l] = mx[i];
+        }
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < Cfg::MT; ++i) {
+            const uint32_t q = at.m0 - at.bm0 + i * 16 + l % 16;
+#pragma unroll
+            for (int w = 0; w < Cfg::WN; ++w) mx[i] = fmaxf(mx[i], lm[w * Cfg::BM + q]);
+            const float shift = shift_of(mx[i]);
+            sum[i] = 0.f;
+#pragma unroll
+            for (int j = 0; j < Cfg::NTT; ++j) {
+                const uint32_t n = at.n0 + j * 16 + l / 16 * 4;
+                float e[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) e[k] = exp2_fast(c * (acc[i][j][k] - shift));
+                sum[i] += (e[0] + e[1]) + (e[2] + e[3]);
+                if (g.hi && at.bm0 + q < at.M && n < Vp) keep(at.bm0 + q, n, e);
+            }
+            sum[i] += __shfl_xor(sum[i], 16);
+            sum[i] += __shfl_xor(sum[i], 32);
+            if (l < 16) ls[at.wn * Cfg::BM + q] = sum[i];
+        }
+        __syncthreads();
+        if (at.wn == 0 && l < 16) {
+#pragma unroll
+            for (int i = 0; i < Cfg::MT; ++i) {
+                const uint32_t q = at.m0 - at.bm0 + i * 16 + l;
+                float s = 0.f;
+#pragma unroll
+                for (int w = 0; w < Cfg::WN; ++w) s += ls[w * Cfg::BM + q];
+                if (at.bm0 + q < at.M)
+                    stat[(uint64_t)(at.bm0 + q) * groups + (v0 + at.bn0) / Cfg::BN] = make_float2(mx[i], s);
+            }
+        }
+    }
+    __device__ __forceinline__ void put_g(uint32_t m, uint32_t n, const float* v, int gexp) const
+    {
+        s16x4 h, q;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            if (g.lo) {
+                uint16_t x, y;
+                split_f16(ldexpf(v[k], gexp), &x, &y);
+                h[k] = (short)x;
+                q[k] = (short)y;
+            } else {
+                h[k] = __builtin_bit_cast(short, (__bf16)v[k]);
+            }
+        }
+        *reinterpret_cast<s16x4*>(g.hi + m * g.ld + n) = h;
+        if (g.lo) *reinterpret_cast<s16x4*>(g.lo + m * g.ld + n) = q;
+    }
+    __device__ __forceinline__ void keep(uint32_t m, uint32_t n, const float* e) const
+    {
+        s16x4 h, q;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            if (g.lo) {
+                h[k] = (short)(__float_as_uint(e[k]) >> 16);
+                q[k] = (short)__float_as_uint(e[k]);
+            } else {
+                h[k] = (short)ce_code(e[k]);
+            }
+        }
+        *reinterpret_cast<s16x4*>(g.hi + m * g.ld + n) = h;
+        if (g.lo) *reinterpret_cast<s16x4*>(g.lo + m * g.ld + n) = q;
+    }
+};
+
+// A live row's statistics joined: loss, lse and what g needs.  A block a row.
+__global__ __launch_bounds__(256) void ce_join_kernel(CeArgs p, const uint32_t* row, const float2* stat,
+                                                      uint32_t groups, const float* zy, CeRow* info, CeScal* scal,
+                                                      bool planes)
+{
+    const uint32_t j = blockIdx.x;
+    if (j >= scal->live) return;
+    __shared__ float sm[4];
+    __shared__ double ss[4];
+    float m = -INFINITY;
+    for (uint32_t i = threadIdx.x; i < groups; i += 256) m = fmaxf(m, stat[(uint64_t)j * groups + i].x);
+#pragma unroll
+    for (int d = 1; d < 64; d *= 2) m = fmaxf(m, __shfl_xor(m, d));
+    if (threadIdx.x % 64 == 0) sm[threadIdx.x / 64] = m;
+    __syncthreads();
+    m = fmaxf(fmaxf(sm[0], sm[1]), fmaxf(sm[2], sm[3]));
+    const float shift = shift_of(m);
+    double s = 0.0;
+    for (uint32_t i = threadIdx.x; i < groups; i += 256) {
+        const float2 q = stat[(uint64_t)j * groups + i];
+        s += (double)q.y * exp2_fast(p.c * (q.x - shift)); // q.x = -inf: its sum is 0, its factor 0
+    }
+#pragma unroll
+    for (int d = 1; d < 64; d *= 2) s += __shfl_xor(s, d);
+    if (threadIdx.x % 64 == 0) ss[threadIdx.x / 64] = s;
+    __syncthreads();
+    if (threadIdx.x) return;
+    s = ss[0] + ss[1] + ss[2] + ss[3];
+    const uint32_t t = row[j];
+    const double w = p.weight ? (double)p.weight[t] : 1.0, lse = p.it * (double)shift + log(s);
+    p.loss[t] = (float)(w * (lse - p.it * (double)zy[j] + p.zc * lse * lse));
+    if (p.lse) p.lse[t] = (float)lse;
+    if (!info) return;
+    const double b = w * p.it / scal->top;
+    const CeRow r = {shift, (float)log2(s), (float)(b * (1.0 + 2.0 * p.zc * lse)), (float)b};
+    info[j] = r;
+    // a maximum of whole numbers: the order of the rows does not matter
+    if (planes) atomicMax(&scal->max_g, __float_as_uint(fmaxf(fabsf(r.a), fabsf(r.b))));
+}
+
+// kept exponentials -> g, in place; rows up to the next multiple of 64 are
+// zeros.  A block takes 2048 columns of a row.
+__global__ __launch_bounds__(256) void ce_grad_kernel(const uint32_t* row, const int32_t* label, const float2* stat,
+                                                      uint32_t groups, uint32_t group_cols, const CeRow* info,
+                                                      const CeScal* scal, CeG g, uint32_t Vp, float c)
+{
+    const uint32_t cols = (Vp + 2047) / 2048, j = blockIdx.x / cols, v0 = (blockIdx.x % cols) * 2048 + threadIdx.x * 8;
+    const uint32_t live = scal->live;
+    if (j >= (live + 63) / 64 * 64 || v0 >= Vp) return;
+    u32x4* const hi = reinterpret_cast<u32x4*>(g.hi + j * g.ld + v0);
+    u32x4* const lo = g.lo ? reinterpret_cast<u32x4*>(g.lo + j * g.ld + v0) : nullptr;
+    if (j >= live) {
+        *hi = u32x4{0, 0, 0, 0};
+        if (lo) *lo = u32x4{0, 0, 0, 0};
+        return;
+    }
+    const CeRow r = info[j];
+    const uint32_t y = (uint32_t)label[row[j]];
+    // a group past the vocabulary's end (padding columns): its exponentials are 0
+    const uint32_t grp = v0 / group_cols;
+    const float scale = grp < groups ? r.a * exp2_fast(c * (stat[(uint64_t)j * groups + grp].x - r.m) - r.ls) : 0.f;
+    const u32x4 h = grp < groups ? *hi : u32x4{0, 0, 0, 0};
+    float v[8];
+    if (lo) {
+        const u32x4 q = grp < groups ? *lo : u32x4{0, 0, 0, 0};
+        const int gexp = ce_exponent(scal->max_g);
+        s16x8 oh, ol;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const uint32_t bits = (h[i / 2] >> (i % 2 * 16) << 16) | (q[i / 2] >> (i % 2 * 16) & 0xffffu);
+            v[i] = scale * __uint_as_float(bits) - (v0 + i == y ? r.b : 0.f);
+            uint16_t a, b;
+            split_f16(ldexpf(v[i], gexp), &a, &b);
+            oh[i] = (short)a;
+            ol[i] = (short)b;
+        }
+        *hi = __builtin_bit_cast(u32x4, oh);
+        *lo = __builtin_bit_cast(u32x4, ol);
+        return;
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        v[i] = scale * ce_decode(h[i / 2] >> (i % 2 * 16) & 0xffffu) - (v0 + i == y ? r.b : 0.f);
+    *hi = RowIO<bf16_bits>::pack(v);
+}
+
+// rows live .. next multiple of 64 of g as zeros (pieces: their product left them)
+__global__ __launch_bounds__(256) void ce_zero_kernel(const CeScal* scal, CeG g, uint32_t Vp)
+{
+    const uint32_t live = scal->live, end = (live + 63) / 64 * 64;
+    const uint32_t per = Vp / 8;
+    for (uint64_t i = blockIdx.x * 256ull + threadIdx.x; i < (uint64_t)(end - live) * per; i += gridDim.x * 256ull) {
+        const uint64_t at = (live + i / per) * g.ld + i % per * 8;
+        *reinterpret_cast<u32x4*>(g.hi + at) = u32x4{0, 0, 0, 0};
+        if (g.lo) *reinterpret_cast<u32x4*>(g.lo + at) = u32x4{0, 0, 0, 0};
+    }
+}
+
+// sums of dx, one set per part of the vocabulary; later pieces add to them
+struct CeHiddenEpi {
+    float* part; // [splits][rows][ld]
+    uint64_t ld, rows;
+    bool add;
+    template <class Cfg>
+    __device__ __forceinline__ void run(const f32x4 (&acc)[Cfg::MT][Cfg::NTT], const TileAt& at) const
+    {
+        const uint32_t l = threadIdx.x % 64;
+#pragma unroll
+        for (int i = 0; i < Cfg::MT; ++i)
+#pragma unroll
+            for (int j = 0; j < Cfg::NTT; ++j) {
+                const uint32_t m = at.m0 + i * 16 + l % 16, n = at.n0 + j * 16 + l / 16 * 4;
+                if (m >= at.M || n >= ld) continue; // ld: H rounded up
+                f32x4* q = reinterpret_cast<f32x4*>(part + (at.split * rows + m) * ld + n);
+                *q = add ? *q + acc[i][j] : acc[i][j];
+            }
+    }
+};
+
+// dx of every row from its sums
+template <typename E>
+__global__ __launch_bounds__(256) void ce_hidden_kernel(const int32_t* pos, const CeScal* scal, const float* part,
+                                                        uint64_t ldp, uint64_t rows, uint32_t splits, bool planes,
+                                                        E* out, uint64_t ld, uint32_t H)
+{
+    const uint64_t t = blockIdx.x;
+    const int32_t j = pos[t];
+    const int unit = planes ? -ce_exponent(scal->max_g) - ce_exponent(scal->max_w) : 0;
+    for (uint32_t h = threadIdx.x; h < H; h += 256) {
+        float s = 0.f;
+        if (j >= 0)
+            for (uint32_t k = 0; k < splits; ++k) s += part[(k * rows + (uint32_t)j) * ldp + h];
+        RowIO<E>::put(out + t * ld + h, j >= 0 ? ldexpf(s, unit) * (float)scal->top : 0.f);
+    }
+}
+
+// dw, rounded once to the caller's type
+struct CeHeadEpi {
+    const CeScal* scal;
+    void* out;
+    uint64_t ld;
+    bool planes, wide; // wide: four neighbours are stored at once
+    template <class Cfg>
+    __device__ __forceinline__ void run(const f32x4 (&acc)[Cfg::MT][Cfg::NTT], const TileAt& at) const
+    {
+        const uint32_t l = threadIdx.x % 64;
+        const int unit = planes ? -ce_exponent(scal->max_g) - ce_exponent(scal->max_x) : 0;
+        const float top = (float)scal->top;
+#pragma unroll
+        for (int i = 0; i < Cfg::MT; ++i)
+#pragma unroll
+            for (int j = 0; j < Cfg::NTT; ++j) {
+                const uint32_t m = at.m0 + i * 16 + l % 16, n = at.n0 + j * 16 + l / 16 * 4;
+                if (m >= at.M || n >= at.N) continue;
+                f32x4 v = acc[i][j];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) v[k] = ldexpf(v[k], unit) * top;
+                if (planes) {
+                    float* q = static_cast<float*>(out) + m * ld + n;
+                    if (wide && n + 4 <= at.N) *reinterpret_cast<f32x4*>(q) = v;
+                    else
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            if (n + k < at.N) q[k] = v[k];
+                } else {
+                    uint16_t* q = static_cast<uint16_t*>(out) + m * ld + n;
+                    s16x4 w;
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) w[k] = __builtin_bit_cast(short, (__bf16)v[k]);
+                    if (wide && n + 4 <= at.N) *reinterpret_cast<s16x4*>(q) = w;
+                    else
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            if (n + k < at.N) q[k] = (uint16_t)w[k];
+                }
+            }
+    }
+};
+
+// zeros where there is no row at all
+template <typename E>
+__global__ __launch_bounds__(256) void ce_no_rows_kernel(E* out, uint64_t ld, uint64_t V, uint32_t H)
+{
+    for (uint64_t i = blockIdx.x * 256ull + threadIdx.x; i < V * H; i += gridDim.x * 256ull)
+        RowIO<E>::put(out + i / H * ld + i % H, 0.f);
+}
+
+// sizes and buffers of a call
+struct CePlan {
+    uint32_t H, Hp, Tp, piece; // Hp, Tp: rounded up to 64; piece: columns of g
+    uint32_t groups, splits;
+    bool two, pack, kept, grads, hidden;
+    int tile; // of the logits' product: 0 large, 1 middle, 2 few rows
+    CeScal* scal;
+    uint32_t* row;
+    int32_t* pos;
+    float *zy, *part;
+    float2* stat;
+    CeRow* info;
+    uint16_t *x[2], *w[2], *g[2];
+};
+
+static int ce_tile_cols(int tile) { return tile == 0 ? 256 : 128; }
+
+static CePlan ce_plan(Carver& cv, uint64_t T, uint64_t V, uint32_t H, sg_dtype dt, const void* head, uint64_t ld_head,
+                      bool hidden, bool dhead, uint64_t keep)
+{
+    CePlan p = {};
+    p.H = H;
+    p.Hp = (uint32_t)align_up(H, 64);
+    p.Tp = (uint32_t)align_up(T, 64);
+    p.two = dt == SG_F32;
+    p.hidden = hidden;
+    p.grads = hidden || dhead;
+    // the head as it lies: bf16 rows that start on 16 bytes, near enough to one another
+    p.pack = p.two || H % 8 || ld_head % 8 || reinterpret_cast<uintptr_t>(head) % 16 || ld_head > GEMM_MAX_LD;
+    p.tile = T <= 32 ? 2 : ceil_div(T, 256) * ceil_div(V, 256) >= 256 ? 0 : 1;
+    p.groups = (uint32_t)ceil_div(V, ce_tile_cols(p.tile));
+    const uint64_t Vp = align_up(V, 256), es = p.two ? 4 : 2;
+    p.kept = Vp <= (1u << 20) && p.Tp * Vp * es <= keep;
+    if (p.kept) {
+        p.piece = (uint32_t)Vp;
+    } else {
+        uint64_t c = keep / (p.Tp * es) / 256 * 256;
+        c = c < 256 ? 256 : c > (1u << 20) ? (1u << 20) : c;
+        p.piece = (uint32_t)(c < Vp ? c : Vp);
+    }
+    // dx has few tiles and a long sum: the vocabulary in parts until there are blocks enough
+    const uint64_t tiles = p.tile == 2 ? ceil_div(p.Hp, 128) : ceil_div(p.Tp, 128) * ceil_div(p.Hp, 128);
+    const uint64_t want = ceil_div(512, tiles), most = ceil_div(p.piece, 512);
+    p.splits = (uint32_t)(want < most ? want : most);
+
+    p.scal = cv.take<CeScal>(1);
+    p.row = cv.take<uint32_t>(p.Tp);
+    p.pos = cv.take<int32_t>(p.Tp);
+    p.zy = cv.take<float>(p.Tp);
+    p.stat = cv.take<float2>((uint64_t)p.Tp * p.groups);
+    p.info = p.grads ? cv.take<CeRow>(p.Tp) : nullptr;
+    for (int i = 0; i < (p.two ? 2 : 1); ++i) {
+        p.x[i] = cv.take<uint16_t>((uint64_t)p.Tp * p.Hp);
+        p.w[i] = p.pack ? cv.take<uint16_t>(V * p.Hp) : nullptr;
+        p.g[i] = p.grads ? cv.take<uint16_t>((uint64_t)p.Tp * p.piece) : nullptr;
+    }
+    p.part = hidden ? cv.take<float>((uint64_t)p.splits * p.Tp * p.Hp) : nullptr;
+    return p;
+}
+
+template <int AL, int BL, class Epi>
+static int ce_product(const CePlan& p, int tile, const Gemm& g, const Epi& e, hipStream_t st)
+{
+    if (tile == 0)
+        return p.two ? launch_gemm<TileL, AL, BL, true>(g, 1, e, st) : launch_gemm<TileL, AL, BL, false>(g, 1, e, st);
+    if (tile == 1)
+        return p.two ? launch_gemm<TileM, AL, BL, true>(g, 1, e, st) : launch_gemm<TileM, AL, BL, false>(g, 1, e, st);
+    return p.two ? launch_gemm<TileRow, AL, BL, true>(g, 1, e, st) : launch_gemm<TileRow, AL, BL, false>(g, 1, e, st);
+}
+
+static bool ce_sizes(uint64_t T, uint64_t V, uint64_t H, sg_dtype dt)
+{
+    return T < (1ull << 31) && V > 0 && V < (1ull << 31) && H > 0 && (dt == SG_F32 || dt == SG_BF16);
+}
+static bool ce_supported(uint64_t T, uint64_t V, uint64_t H)
+{
+    // blocks of 128 x 128 tiles, and of 2048 columns of a row
+    return H <= (1u << 20) && T <= (1u << 24) && ceil_div(T, 32) * ceil_div(V, 128) < (1ull << 31) &&
+           align_up(T, 64) * ceil_div(V, 2048) < (1ull << 31);
+}
+
+} // namespace sg
+
+using namespace sg;
+
+extern "C" size_t sg_linear_ce_workspace_bytes(uint64_t T, uint64_t V, uint64_t H, sg_dtype dt, const void* d_head,
+                                               uint64_t ld_head, int want_hidden, int want_head, uint64_t keep_bytes)
+{
+    if (T == 0 || !ce_sizes(T, V, H, dt) || !ce_supported(T, V, H)) return 0;
+    Carver cv(nullptr);
+    ce_plan(cv, T, V, (uint32_t)H, dt, d_head, ld_head, want_hidden != 0, want_head != 0, keep_bytes);
+    return cv.bytes();
+}
+
+extern "C" int sg_linear_ce_loss(const void* d_hidden, uint64_t ld_hidden, const void* d_head, uint64_t ld_head,
+                                 sg_dtype dt, uint64_t T, uint64_t V, uint64_t H, double inv_temp,
+                                 const int32_t* d_label, const float* d_weight, double z_coef, float* d_loss,
+                                 float* d_lse, void* d_grad_hidden, uint64_t ld_grad_hidden, void* d_grad_head,
+                                 uint64_t ld_grad_head, uint64_t keep_bytes, void* d_ws, size_t ws_bytes, void* stream)
+{
+    if (!ce_sizes(T, V, H, dt)) return SG_EINVAL;
+    if (!(inv_temp >= 1e-37) || !(inv_temp <= 1e6) || !(z_coef >= 0.0) || !(z_coef <= 1e6)) return SG_EINVAL;
+    const uint64_t es = dt == SG_F32 ? 4 : 2, far = 1ull << 40;
+    if (ld_hidden < H || ld_hidden >= far || ld_head < H || ld_head >= far) return SG_EINVAL;
+    if (d_grad_hidden && (ld_grad_hidden < H || ld_grad_hidden >= far)) return SG_EINVAL;
+    if (d_grad_head && (ld_grad_head < H || ld_grad_head >= far)) return SG_EINVAL;
+    for (const void* q : {d_hidden, d_head, (const void*)d_grad_hidden, (const void*)d_grad_head})
+        if (reinterpret_cast<uintptr_t>(q) % es) return SG_EINVAL;
+    if (!d_head || (T > 0 && (!d_hidden || !d_label || !d_loss))) return SG_EINVAL;
+    if (d_grad_head && d_grad_head == d_head) return SG_EINVAL; // the head is read to the end
+    if (!ce_supported(T, V, H)) return SG_EUNSUPPORTED;
+    hipStream_t st = as_stream(stream);
+    if (T == 0) {
+        if (!d_grad_head) return SG_OK;
+        if (dt == SG_F32) ce_no_rows_kernel<float><<<2048, 256, 0, st>>>((float*)d_grad_head, ld_grad_head, V, (uint32_t)H);
+        else ce_no_rows_kernel<bf16_bits><<<2048, 256, 0, st>>>((bf16_bits*)d_grad_head, ld_grad_head, V, (uint32_t)H);
+        SG_TRY_LAUNCH();
+        return SG_OK;
+    }
+    if (!d_ws) return SG_EINVAL;
+    if (ws_bytes < sg_linear_ce_workspace_bytes(T, V, H, dt, d_head, ld_head, d_grad_hidden != nullptr, d_grad_head != nullptr, keep_bytes))
+        return SG_ECAPACITY;
+    Carver cv(d_ws);
+    const CePlan p = ce_plan(cv, T, V, (uint32_t)H, dt, d_head, ld_head, d_grad_hidden != nullptr, d_grad_head != nullptr, keep_bytes);
+    const float c = (float)(inv_temp * 1.4426950408889634);
+    const CeArgs a = {d_label, d_weight, d_loss, d_lse, T, (uint32_t)V, inv_temp, z_coef, c};
+    const auto wide = [&](const void* q, uint64_t ld, uint64_t b) { return reinterpret_cast<uintptr_t>(q) % b == 0 && ld * es % b == 0; };
+
+    ce_rows_kernel<<<1, 1024, 0, st>>>(a, p.row, p.pos, p.scal);
+    SG_TRY_LAUNCH();
+    const CeSrc sx = {d_hidden, ld_hidden, p.H, wide(d_hidden, ld_hidden, 16)},
+                sw = {d_head, ld_head, p.H, wide(d_head, ld_head, 16)};
+    const auto blocks = [](uint64_t items) { const uint64_t b = ceil_div(items, 256); return (unsigned)(b < 8192 ? b : 8192); };
+    const unsigned bx = blocks((uint64_t)p.Tp * p.Hp / 8), bw = blocks(V * p.Hp / 8);
+    if (p.two) {
+        ce_max_kernel<<<bx < 1024 ? bx : 1024, 256, 0, st>>>(sx, T, p.row, p.scal, &p.scal->max_x);
+        SG_TRY_LAUNCH();
+        ce_max_kernel<<<bw < 2048 ? bw : 2048, 256, 0, st>>>(sw, V, nullptr, p.scal, &p.scal->max_w);
+        SG_TRY_LAUNCH();
+        ce_pack_kernel<float><<<bx, 256, 0, st>>>(sx, T, p.row, p.scal, &p.scal->max_x, p.x[0], p.x[1], p.Hp);
+        SG_TRY_LAUNCH();
+        ce_pack_kernel<float><<<bw, 256, 0, st>>>(sw, V, nullptr, p.scal, &p.scal->max_w, p.w[0], p.w[1], p.Hp);
+        SG_TRY_LAUNCH();
+    } else {
+        ce_pack_kernel<bf16_bits><<<bx, 256, 0, st>>>(sx, T, p.row, p.scal, nullptr, p.x[0], nullptr, p.Hp);
+        SG_TRY_LAUNCH();
+        if (p.pack) {
+            ce_pack_kernel<bf16_bits><<<bw, 256, 0, st>>>(sw, V, nullptr, p.scal, nullptr, p.w[0], nullptr, p.Hp);
+            SG_TRY_LAUNCH();
+        }
+    }
+    const uint32_t nseg = p.two ? 3 : 1;
+    const uint64_t ldw = p.pack ? p.Hp : ld_head;
+    const uint16_t* const w0 = p.pack ? p.w[0] : static_cast<const uint16_t*>(d_head);
+    // rows v0 .. v0 + n of the head
+    const auto head = [&](uint64_t v0, uint64_t n) {
+        return Mat{{w0 + v0 * ldw, p.w[1] ? p.w[1] + v0 * ldw : nullptr}, ldw, (n - 1) * ldw + (p.pack ? p.Hp : H), 0};
+    };
+    const Mat mx = {{p.x[0], p.x[1]}, p.Hp, (uint64_t)p.Tp * p.Hp, 0};
+    const CeG none = {nullptr, nullptr, 0}, g = {p.g[0], p.g[1], p.piece};
+    const uint32_t* live = &p.scal->live;
+    const uint32_t k1 = p.pack ? p.Hp : p.H;
+    int rc;
+
+    const bool keep = p.kept && p.grads;
+    const CeLogitsEpi first = {p.row, d_label, p.scal, p.stat, p.zy, nullptr, keep ? g : none, p.groups, 0, p.piece, p.two, c};
+    const Gemm g1 = {mx, head(0, V), (uint32_t)T, (uint32_t)V, k1, nseg, 1, 0, live, nullptr};
+    if ((rc = ce_product<KC, KC>(p, p.tile, g1, first, st))) return rc;
+    ce_join_kernel<<<(unsigned)T, 256, 0, st>>>(a, p.row, p.stat, p.groups, p.zy, p.info, p.scal, p.two);
+    SG_TRY_LAUNCH();
+    if (!p.grads) return SG_OK;
+
+    for (uint64_t v0 = 0; v0 < V; v0 += p.piece) {
+        const uint64_t n = V - v0 < p.piece ? V - v0 : p.piece, np = align_up(n, 64);
+        if (p.kept) {
+            ce_grad_kernel<<<(unsigned)(p.Tp * ceil_div(p.piece, 2048)), 256, 0, st>>>(
+                p.row, d_label, p.stat, p.groups, ce_tile_cols(p.tile), p.info, p.scal, g, p.piece, c);
+            SG_TRY_LAUNCH();
+        } else {
+            const CeLogitsEpi second = {p.row, d_label, p.scal, nullptr, nullptr, p.info, g, p.groups, (uint32_t)v0, p.piece, p.two, c};
+            const Gemm g2 = {mx, head(v0, n), (uint32_t)T, (uint32_t)n, k1, nseg, 1, 0, live, nullptr};
+            if ((rc = ce_product<KC, KC>(p, p.tile, g2, second, st))) return rc;
+            ce_zero_kernel<<<256, 256, 0, st>>>(p.scal, g, p.piece);
+            SG_TRY_LAUNCH();
+        }
+        const Mat mg = {{p.g[0], p.g[1]}, p.piece, (uint64_t)p.Tp * p.piece, 0};
+        if (d_grad_head) {
+            const CeHeadEpi e = {p.scal, static_cast<char*>(d_grad_head) + v0 * ld_grad_head * es, ld_grad_head, p.two, wide(d_grad_head, ld_grad_head, 4 * es)};
+            const Gemm g3 = {mg, mx, (uint32_t)n, p.H, 0, nseg, 1, 0, nullptr, live};
+            const int tile = T > 64 && ceil_div(n, 256) * ceil_div(H, 256) >= 256 ? 0 : 1;
+            if ((rc = ce_product<KS, KS>(p, tile, g3, e, st))) return rc;
+        }
+        if (d_grad_hidden) {
+            const CeHiddenEpi e = {p.part, p.Hp, p.Tp, v0 > 0};
+            const Gemm g4 = {mg, head(v0, n), (uint32_t)T, p.H, (uint32_t)np, nseg, p.splits, 0, live, nullptr};
+            const int tile = p.tile == 2 ? 2 : p.splits == 1 ? 0 : 1;
+            if ((rc = ce_product<KC, KS>(p, tile, g4, e, st))) return rc;
+        }
+    }
+    if (d_grad_hidden) {
+        if (p.two) ce_hidden_kernel<float><<<(unsigned)T, 256, 0, st>>>(p.pos, p.scal, p.part, p.Hp, p.Tp, p.splits, true, (float*)d_grad_hidden, ld_grad_hidden, p.H);
+        else ce_hidden_kernel<bf16_bits><<<(unsigned)T, 256, 0, st>>>(p.pos, p.scal, p.part, p.Hp, p.Tp, p.splits, false, (bf16_bits*)d_grad_hidden, ld_grad_hidden, p.H);
+        SG_TRY_LAUNCH();
+    }
+    return SG_OK;
+}
