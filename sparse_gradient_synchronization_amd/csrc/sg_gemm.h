@@ -48,7 +48,7 @@ struct Gemm {
     Mat a, b;
     uint32_t M, N, K;
     uint32_t nseg;       // 1, or 3 for two planes
-    uint32_t splits;     // k in so many parts, one per blockIdx.y
+    uint32_t splits;     // k in so many parts, each with sums of its own
     uint32_t tri;        // 1: symmetric result, no tiles below the diagonal
     const uint32_t* d_m; // M, and K (rounded up to 64), from device memory instead
     const uint32_t* d_k;
@@ -59,30 +59,20 @@ constexpr uint64_t GEMM_MAX_LD = 1u << 21; // 256 rows of it stay below 2^31 byt
 
 #define SG_LDS(p) ((__attribute__((address_space(3))) void*)(p))
 
-// where the chunk that thread-unit u of a tile fetches lies, in bytes from
-// the tile's first element
-template <int LAY, int R>
-__device__ __forceinline__ uint32_t tile_source(uint32_t u, uint32_t ld, uint32_t* k_of)
-{
-    if (LAY == KC) {
-        const uint32_t r = u / 8, c = (u % 8) ^ (r & 7);
-        *k_of = c * 8;
-        return (r * ld + c * 8) * 2;
-    }
-    constexpr uint32_t PER = R / 8;
-    const uint32_t k = u / PER, g = ((k & 3) | ((k >> 3) & 1) << 2) & (R / 16 - 1);
-    *k_of = 0; // rows past the end lie past the buffer's end
-    return (k * ld + ((u % PER) ^ (2 * g)) * 8) * 2;
-}
-
 // One operand's tiles: R rows (KC) or columns (KS) from first, NT threads.
 template <int LAY, int R, int NT>
 struct TileLoader {
     static constexpr int U = R * 8 / NT; // chunks a thread fetches per step
     static_assert(R * 8 % NT == 0, "the tile is a whole number of chunks a thread");
+    static constexpr int PER = LAY == KC ? 8 : R / 8; // chunks of a row (of 64 k, or of R columns)
+    // A thread's chunks lie multiples of 8 rows apart.  The places repeat after
+    // 8 (KC) or 16 (KS), so its odd chunks may have a place of their own.
+    static_assert(U == 1 || NT / PER % 8 == 0, "at most two places for a thread's chunks");
+    static constexpr bool TWO = LAY == KS && U > 1 && NT / PER % 16 != 0;
     const uint16_t* p[2];
-    uint64_t ld, left; // elements from the tile's start to the operand's end
-    uint32_t src[U], kk[U], K;
+    uint64_t ld, left;   // elements from the tile's start to the operand's end
+    uint32_t src[2], kk, K; // the thread's first chunk, in bytes (for even and odd ones), and its k
+    uint32_t apart;      // bytes between its chunks
 
     __device__ __forceinline__ TileLoader(const Mat& m, uint64_t first, uint32_t batch, uint32_t K_) : ld(m.ld), K(K_)
     {
@@ -90,25 +80,48 @@ struct TileLoader {
         left = m.elems > at ? m.elems - at : 0;
         p[0] = m.p[0] + batch * m.batch + at;
         p[1] = m.p[1] ? m.p[1] + batch * m.batch + at : p[0];
-#pragma unroll
-        for (int i = 0; i < U; ++i) src[i] = tile_source<LAY, R>(i * NT + threadIdx.x, (uint32_t)m.ld, &kk[i]);
+        const uint32_t r = threadIdx.x / PER, q = threadIdx.x % PER;
+        const uint32_t c = LAY == KC ? q ^ (r & 7) : q ^ (2 * (((r & 3) | ((r >> 3) & 1) << 2) & (R / 16 - 1)));
+        src[0] = (r * (uint32_t)m.ld + c * 8) * 2;
+        src[1] = (r * (uint32_t)m.ld + (c ^ (2 * (4 & (R / 16 - 1)))) * 8) * 2;
+        kk = c * 8;
+        apart = NT / PER * (uint32_t)m.ld * 2;
     }
-    __device__ __forceinline__ void load(uint32_t k0, int plane, char* lds) const
+    // One step's fetch, set up at once and issued chunk by chunk: 64 k from k0; nothing (zeros) if !on
+    struct Step {
+        __amdgpu_buffer_rsrc_t r;
+        uint32_t off[2], apart;
+        char* to;
+        __device__ __forceinline__ void issue(int i) const
+        {
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(r, SG_LDS(to + i * NT * 16), 16, off[TWO ? i % 2 : 0] + i * apart, 0,
+                                                     0, 0);
+        }
+    };
+    __device__ __forceinline__ Step step(uint32_t k0, int plane, bool on, char* lds) const
     {
         const uint64_t at = LAY == KC ? (uint64_t)k0 : (uint64_t)k0 * ld;
-        uint64_t bytes = left > at ? (left - at) * 2 : 0;
+        uint64_t bytes = on && left > at ? (left - at) * 2 : 0;
         if (bytes > 0x7ffffff0ull) bytes = 0x7ffffff0ull;
-        const __amdgpu_buffer_rsrc_t r = __builtin_amdgcn_make_buffer_rsrc(
-            const_cast<uint16_t*>(p[plane] + at), 0, (uint32_t)bytes, 0x00020000);
-        char* to = lds + (threadIdx.x / 64) * 1024;
-#pragma unroll
-        for (int i = 0; i < U; ++i) {
-            // past the row's end: an offset past the buffer's end
-            const uint32_t off = LAY == KS || k0 + kk[i] < K ? src[i] : 0xfffffff0u;
-            __builtin_amdgcn_raw_ptr_buffer_load_lds(r, SG_LDS(to + i * NT * 16), 16, off, 0, 0, 0);
-        }
+        Step s;
+        s.r = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint16_t*>(p[plane] + at), 0, (uint32_t)bytes, 0x00020000);
+        // KC, past the row's end: an offset past the buffer's end.  KS: rows past the end lie there
+        s.off[0] = LAY == KS || k0 + kk < K ? src[0] : 0x80000000u;
+        s.off[1] = src[1];
+        s.apart = apart;
+        s.to = lds + (threadIdx.x / 64) * 1024;
+        return s;
     }
 };
+
+typedef __attribute__((address_space(3))) s16x4 LdsS16x4;
+// __restrict__ gives the read an alias scope.  Without one the compiler takes
+// every fetch into LDS for one that this read may depend on and waits for all of
+// them (the waits that are needed stand in the kernel).
+__device__ __forceinline__ s16x4 read_transposed(LdsS16x4* __restrict__ p)
+{
+    return __builtin_amdgcn_ds_read_tr16_b64_v4i16(p);
+}
 
 // A wave's fragments of 16 rows or columns from LDS, T side by side.
 template <int LAY, int R, int T>
@@ -131,10 +144,8 @@ struct FragReader {
     __device__ __forceinline__ s16x8 read(const char* lds, int t, int h) const
     {
         if (LAY == KC) return *reinterpret_cast<const s16x8*>(lds + (at[0] ^ h * 64) + t * 2048);
-        typedef __attribute__((address_space(3))) s16x4* P;
         const char* q = lds + at[LAY == KC ? 0 : t] + h * 32 * R * 2;
-        const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((P)(q));
-        const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((P)(q + 4 * R * 2));
+        const s16x4 lo = read_transposed((LdsS16x4*)q), hi = read_transposed((LdsS16x4*)(q + 4 * R * 2));
         return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
     }
 };
@@ -156,16 +167,49 @@ __device__ __forceinline__ void wait_loads()
     asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
 }
 
-// Consecutive blocks go to the 8 XCDs in turn; each XCD gets a contiguous run
-// of tiles, in groups of 8 tile rows, so that its L2 holds what they share.
-__device__ __forceinline__ void tile_of(uint32_t tm, uint32_t tn, uint32_t* m, uint32_t* n)
+// The tiles of a launch, in their order: tiles, parts of k, matrices of a
+// batch.  Consecutive blocks go to the 8 XCDs in turn; each XCD gets a contiguous
+// run of what there is to do, so that its L2 holds what the tiles share and
+// all have as much: groups of 8 tile rows, or, of a symmetric result, the rows of
+// the tiles that are not wholly below the diagonal.
+template <int BM, int BN>
+__host__ __device__ __forceinline__ uint32_t tri_first(uint32_t m) // of tile row m
 {
-    const uint32_t id = blockIdx.x, total = tm * tn, x = id % 8, q = total / 8, r = total % 8;
-    const uint32_t pid = x * q + (x < r ? x : r) + id / 8;
+    return m * BM / BN;
+}
+template <int BM, int BN>
+__host__ __device__ __forceinline__ uint32_t tile_count(uint32_t tm, uint32_t tn, uint32_t tri)
+{
+    if (!tri) return tm * tn;
+    uint32_t c = 0;
+    for (uint32_t m = 0; m < tm && tri_first<BM, BN>(m) < tn; ++m) c += tn - tri_first<BM, BN>(m);
+    return c;
+}
+struct TilePlace {
+    uint32_t m, n, split, batch;
+};
+template <int BM, int BN>
+__device__ __forceinline__ bool tile_of(uint32_t tm, uint32_t tn, uint32_t tri, uint32_t splits, uint32_t batch,
+                                        TilePlace* p)
+{
+    const uint32_t tiles = tile_count<BM, BN>(tm, tn, tri), total = tiles * splits * batch;
+    const uint32_t id = blockIdx.x, x = id % 8, q = total / 8, r = total % 8;
+    if (id >= total) return false; // fewer rows than the launch was made for
+    const uint32_t at = x * q + (x < r ? x : r) + id / 8, pid = at % tiles, rest = at / tiles;
+    p->split = rest % splits;
+    p->batch = rest / splits;
+    if (tri) {
+        uint32_t m = 0, in = pid;
+        while (in >= tn - tri_first<BM, BN>(m)) in -= tn - tri_first<BM, BN>(m++);
+        p->m = m;
+        p->n = tri_first<BM, BN>(m) + in;
+        return true;
+    }
     const uint32_t group = pid / (8 * tn), first = group * 8, rows = tm - first < 8 ? tm - first : 8,
                    in = pid % (8 * tn);
-    *m = first + in % rows;
-    *n = in / rows;
+    p->m = first + in % rows;
+    p->n = in / rows;
+    return true;
 }
 
 template <int BM_, int BN_, int WM_, int WN_>
@@ -193,28 +237,42 @@ struct TileAt {
     char* lds;
 };
 
+// Two stages of LDS, two halves of 32 k to a stage.  While one half is
+// multiplied the next one is read into registers; the block meets once a step,
+// between the halves, with the second half in registers: there are products to do
+// on both sides of the barrier, behind which the stage just read is fetched into
+// again.  Fetches are issued one at a time among the products: issued together
+// they hold up the wave for as long as the memory pipeline takes them in (8192^3
+// bf16: 870 us together, 790 apart; 670 without any fetch and 650 with neither
+// fetch nor barrier, what the products alone take at the clock they leave the card).
+// Tiles one after another in a block, the next one's fetches under the epilogue, took
+// as long: a wait for fetches is one for the stores before them.
 template <class Cfg, int AL, int BL, bool F16, class Epi>
-__global__ __launch_bounds__(Cfg::NT, Cfg::PER_SIMD) void gemm_kernel(Gemm g, Epi epi)
+__global__ __launch_bounds__(Cfg::NT, Cfg::PER_SIMD) void gemm_kernel(Gemm g, uint32_t batch, Epi epi)
 {
     __shared__ __align__(1024) char lds[Cfg::LDS];
     if (g.d_m) g.M = *g.d_m;
     if (g.d_k) g.K = (*g.d_k + GEMM_BK - 1) / GEMM_BK * GEMM_BK;
-    const uint32_t tiles_n = (g.N + Cfg::BN - 1) / Cfg::BN;
-    uint32_t tm, tn;
-    tile_of(gridDim.x / tiles_n, tiles_n, &tm, &tn);
-    if (tm * Cfg::BM >= g.M) return;                   // fewer rows than the launch was made for
-    if (g.tri && tm * Cfg::BM >= (tn + 1) * Cfg::BN) return; // wholly below the diagonal
+    TilePlace t;
+    if (!tile_of<Cfg::BM, Cfg::BN>((g.M + Cfg::BM - 1) / Cfg::BM, (g.N + Cfg::BN - 1) / Cfg::BN, g.tri, g.splits, batch,
+                                   &t))
+        return;
     const uint32_t w = threadIdx.x / 64, wm = w / Cfg::WN, wn = w % Cfg::WN;
 
-    const TileLoader<AL, Cfg::BM, Cfg::NT> la(g.a, (uint64_t)tm * Cfg::BM, blockIdx.z, g.K);
-    const TileLoader<BL, Cfg::BN, Cfg::NT> lb(g.b, (uint64_t)tn * Cfg::BN, blockIdx.z, g.K);
+    typedef TileLoader<AL, Cfg::BM, Cfg::NT> LoadA;
+    typedef TileLoader<BL, Cfg::BN, Cfg::NT> LoadB;
+    const LoadA la(g.a, (uint64_t)t.m * Cfg::BM, t.batch, g.K);
+    const LoadB lb(g.b, (uint64_t)t.n * Cfg::BN, t.batch, g.K);
     const FragReader<AL, Cfg::BM, Cfg::MT> fa(wm * (Cfg::BM / Cfg::WM));
     const FragReader<BL, Cfg::BN, Cfg::NTT> fb(wn * (Cfg::BN / Cfg::WN));
-    constexpr int UA = Cfg::BM * GEMM_BK * 2, LOADS = la.U + lb.U;
+    constexpr int UA = Cfg::BM * GEMM_BK * 2, LOADS = LoadA::U + LoadB::U;
+    constexpr int READS = Cfg::MT + Cfg::NTT, PRODUCTS = Cfg::MT * Cfg::NTT;
+    // groups of a half's work: a fetch each, and reads in the first three quarters
+    constexpr int G = LOADS < PRODUCTS ? LOADS : PRODUCTS, RG = G * 3 / 4;
 
     // this part's steps of 64 k, then all of them again for the next segment
     const uint32_t ks = (g.K + GEMM_BK - 1) / GEMM_BK, per = (ks + g.splits - 1) / g.splits;
-    const uint32_t first = blockIdx.y * per < ks ? blockIdx.y * per : ks, last = first + per < ks ? first + per : ks;
+    const uint32_t first = t.split * per < ks ? t.split * per : ks, last = first + per < ks ? first + per : ks;
     const uint32_t steps = (last - first) * g.nseg;
 
     f32x4 acc[Cfg::MT][Cfg::NTT];
@@ -223,52 +281,84 @@ __global__ __launch_bounds__(Cfg::NT, Cfg::PER_SIMD) void gemm_kernel(Gemm g, Ep
 #pragma unroll
         for (int j = 0; j < Cfg::NTT; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
 
-    uint32_t k = first, seg = 0; // of the next step to fetch
-    const auto fetch = [&](char* to) {
-        la.load(k * GEMM_BK, seg == 2, to);
-        lb.load(k * GEMM_BK, seg == 1, to + UA);
-        if (++k == last) {
-            k = first;
-            ++seg;
+    uint32_t k = first, seg = 0; // of the next step to fetch; past the last one it fetches nothing
+    struct Fetch {
+        typename LoadA::Step a;
+        typename LoadB::Step b;
+        __device__ __forceinline__ void issue(int i) const
+        {
+            if (i < LoadA::U) a.issue(i);
+            else b.issue(i - LoadA::U);
         }
     };
-    if (steps > 0) fetch(lds);
-    for (uint32_t s = 0; s < steps; ++s) {
-        char* const cur = lds + (s & 1) * Cfg::STAGE;
-        if (s + 1 < steps) {
-            fetch(lds + (~s & 1) * Cfg::STAGE);
-            wait_loads<LOADS>();
-        } else {
-            wait_loads<0>();
+    const auto fetch = [&](char* to) {
+        const bool on = seg < g.nseg;
+        const Fetch f = {la.step(k * GEMM_BK, seg == 2, on, to), lb.step(k * GEMM_BK, seg == 1, on, to + UA)};
+        const bool wrap = k + 1 >= last;
+        k = wrap ? first : k + 1;
+        seg += wrap ? 1 : 0;
+        return f;
+    };
+    struct Half { // a wave's fragments of 32 k
+        s16x8 a[Cfg::MT], b[Cfg::NTT];
+    } h0, h1;
+    const auto read_one = [&](const char* from, int h, Half& to, int i) {
+        if (i < Cfg::NTT) to.b[i] = fb.read(from + UA, i, h);
+        else to.a[i - Cfg::NTT] = fa.read(from, i - Cfg::NTT, h);
+    };
+    // the products of one half, with the next half's reads and (f) a step's fetches among them
+    const auto work = [&](const Half& have, const char* from, int h, Half& next, const Fetch* f) {
+#pragma unroll
+        for (int q = 0; q < G; ++q) {
+#pragma unroll
+            for (int i = q * LOADS / G; i < (q + 1) * LOADS / G; ++i)
+                if (f) f->issue(i);
+#pragma unroll
+            for (int i = q * READS / RG; i < (q + 1) * READS / RG && i < READS; ++i) read_one(from, h, next, i);
+#pragma unroll
+            for (int i = q * PRODUCTS / G; i < (q + 1) * PRODUCTS / G; ++i) {
+                f32x4& c = acc[i / Cfg::NTT][i % Cfg::NTT];
+                c = mfma16<F16>(have.b[i % Cfg::NTT], have.a[i / Cfg::NTT], c);
+            }
+            __builtin_amdgcn_sched_barrier(0);
         }
+    };
+    if (steps > 0) {
+        const Fetch f0 = fetch(lds);
+#pragma unroll
+        for (int i = 0; i < LOADS; ++i) f0.issue(i);
+        const Fetch f1 = fetch(lds + Cfg::STAGE);
+#pragma unroll
+        for (int i = 0; i < LOADS; ++i) f1.issue(i);
+        wait_loads<LOADS>();
         __builtin_amdgcn_s_barrier();
         asm volatile("" ::: "memory");
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            s16x8 b[Cfg::NTT];
-#pragma unroll
-            for (int j = 0; j < Cfg::NTT; ++j) b[j] = fb.read(cur + UA, j, h);
-#pragma unroll
-            for (int i = 0; i < Cfg::MT; ++i) {
-                const s16x8 a = fa.read(cur, i, h);
-#pragma unroll
-                for (int j = 0; j < Cfg::NTT; ++j) acc[i][j] = mfma16<F16>(b[j], a, acc[i][j]);
-            }
+        for (int i = 0; i < READS; ++i) read_one(lds, 0, h0, i);
+        for (uint32_t s = 0; s < steps; ++s) {
+            char *const cur = lds + (s & 1) * Cfg::STAGE, *const next = lds + (~s & 1) * Cfg::STAGE;
+            const Fetch f = fetch(cur);
+            work(h0, cur, 1, h1, nullptr);
+            // every wave's reads of this stage and fetches of the next are done
+            asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+            __builtin_amdgcn_s_barrier();
+            asm volatile("" ::: "memory");
+            work(h1, next, 0, h0, &f);
         }
-        // this wave's reads are done before another wave fetches into the same place
-        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+        // the fetches past the end wrote zeros to LDS, which the epilogue may use
+        asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
         __builtin_amdgcn_s_barrier();
         asm volatile("" ::: "memory");
     }
     TileAt at;
-    at.bm0 = tm * Cfg::BM;
-    at.bn0 = tn * Cfg::BN;
+    at.bm0 = t.m * Cfg::BM;
+    at.bn0 = t.n * Cfg::BN;
     at.m0 = at.bm0 + wm * (Cfg::BM / Cfg::WM);
     at.n0 = at.bn0 + wn * (Cfg::BN / Cfg::WN);
     at.M = g.M;
     at.N = g.N;
-    at.split = blockIdx.y;
-    at.batch = blockIdx.z;
+    at.split = t.split;
+    at.batch = t.batch;
     at.wm = wm;
     at.wn = wn;
     at.lds = lds;
@@ -278,11 +368,12 @@ __global__ __launch_bounds__(Cfg::NT, Cfg::PER_SIMD) void gemm_kernel(Gemm g, Ep
 template <class Cfg, int AL, int BL, bool F16, class Epi>
 static int launch_gemm(const Gemm& g, uint32_t batch, const Epi& epi, hipStream_t st)
 {
-    const uint64_t tiles = ceil_div(g.M, Cfg::BM) * ceil_div(g.N, Cfg::BN);
-    if (tiles == 0 || batch == 0) return SG_OK;
-    if (tiles >= (1ull << 31) || g.splits == 0 || g.splits > 65535 || batch > 65535) return SG_EUNSUPPORTED;
+    const uint64_t tm = ceil_div(g.M, Cfg::BM), tn = ceil_div(g.N, Cfg::BN);
+    if (tm == 0 || tn == 0 || batch == 0) return SG_OK;
+    if (tm * tn * g.splits * batch >= (1ull << 31) || g.splits == 0) return SG_EUNSUPPORTED;
     if (g.a.ld > GEMM_MAX_LD || g.b.ld > GEMM_MAX_LD) return SG_EUNSUPPORTED;
-    gemm_kernel<Cfg, AL, BL, F16, Epi><<<dim3((unsigned)tiles, g.splits, batch), Cfg::NT, 0, st>>>(g, epi);
+    const uint32_t blocks = tile_count<Cfg::BM, Cfg::BN>((uint32_t)tm, (uint32_t)tn, g.tri) * g.splits * batch;
+    gemm_kernel<Cfg, AL, BL, F16, Epi><<<blocks, Cfg::NT, 0, st>>>(g, batch, epi);
     SG_TRY_LAUNCH();
     return SG_OK;
 }

@@ -26,6 +26,8 @@
 // two per tensor (sg_gemm.h), which loses 2^-22 of each element down to 2^-17
 // of the tensor's largest and an absolute 2^-39 of it below.  The kept
 // exponentials are whole fp32 there, in the two planes of g.
+#include <type_traits>
+
 #include "sg_gemm.h"
 #include "sg_rows.h"
 
@@ -115,14 +117,13 @@ __global__ __launch_bounds__(1024) void ce_rows_kernel(CeArgs p, uint32_t* row, 
 struct CeSrc {
     const void* x;
     uint64_t ld;
-    uint32_t n;   // elements of a row
-    bool wide;    // rows start on 16 bytes
+    uint32_t n; // elements of a row
 };
 template <typename E>
 __device__ __forceinline__ void ce_load8(const CeSrc& s, uint64_t r, uint32_t c, float* v)
 {
     const E* x = static_cast<const E*>(s.x) + r * s.ld + c;
-    if (s.wide && c + 8 <= s.n) {
+    if (c + 8 <= s.n) { // gfx950 loads 16 bytes at any element's address
         constexpr int VEC = RowIO<E>::VEC;
 #pragma unroll
         for (int i = 0; i < 8; i += VEC) RowIO<E>::unpack(load_chunk(x + i), v + i);
@@ -193,8 +194,8 @@ __global__ __launch_bounds__(256) void ce_pack_kernel(CeSrc s, uint64_t rows, co
 // a number in [0, 1] in 16 bits, and back; below 2^-63 it is 0
 __device__ __forceinline__ uint16_t ce_code(float e)
 {
-    const uint32_t b = __float_as_uint(e);
-    return (uint16_t)((b < 0x20000000u ? 0u : b - 0x20000000u + 0x1000u) >> 13);
+    const int b = (int)__float_as_uint(e) - (0x20000000 - 0x1000);
+    return (uint16_t)((b > 0 ? b : 0) >> 13);
 }
 __device__ __forceinline__ float ce_decode(uint32_t code)
 {
@@ -207,57 +208,70 @@ struct CeG {
     uint64_t ld;
 };
 
-// where the logits' products end: statistics (and exponentials), or g
+// Where the logits' products end the first time: the rows' statistics over the
+// block's columns, the labels' logits, and (g.hi) the exponentials.
+template <bool PLANES>
 struct CeLogitsEpi {
     const uint32_t* row;
     const int32_t* label;
     const CeScal* scal;
     float2* stat; // [rows][groups]
     float* zy;    // [rows] the label's logit
-    const CeRow* info; // not NULL: g, from the joined sums
     CeG g;        // hi NULL: keep nothing
-    uint32_t groups, v0, Vp; // v0: first token of this piece; Vp: its padded end in g
-    bool planes;
+    uint32_t groups, Vp; // Vp: columns of g
     float c;
 
     template <class Cfg>
     __device__ __forceinline__ void run(f32x4 (&acc)[Cfg::MT][Cfg::NTT], const TileAt& at) const
     {
         const uint32_t l = threadIdx.x % 64;
-        const int unit = planes ? -ce_exponent(scal->max_x) - ce_exponent(scal->max_w) : 0;
-        const int gexp = planes && info ? ce_exponent(scal->max_g) : 0;
+        const int unit = PLANES ? -ce_exponent(scal->max_x) - ce_exponent(scal->max_w) : 0;
         float mx[Cfg::MT], sum[Cfg::MT];
-        float* const lm = reinterpret_cast<float*>(at.lds);  // [WN][BM]
+        uint32_t y[Cfg::MT]; // the row's label as a column of the wave's part
+        float* const lm = reinterpret_cast<float*>(at.lds); // [WN][BM]
         float* const ls = lm + Cfg::WN * Cfg::BM;
+        const uint32_t last = at.M - 1;
 #pragma unroll
         for (int i = 0; i < Cfg::MT; ++i) {
             const uint32_t m = at.m0 + i * 16 + l % 16;
-            const bool in = m < at.M;
-            const uint32_t y = in ? (uint32_t)label[row[m]] - v0 : 0xffffffffu; // in this piece, if below N
-            const CeRow r = in && info ? info[m] : CeRow{0.f, 0.f, 0.f, 0.f};
-            mx[i] = -INFINITY;
-#pragma unroll
-            for (int j = 0; j < Cfg::NTT; ++j) {
-                const uint32_t n = at.n0 + j * 16 + l / 16 * 4;
-                float v[4];
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    v[k] = planes ? ldexpf(acc[i][j][k], unit) : acc[i][j][k];
-                    if (!info && n + k == y) zy[m] = v[k];
-                    if (n + k >= at.N) v[k] = -INFINITY;
-                    if (info) {
-                        v[k] = r.a * exp2_fast(c * (v[k] - r.m) - r.ls) - (n + k == y ? r.b : 0.f);
-                    }
-                    mx[i] = fmaxf(mx[i], v[k]);
-                    acc[i][j][k] = v[k];
-                }
-                if (info && in && n < Vp) put_g(m, n, v, gexp);
-            }
+            y[i] = row[m < at.M ? m : last];
         }
-        if (info) return;
-        // the rows' maxima over the block's columns
+#pragma unroll
+        for (int i = 0; i < Cfg::MT; ++i) y[i] = (uint32_t)label[y[i]] - at.n0;
+        if (PLANES) {
+#pragma unroll
+            for (int i = 0; i < Cfg::MT; ++i)
+#pragma unroll
+                for (int j = 0; j < Cfg::NTT; ++j)
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) acc[i][j][k] = ldexpf(acc[i][j][k], unit);
+        }
+        if (at.n0 + Cfg::NTT * 16 > at.N) { // columns past the vocabulary's end
+#pragma unroll
+            for (int i = 0; i < Cfg::MT; ++i)
+#pragma unroll
+                for (int j = 0; j < Cfg::NTT; ++j)
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        if (at.n0 + j * 16 + l / 16 * 4 + k >= at.N) acc[i][j][k] = -INFINITY;
+        }
 #pragma unroll
         for (int i = 0; i < Cfg::MT; ++i) {
+            // few tiles hold a label of their rows
+            const uint32_t mine = y[i] - l / 16 * 4; // 16 j + k where this lane holds it
+            if (__any(y[i] < Cfg::NTT * 16)) {
+                float z = 0.f;
+#pragma unroll
+                for (int j = 0; j < Cfg::NTT; ++j)
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) z = mine == j * 16u + k ? acc[i][j][k] : z;
+                if (mine < Cfg::NTT * 16u && mine % 16 < 4 && at.m0 + i * 16 + l % 16 < at.M)
+                    zy[at.m0 + i * 16 + l % 16] = z;
+            }
+            mx[i] = -INFINITY;
+#pragma unroll
+            for (int j = 0; j < Cfg::NTT; ++j)
+                mx[i] = fmaxf(mx[i], fmaxf(fmaxf(acc[i][j][0], acc[i][j][1]), fmaxf(acc[i][j][2], acc[i][j][3])));
             mx[i] = fmaxf(mx[i], __shfl_xor(mx[i], 16));
             mx[i] = fmaxf(mx[i], __shfl_xor(mx[i], 32));
             if (l < 16) lm[at.wn * Cfg::BM + at.m0 - at.bm0 + i * 16 + l] = mx[i];
@@ -272,16 +286,20 @@ struct CeLogitsEpi {
             sum[i] = 0.f;
 #pragma unroll
             for (int j = 0; j < Cfg::NTT; ++j) {
-                const uint32_t n = at.n0 + j * 16 + l / 16 * 4;
-                float e[4];
 #pragma unroll
-                for (int k = 0; k < 4; ++k) e[k] = exp2_fast(c * (acc[i][j][k] - shift));
-                sum[i] += (e[0] + e[1]) + (e[2] + e[3]);
-                if (g.hi && at.bm0 + q < at.M && n < Vp) keep(at.bm0 + q, n, e);
+                for (int k = 0; k < 4; ++k) acc[i][j][k] = exp2_fast(c * (acc[i][j][k] - shift));
+                sum[i] += (acc[i][j][0] + acc[i][j][1]) + (acc[i][j][2] + acc[i][j][3]);
             }
             sum[i] += __shfl_xor(sum[i], 16);
             sum[i] += __shfl_xor(sum[i], 32);
             if (l < 16) ls[at.wn * Cfg::BM + q] = sum[i];
+            if (g.hi && at.bm0 + q < at.M) {
+#pragma unroll
+                for (int j = 0; j < Cfg::NTT; ++j) {
+                    const uint32_t n = at.n0 + j * 16 + l / 16 * 4;
+                    if (n < Vp) keep(at.bm0 + q, n, acc[i][j]);
+                }
+            }
         }
         __syncthreads();
         if (at.wn == 0 && l < 16) {
@@ -292,33 +310,16 @@ struct CeLogitsEpi {
 #pragma unroll
                 for (int w = 0; w < Cfg::WN; ++w) s += ls[w * Cfg::BM + q];
                 if (at.bm0 + q < at.M)
-                    stat[(uint64_t)(at.bm0 + q) * groups + (v0 + at.bn0) / Cfg::BN] = make_float2(mx[i], s);
+                    stat[(uint64_t)(at.bm0 + q) * groups + at.bn0 / Cfg::BN] = make_float2(mx[i], s);
             }
         }
     }
-    __device__ __forceinline__ void put_g(uint32_t m, uint32_t n, const float* v, int gexp) const
+    __device__ __forceinline__ void keep(uint32_t m, uint32_t n, f32x4 e) const
     {
         s16x4 h, q;
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-            if (g.lo) {
-                uint16_t x, y;
-                split_f16(ldexpf(v[k], gexp), &x, &y);
-                h[k] = (short)x;
-                q[k] = (short)y;
-            } else {
-                h[k] = __builtin_bit_cast(short, (__bf16)v[k]);
-            }
-        }
-        *reinterpret_cast<s16x4*>(g.hi + m * g.ld + n) = h;
-        if (g.lo) *reinterpret_cast<s16x4*>(g.lo + m * g.ld + n) = q;
-    }
-    __device__ __forceinline__ void keep(uint32_t m, uint32_t n, const float* e) const
-    {
-        s16x4 h, q;
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            if (g.lo) {
+            if (PLANES) {
                 h[k] = (short)(__float_as_uint(e[k]) >> 16);
                 q[k] = (short)__float_as_uint(e[k]);
             } else {
@@ -326,7 +327,61 @@ struct CeLogitsEpi {
             }
         }
         *reinterpret_cast<s16x4*>(g.hi + m * g.ld + n) = h;
-        if (g.lo) *reinterpret_cast<s16x4*>(g.lo + m * g.ld + n) = q;
+        if (PLANES) *reinterpret_cast<s16x4*>(g.lo + m * g.ld + n) = q;
+    }
+};
+
+// The second time, for a piece of the vocabulary: g from the joined sums.
+template <bool PLANES>
+struct CePieceEpi {
+    const uint32_t* row;
+    const int32_t* label;
+    const CeScal* scal;
+    const CeRow* info;
+    CeG g;
+    uint32_t v0, Vp; // first token of the piece; columns of g
+    float c;
+
+    template <class Cfg>
+    __device__ __forceinline__ void run(const f32x4 (&acc)[Cfg::MT][Cfg::NTT], const TileAt& at) const
+    {
+        const uint32_t l = threadIdx.x % 64, last = at.M - 1;
+        const int unit = PLANES ? -ce_exponent(scal->max_x) - ce_exponent(scal->max_w) : 0;
+        const int gexp = PLANES ? ce_exponent(scal->max_g) : 0;
+        uint32_t y[Cfg::MT];
+        CeRow r[Cfg::MT];
+#pragma unroll
+        for (int i = 0; i < Cfg::MT; ++i) {
+            const uint32_t m = at.m0 + i * 16 + l % 16;
+            y[i] = row[m < at.M ? m : last];
+            r[i] = info[m < at.M ? m : last];
+        }
+#pragma unroll
+        for (int i = 0; i < Cfg::MT; ++i) y[i] = (uint32_t)label[y[i]] - v0;
+#pragma unroll
+        for (int i = 0; i < Cfg::MT; ++i)
+#pragma unroll
+            for (int j = 0; j < Cfg::NTT; ++j) {
+                const uint32_t m = at.m0 + i * 16 + l % 16, n = at.n0 + j * 16 + l / 16 * 4;
+                s16x4 h, q;
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const float z = PLANES ? ldexpf(acc[i][j][k], unit) : acc[i][j][k];
+                    const float e = n + k < at.N ? r[i].a * exp2_fast(c * (z - r[i].m) - r[i].ls) : 0.f;
+                    const float v = e - (n + k == y[i] ? r[i].b : 0.f);
+                    if (PLANES) {
+                        uint16_t a, b;
+                        split_f16(ldexpf(v, gexp), &a, &b);
+                        h[k] = (short)a;
+                        q[k] = (short)b;
+                    } else {
+                        h[k] = __builtin_bit_cast(short, (__bf16)v);
+                    }
+                }
+                if (m >= at.M || n >= Vp) continue;
+                *reinterpret_cast<s16x4*>(g.hi + m * g.ld + n) = h;
+                if (PLANES) *reinterpret_cast<s16x4*>(g.lo + m * g.ld + n) = q;
+            }
     }
 };
 
@@ -449,21 +504,30 @@ struct CeHiddenEpi {
     }
 };
 
-// dx of every row from its sums
+// dx of every row from its sums: 1024 columns to a block
 template <typename E>
 __global__ __launch_bounds__(256) void ce_hidden_kernel(const int32_t* pos, const CeScal* scal, const float* part,
                                                         uint64_t ldp, uint64_t rows, uint32_t splits, bool planes,
                                                         E* out, uint64_t ld, uint32_t H)
 {
-    const uint64_t t = blockIdx.x;
+    const uint32_t cols = (H + 1023) / 1024;
+    const uint64_t t = blockIdx.x / cols;
+    const uint32_t h = blockIdx.x % cols * 1024 + threadIdx.x * 4;
+    if (h >= H) return;
     const int32_t j = pos[t];
-    const int unit = planes ? -ce_exponent(scal->max_g) - ce_exponent(scal->max_w) : 0;
-    for (uint32_t h = threadIdx.x; h < H; h += 256) {
-        float s = 0.f;
-        if (j >= 0)
-            for (uint32_t k = 0; k < splits; ++k) s += part[(k * rows + (uint32_t)j) * ldp + h];
-        RowIO<E>::put(out + t * ld + h, j >= 0 ? ldexpf(s, unit) * (float)scal->top : 0.f);
+    f32x4 s = {0.f, 0.f, 0.f, 0.f};
+    if (j >= 0) {
+        const float* q = part + (uint32_t)j * ldp + h;
+#pragma unroll 8
+        for (uint32_t k = 0; k < splits; ++k) s += *reinterpret_cast<const f32x4*>(q + k * rows * ldp);
+        const int unit = planes ? -ce_exponent(scal->max_g) - ce_exponent(scal->max_w) : 0;
+        const float top = (float)scal->top;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) s[i] = ldexpf(s[i], unit) * top;
     }
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        if (h + i < H) RowIO<E>::put(out + t * ld + h + i, s[i]);
 }
 
 // dw, rounded once to the caller's type
@@ -577,14 +641,13 @@ static CePlan ce_plan(Carver& cv, uint64_t T, uint64_t V, uint32_t H, sg_dtype d
     return p;
 }
 
-template <int AL, int BL, class Epi>
-static int ce_product(const CePlan& p, int tile, const Gemm& g, const Epi& e, hipStream_t st)
+template <int AL, int BL, bool F16, class Epi>
+static int ce_product(int tile, const Gemm& g, const Epi& e, hipStream_t st)
 {
-    if (tile == 0)
-        return p.two ? launch_gemm<TileL, AL, BL, true>(g, 1, e, st) : launch_gemm<TileL, AL, BL, false>(g, 1, e, st);
-    if (tile == 1)
-        return p.two ? launch_gemm<TileM, AL, BL, true>(g, 1, e, st) : launch_gemm<TileM, AL, BL, false>(g, 1, e, st);
-    return p.two ? launch_gemm<TileRow, AL, BL, true>(g, 1, e, st) : launch_gemm<TileRow, AL, BL, false>(g, 1, e, st);
+    if (tile == 0) return launch_gemm<TileL, AL, BL, F16>(g, 1, e, st);
+    if (AL == KS || tile == 1) return launch_gemm<TileM, AL, BL, F16>(g, 1, e, st); // dw has the vocabulary's rows
+    if constexpr (AL == KC) return launch_gemm<TileRow, AL, BL, F16>(g, 1, e, st);
+    return SG_EUNSUPPORTED;
 }
 
 static bool ce_sizes(uint64_t T, uint64_t V, uint64_t H, sg_dtype dt)
@@ -647,8 +710,7 @@ extern "C" int sg_linear_ce_loss(const void* d_hidden, uint64_t ld_hidden, const
 
     ce_rows_kernel<<<1, 1024, 0, st>>>(a, p.row, p.pos, p.scal);
     SG_TRY_LAUNCH();
-    const CeSrc sx = {d_hidden, ld_hidden, p.H, wide(d_hidden, ld_hidden, 16)},
-                sw = {d_head, ld_head, p.H, wide(d_head, ld_head, 16)};
+    const CeSrc sx = {d_hidden, ld_hidden, p.H}, sw = {d_head, ld_head, p.H};
     const auto blocks = [](uint64_t items) { const uint64_t b = ceil_div(items, 256); return (unsigned)(b < 8192 ? b : 8192); };
     const unsigned bx = blocks((uint64_t)p.Tp * p.Hp / 8), bw = blocks(V * p.Hp / 8);
     if (p.two) {
@@ -682,9 +744,12 @@ extern "C" int sg_linear_ce_loss(const void* d_hidden, uint64_t ld_hidden, const
     int rc;
 
     const bool keep = p.kept && p.grads;
-    const CeLogitsEpi first = {p.row, d_label, p.scal, p.stat, p.zy, nullptr, keep ? g : none, p.groups, 0, p.piece, p.two, c};
     const Gemm g1 = {mx, head(0, V), (uint32_t)T, (uint32_t)V, k1, nseg, 1, 0, live, nullptr};
-    if ((rc = ce_product<KC, KC>(p, p.tile, g1, first, st))) return rc;
+    const auto first = [&](auto planes) {
+        const CeLogitsEpi<decltype(planes)::value> e = {p.row, d_label, p.scal, p.stat, p.zy, keep ? g : none, p.groups, p.piece, c};
+        return ce_product<KC, KC, decltype(planes)::value>(p.tile, g1, e, st);
+    };
+    if ((rc = p.two ? first(std::true_type()) : first(std::false_type()))) return rc;
     ce_join_kernel<<<(unsigned)T, 256, 0, st>>>(a, p.row, p.stat, p.groups, p.zy, p.info, p.scal, p.two);
     SG_TRY_LAUNCH();
     if (!p.grads) return SG_OK;
@@ -696,9 +761,12 @@ extern "C" int sg_linear_ce_loss(const void* d_hidden, uint64_t ld_hidden, const
                 p.row, d_label, p.stat, p.groups, ce_tile_cols(p.tile), p.info, p.scal, g, p.piece, c);
             SG_TRY_LAUNCH();
         } else {
-            const CeLogitsEpi second = {p.row, d_label, p.scal, nullptr, nullptr, p.info, g, p.groups, (uint32_t)v0, p.piece, p.two, c};
             const Gemm g2 = {mx, head(v0, n), (uint32_t)T, (uint32_t)n, k1, nseg, 1, 0, live, nullptr};
-            if ((rc = ce_product<KC, KC>(p, p.tile, g2, second, st))) return rc;
+            const auto second = [&](auto planes) {
+                const CePieceEpi<decltype(planes)::value> e = {p.row, d_label, p.scal, p.info, g, (uint32_t)v0, p.piece, c};
+                return ce_product<KC, KC, decltype(planes)::value>(p.tile, g2, e, st);
+            };
+            if ((rc = p.two ? second(std::true_type()) : second(std::false_type()))) return rc;
             ce_zero_kernel<<<256, 256, 0, st>>>(p.scal, g, p.piece);
             SG_TRY_LAUNCH();
         }
@@ -707,18 +775,21 @@ extern "C" int sg_linear_ce_loss(const void* d_hidden, uint64_t ld_hidden, const
             const CeHeadEpi e = {p.scal, static_cast<char*>(d_grad_head) + v0 * ld_grad_head * es, ld_grad_head, p.two, wide(d_grad_head, ld_grad_head, 4 * es)};
             const Gemm g3 = {mg, mx, (uint32_t)n, p.H, 0, nseg, 1, 0, nullptr, live};
             const int tile = T > 64 && ceil_div(n, 256) * ceil_div(H, 256) >= 256 ? 0 : 1;
-            if ((rc = ce_product<KS, KS>(p, tile, g3, e, st))) return rc;
+            rc = p.two ? ce_product<KS, KS, true>(tile, g3, e, st) : ce_product<KS, KS, false>(tile, g3, e, st);
+            if (rc) return rc;
         }
         if (d_grad_hidden) {
             const CeHiddenEpi e = {p.part, p.Hp, p.Tp, v0 > 0};
             const Gemm g4 = {mg, head(v0, n), (uint32_t)T, p.H, (uint32_t)np, nseg, p.splits, 0, live, nullptr};
             const int tile = p.tile == 2 ? 2 : p.splits == 1 ? 0 : 1;
-            if ((rc = ce_product<KC, KS>(p, tile, g4, e, st))) return rc;
+            rc = p.two ? ce_product<KC, KS, true>(tile, g4, e, st) : ce_product<KC, KS, false>(tile, g4, e, st);
+            if (rc) return rc;
         }
     }
     if (d_grad_hidden) {
-        if (p.two) ce_hidden_kernel<float><<<(unsigned)T, 256, 0, st>>>(p.pos, p.scal, p.part, p.Hp, p.Tp, p.splits, true, (float*)d_grad_hidden, ld_grad_hidden, p.H);
-        else ce_hidden_kernel<bf16_bits><<<(unsigned)T, 256, 0, st>>>(p.pos, p.scal, p.part, p.Hp, p.Tp, p.splits, false, (bf16_bits*)d_grad_hidden, ld_grad_hidden, p.H);
+        const unsigned hblocks = (unsigned)(T * ceil_div(H, 1024));
+        if (p.two) ce_hidden_kernel<float><<<hblocks, 256, 0, st>>>(p.pos, p.scal, p.part, p.Hp, p.Tp, p.splits, true, (float*)d_grad_hidden, ld_grad_hidden, p.H);
+        else ce_hidden_kernel<bf16_bits><<<hblocks, 256, 0, st>>>(p.pos, p.scal, p.part, p.Hp, p.Tp, p.splits, false, (bf16_bits*)d_grad_hidden, ld_grad_hidden, p.H);
         SG_TRY_LAUNCH();
     }
     return SG_OK;

@@ -27,7 +27,7 @@ namespace sg {
 // largest stored values are 4 * 2^10, 16 * 2^10 and 128 * 2^8; the smallest
 // step of fp16 (2^-24) is 2^-34, 2^-34 and 2^-32 of the true values.
 constexpr int NS_EX = 10, NS_EG = 10, NS_EB = 8;
-constexpr int NS_NORM_BLOCKS = 64;
+constexpr uint32_t NS_NORM_BLOCKS = 512; // of a matrix; 2048 of a batch are enough for the card
 
 struct NsCoef {
     float a, b, c;
@@ -47,7 +47,6 @@ struct NsIn {
     const void* x;
     uint64_t ld, stride;
     uint32_t m, n;
-    bool wide; // rows start on 16 bytes and may be loaded as such
 };
 
 // 8 elements of a row from column c; what is past the end is 0
@@ -55,7 +54,7 @@ template <typename E>
 __device__ __forceinline__ void ns_load8(const NsIn& in, uint32_t b, uint32_t r, uint32_t c, float* v)
 {
     const E* x = static_cast<const E*>(in.x) + b * in.stride + r * in.ld + c;
-    if (in.wide && c + 8 <= in.n) {
+    if (c + 8 <= in.n) { // gfx950 loads 16 bytes at any element's address
         constexpr int VEC = RowIO<E>::VEC;
 #pragma unroll
         for (int i = 0; i < 8; i += VEC) RowIO<E>::unpack(load_chunk(x + i), v + i);
@@ -100,8 +99,9 @@ __global__ __launch_bounds__(256) void ns_pack_kernel(NsIn in, const double* par
                                                       double a, double b, double c, uint16_t* hi, uint16_t* lo,
                                                       uint32_t mp, uint32_t np, NsScale* scale)
 {
-    const uint32_t at = threadIdx.x % 64;
-    const double norm = sqrt(wave_sum64(at < parts ? part[blockIdx.y * parts + at] : 0.0));
+    double sum = 0.0;
+    for (uint32_t i = threadIdx.x % 64; i < parts; i += 64) sum += part[blockIdx.y * parts + i];
+    const double norm = sqrt(wave_sum64(sum));
     int e = 0, q = 0;
     double f = NAN; // an infinity or NaN, or 0 / 0: its whole matrix is NaN
     if (isfinite(norm) && norm > 0.0) {
@@ -144,20 +144,7 @@ struct NsPlanes {
     float* diag; // [B][ld], NULL: none
 };
 
-// four neighbours of a plane pair's values
-__device__ __forceinline__ f32x4 ns_get(const NsPlanes& p, uint64_t at)
-{
-    const s16x4 h = *reinterpret_cast<const s16x4*>(p.hi + at);
-    f32x4 v;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) v[i] = f16_value((uint16_t)h[i]);
-    if (p.lo) {
-        const s16x4 l = *reinterpret_cast<const s16x4*>(p.lo + at);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) v[i] += f16_value((uint16_t)l[i]);
-    }
-    return v;
-}
+// four neighbours
 __device__ __forceinline__ void ns_put(const NsPlanes& p, uint64_t at, f32x4 v)
 {
     s16x4 h, l;
@@ -171,16 +158,30 @@ __device__ __forceinline__ void ns_put(const NsPlanes& p, uint64_t at, f32x4 v)
     *reinterpret_cast<s16x4*>(p.hi + at) = h;
     if (p.lo) *reinterpret_cast<s16x4*>(p.lo + at) = l;
 }
-// the same four, one below the other: the mirrored half of a symmetric result
-__device__ __forceinline__ void ns_put_down(const NsPlanes& p, uint64_t at, f32x4 v)
+// The mirrored place of a wave's 16 x 16 block of a symmetric result: through
+// 512 bytes of LDS of the wave's own a plane, read back transposed, so that
+// a lane again has four neighbours.  A wave's LDS operations run in order.
+__device__ __forceinline__ void ns_put_mirrored(const NsPlanes& p, uint64_t base, uint32_t m0, uint32_t n0, f32x4 v,
+                                                char* lds)
 {
+    const uint32_t l = threadIdx.x % 64;
+    s16x4 h, q;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         uint16_t x, y;
         split_f16(v[i], &x, &y);
-        p.hi[at + i * p.ld] = x;
-        if (p.lo) p.lo[at + i * p.ld] = y;
+        h[i] = (short)x;
+        q[i] = (short)y;
     }
+    char* const w = lds + l % 16 * 32 + l / 16 * 8;                     // row m, columns n
+    char* const r = lds + (l / 16 * 4 + l % 16 / 4) * 32 + l % 4 * 8;   // four rows of one column
+    const uint64_t at = base + (n0 + l % 16) * p.ld + m0 + l / 16 * 4;
+    *reinterpret_cast<s16x4*>(w) = h;
+    if (p.lo) *reinterpret_cast<s16x4*>(w + 512) = q;
+    asm volatile("" ::: "memory");
+    *reinterpret_cast<s16x4*>(p.hi + at) = read_transposed((LdsS16x4*)r);
+    if (p.lo) *reinterpret_cast<s16x4*>(p.lo + at) = read_transposed((LdsS16x4*)(r + 512));
+    asm volatile("" ::: "memory");
 }
 
 // what rounding takes from the diagonal, where the four neighbours from (m, n) meet it
@@ -188,21 +189,23 @@ __device__ __forceinline__ void ns_put_diag(const NsPlanes& p, uint32_t batch, u
 {
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-        if (p.diag && m == n + i) p.diag[batch * p.ld + m] = v[i] - (float)(_Float16)v[i];
+        if (m == n + i) p.diag[batch * p.ld + m] = v[i] - (float)(_Float16)v[i];
 }
 
-// calls f(m, n, four sums) for what lies inside; M and N are multiples of 64
-template <class Cfg, class F>
-__device__ __forceinline__ void each_four(const f32x4 (&acc)[Cfg::MT][Cfg::NTT], const TileAt& at, const F& f)
+// A block of a symmetric result, and its mirror image; M and N are multiples of 64,
+// so a 16 x 16 block lies inside or outside.
+template <class Cfg>
+__device__ __forceinline__ void ns_put_symmetric(const NsPlanes& p, const TileAt& at, int i, int j, f32x4 v)
 {
-    const uint32_t l = threadIdx.x % 64;
-#pragma unroll
-    for (int i = 0; i < Cfg::MT; ++i)
-#pragma unroll
-        for (int j = 0; j < Cfg::NTT; ++j) {
-            const uint32_t m = at.m0 + i * 16 + l % 16, n = at.n0 + j * 16 + l / 16 * 4;
-            if (m < at.M && n < at.N) f(m, n, acc[i][j]);
-        }
+    const uint32_t l = threadIdx.x % 64, m0 = at.m0 + i * 16, n0 = at.n0 + j * 16;
+    if (m0 >= at.M || n0 >= at.N) return;
+    const uint64_t base = at.batch * p.batch;
+    const uint32_t m = m0 + l % 16, n = n0 + l / 16 * 4;
+    ns_put(p, base + m * p.ld + n, v);
+    if (p.diag && m0 == n0) ns_put_diag(p, at.batch, m, n, v);
+    // the mirrored block's own tile, if it is taken, writes it itself
+    const uint32_t tm = n0 / Cfg::BM, tn = m0 / Cfg::BN;
+    if (m0 < n0 && tn < tri_first<Cfg::BM, Cfg::BN>(tm)) ns_put_mirrored(p, base, m0, n0, v, at.lds + (at.wm * Cfg::WN + at.wn) * 1024);
 }
 
 // G = X X^T: the tiles on and above the diagonal, and their mirror images
@@ -211,16 +214,40 @@ struct NsGramEpi {
     template <class Cfg>
     __device__ __forceinline__ void run(const f32x4 (&acc)[Cfg::MT][Cfg::NTT], const TileAt& at) const
     {
-        const uint64_t b = at.batch * out.batch;
-        const bool mirror = at.bm0 + Cfg::BM <= at.bn0;
-        each_four<Cfg>(acc, at, [&](uint32_t m, uint32_t n, f32x4 v) {
-            v *= 1.f / (1 << (2 * NS_EX - NS_EG));
-            ns_put(out, b + m * out.ld + n, v);
-            ns_put_diag(out, at.batch, m, n, v);
-            if (mirror) ns_put_down(out, b + n * out.ld + m, v);
-        });
+#pragma unroll
+        for (int i = 0; i < Cfg::MT; ++i)
+#pragma unroll
+            for (int j = 0; j < Cfg::NTT; ++j)
+                ns_put_symmetric<Cfg>(out, at, i, j, acc[i][j] * (1.f / (1 << (2 * NS_EX - NS_EG))));
     }
 };
+
+// Four neighbours of planes for the blocks of rows i0 .. i0 + R of a wave's
+// part, all loaded before the first is used (what lies outside from element 0).
+template <class Cfg, int R>
+__device__ __forceinline__ void ns_get_rows(const NsPlanes& p, const TileAt& at, int i0, f32x4 (&v)[R][Cfg::NTT])
+{
+    const uint32_t l = threadIdx.x % 64;
+    s16x4 h[R][Cfg::NTT], q[R][Cfg::NTT];
+#pragma unroll
+    for (int i = 0; i < R; ++i)
+#pragma unroll
+        for (int j = 0; j < Cfg::NTT; ++j) {
+            const uint32_t m = at.m0 + (i0 + i) * 16 + l % 16, n = at.n0 + j * 16 + l / 16 * 4;
+            const uint64_t o = at.batch * p.batch + (m < at.M && n < at.N ? m * p.ld + n : 0);
+            h[i][j] = *reinterpret_cast<const s16x4*>(p.hi + o);
+            if (p.lo) q[i][j] = *reinterpret_cast<const s16x4*>(p.lo + o);
+        }
+#pragma unroll
+    for (int i = 0; i < R; ++i)
+#pragma unroll
+        for (int j = 0; j < Cfg::NTT; ++j)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                v[i][j][k] = f16_value((uint16_t)h[i][j][k]);
+                if (p.lo) v[i][j][k] += f16_value((uint16_t)q[i][j][k]);
+            }
+}
 
 // b G + c G^2 from the sums of G^2
 struct NsPolyEpi {
@@ -231,25 +258,42 @@ struct NsPolyEpi {
     template <class Cfg>
     __device__ __forceinline__ void run(const f32x4 (&acc)[Cfg::MT][Cfg::NTT], const TileAt& at) const
     {
-        const uint64_t b = at.batch * out.batch;
+        const uint32_t l = threadIdx.x % 64;
         const NsScale sc = scale[at.batch];
         const NsCoef k = step == 0 ? sc.first : coef;
         const int q0 = ns_q(sc, step);
         const float kb = ldexpf(k.b, NS_EB - NS_EG - 2 * q0), kc = ldexpf(k.c, NS_EB - 2 * NS_EG - 4 * q0);
-        const bool mirror = at.bm0 + Cfg::BM <= at.bn0;
-        each_four<Cfg>(acc, at, [&](uint32_t m, uint32_t n, f32x4 v) {
-            f32x4 q = ns_get(gram, b + m * gram.ld + n);
-            if (gram.diag) { // G = q + diag(d): G^2 = q^2 + d_m q + q d_n (+ d^2, below fp32's last bit)
-                const float* d = gram.diag + at.batch * gram.ld;
-                v += (d[m] + *reinterpret_cast<const f32x4*>(d + n)) * q;
+        // G = q + diag(d): G^2 = q^2 + d_m q + q d_n (+ d^2, below fp32's last bit)
+        float dm[Cfg::MT];
+        f32x4 dn[Cfg::NTT];
+        const float* const d = gram.diag ? gram.diag + at.batch * gram.ld : nullptr;
 #pragma unroll
-                for (int i = 0; i < 4; ++i) q[i] += m == n + i ? d[m] : 0.f;
-            }
-            v = kc * v + kb * q;
-            ns_put(out, b + m * out.ld + n, v);
-            ns_put_diag(out, at.batch, m, n, v);
-            if (mirror) ns_put_down(out, b + n * out.ld + m, v);
-        });
+        for (int i = 0; i < Cfg::MT; ++i) {
+            const uint32_t m = at.m0 + i * 16 + l % 16;
+            dm[i] = d ? d[m < at.M ? m : 0] : 0.f;
+        }
+#pragma unroll
+        for (int j = 0; j < Cfg::NTT; ++j) {
+            const uint32_t n = at.n0 + j * 16 + l / 16 * 4;
+            dn[j] = d ? *reinterpret_cast<const f32x4*>(d + (n < at.N ? n : 0)) : f32x4{0.f, 0.f, 0.f, 0.f};
+        }
+        constexpr int R = Cfg::MT % 4 == 0 ? 4 : Cfg::MT;
+#pragma unroll
+        for (int i0 = 0; i0 < Cfg::MT; i0 += R) {
+            f32x4 q[R][Cfg::NTT];
+            ns_get_rows<Cfg>(gram, at, i0, q);
+#pragma unroll
+            for (int i = 0; i < R; ++i)
+#pragma unroll
+                for (int j = 0; j < Cfg::NTT; ++j) {
+                    f32x4 v = acc[i0 + i][j] + (dm[i0 + i] + dn[j]) * q[i][j];
+                    const uint32_t m = at.m0 + (i0 + i) * 16 + l % 16, n = at.n0 + j * 16 + l / 16 * 4;
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) q[i][j][x] += m == n + x ? dm[i0 + i] : 0.f;
+                    v = kc * v + kb * q[i][j];
+                    ns_put_symmetric<Cfg>(out, at, i0 + i, j, v);
+                }
+        }
     }
 };
 
@@ -275,21 +319,40 @@ struct NsStepEpi {
         // the next planes' scale, or none
         const float up = ldexpf(1.f, last ? -NS_EX - q0 : q1 - q0);
         const float a = step == 0 ? sc.first.a : coef.a;
-        each_four<Cfg>(acc, at, [&](uint32_t r, uint32_t c, f32x4 v) {
-            const uint64_t p = at.batch * x.batch + r * x.ld + c;
-            f32x4 k = {a, a, a, a};
-            if (diag) {
-                const float* d = diag + at.batch * (uint64_t)sp;
-                const f32x4 one = tall ? *reinterpret_cast<const f32x4*>(d + c) : f32x4{d[r], d[r], d[r], d[r]};
-                k += one * (1.f / (1 << NS_EB));
-            }
-            v = (k * ns_get(x, p) + v * (1.f / (1 << NS_EB))) * up;
-            if (!last) {
-                ns_put(out, p, v);
-                return;
-            }
-            if (r < m && c < n) put_result(r, c, v, at.batch);
-        });
+        const uint32_t l = threadIdx.x % 64;
+        const float* const d = diag ? diag + at.batch * (uint64_t)sp : nullptr;
+        // a and the polynomial's diagonal, by rows, or by columns for a tall matrix
+        float dm[Cfg::MT];
+        f32x4 dn[Cfg::NTT];
+#pragma unroll
+        for (int i = 0; i < Cfg::MT; ++i) {
+            const uint32_t r = at.m0 + i * 16 + l % 16;
+            dm[i] = a + (d && !tall ? d[r < at.M ? r : 0] * (1.f / (1 << NS_EB)) : 0.f);
+        }
+#pragma unroll
+        for (int j = 0; j < Cfg::NTT; ++j) {
+            const uint32_t c = at.n0 + j * 16 + l / 16 * 4;
+            dn[j] = f32x4{0.f, 0.f, 0.f, 0.f};
+            if (d && tall) dn[j] = *reinterpret_cast<const f32x4*>(d + (c < at.N ? c : 0)) * (1.f / (1 << NS_EB));
+        }
+        constexpr int R = Cfg::MT % 4 == 0 ? 4 : Cfg::MT;
+#pragma unroll
+        for (int i0 = 0; i0 < Cfg::MT; i0 += R) {
+            f32x4 have[R][Cfg::NTT];
+            ns_get_rows<Cfg>(x, at, i0, have);
+#pragma unroll
+            for (int i = 0; i < R; ++i)
+#pragma unroll
+                for (int j = 0; j < Cfg::NTT; ++j) {
+                    const uint32_t r = at.m0 + (i0 + i) * 16 + l % 16, c = at.n0 + j * 16 + l / 16 * 4;
+                    const f32x4 v = ((dm[i0 + i] + dn[j]) * have[i][j] + acc[i0 + i][j] * (1.f / (1 << NS_EB))) * up;
+                    if (last) {
+                        if (r < m && c < n) put_result(r, c, v, at.batch);
+                    } else if (r < at.M && c < at.N) {
+                        ns_put(out, at.batch * out.batch + r * out.ld + c, v);
+                    }
+                }
+        }
     }
     __device__ __forceinline__ void put_result(uint32_t r, uint32_t c, f32x4 v, uint32_t batch) const
     {
@@ -410,10 +473,11 @@ extern "C" int sg_orthogonalize(const void* d_update, sg_dtype dt, uint32_t B, u
     NsWs w = ns_carve(cv, B, m, n, two);
     hipStream_t st = as_stream(stream);
 
-    const bool wide = reinterpret_cast<uintptr_t>(d_update) % 16 == 0 && ld * es % 16 == 0 && (B == 1 || stride * es % 16 == 0);
-    const NsIn in = {d_update, ld, stride, m, n, wide};
+    const NsIn in = {d_update, ld, stride, m, n};
     const uint64_t items = ceil_div((uint64_t)m * ceil_div(n, 8), 256);
-    const uint32_t parts = (uint32_t)(items < NS_NORM_BLOCKS ? items : NS_NORM_BLOCKS);
+    uint32_t parts = (uint32_t)ceil_div(2048, B);
+    if (parts > NS_NORM_BLOCKS) parts = NS_NORM_BLOCKS;
+    if (parts > items) parts = (uint32_t)items;
     const uint64_t pitems = ceil_div((uint64_t)w.mp * w.np / 8, 256);
     const dim3 ngrid(parts, B), pgrid((unsigned)(pitems < 4096 ? pitems : 4096), B);
     if (two) ns_norm_kernel<float><<<ngrid, 256, 0, st>>>(in, w.part);
