@@ -42,6 +42,9 @@ struct Mat {
     uint64_t ld;          // elements between rows, a multiple of 8
     uint64_t elems;       // from the start to the end of the last row
     uint64_t batch;       // elements between the matrices of a batch
+    // not 0: columns in panels of 256, so many elements apart, ld between the rows of one.
+    // A tile of a wide matrix then lies close together and not over a page a row
+    uint64_t panel;
 };
 
 struct Gemm {
@@ -71,16 +74,19 @@ struct TileLoader {
     static constexpr bool TWO = LAY == KS && U > 1 && NT / PER % 16 != 0;
     const uint16_t* p[2];
     uint64_t ld, left;   // elements from the tile's start to the operand's end
+    uint64_t panel;
     uint32_t src[2], kk, K; // the thread's first chunk, in bytes (for even and odd ones), and its k
     uint32_t apart;      // bytes between its chunks
 
-    __device__ __forceinline__ TileLoader(const Mat& m, uint64_t first, uint32_t batch, uint32_t K_) : ld(m.ld), K(K_)
+    __device__ __forceinline__ TileLoader(const Mat& m, uint64_t first, uint32_t batch, uint32_t K_)
+        : ld(m.ld), panel(m.panel), K(K_)
     {
-        const uint64_t at = LAY == KC ? first * m.ld : first;
+        const uint32_t tid = threadIdx.x % NT;
+        const uint64_t at = LAY == KC ? first * m.ld : panel ? first / 256 * panel + first % 256 : first;
         left = m.elems > at ? m.elems - at : 0;
         p[0] = m.p[0] + batch * m.batch + at;
         p[1] = m.p[1] ? m.p[1] + batch * m.batch + at : p[0];
-        const uint32_t r = threadIdx.x / PER, q = threadIdx.x % PER;
+        const uint32_t r = tid / PER, q = tid % PER;
         const uint32_t c = LAY == KC ? q ^ (r & 7) : q ^ (2 * (((r & 3) | ((r >> 3) & 1) << 2) & (R / 16 - 1)));
         src[0] = (r * (uint32_t)m.ld + c * 8) * 2;
         src[1] = (r * (uint32_t)m.ld + (c ^ (2 * (4 & (R / 16 - 1)))) * 8) * 2;
@@ -100,7 +106,7 @@ struct TileLoader {
     };
     __device__ __forceinline__ Step step(uint32_t k0, int plane, bool on, char* lds) const
     {
-        const uint64_t at = LAY == KC ? (uint64_t)k0 : (uint64_t)k0 * ld;
+        const uint64_t at = LAY == KS ? (uint64_t)k0 * ld : panel ? k0 / 256 * panel + k0 % 256 : (uint64_t)k0;
         uint64_t bytes = on && left > at ? (left - at) * 2 : 0;
         if (bytes > 0x7ffffff0ull) bytes = 0x7ffffff0ull;
         Step s;
@@ -109,7 +115,7 @@ struct TileLoader {
         s.off[0] = LAY == KS || k0 + kk < K ? src[0] : 0x80000000u;
         s.off[1] = src[1];
         s.apart = apart;
-        s.to = lds + (threadIdx.x / 64) * 1024;
+        s.to = lds + (threadIdx.x % NT / 64) * 1024;
         return s;
     }
 };
@@ -212,20 +218,24 @@ __device__ __forceinline__ bool tile_of(uint32_t tm, uint32_t tn, uint32_t tri, 
     return true;
 }
 
-template <int BM_, int BN_, int WM_, int WN_>
+// GR_: groups of WM x WN waves in a block, each with stages of its own and every
+// GR-th step; their sums are added at the end
+template <int BM_, int BN_, int WM_, int WN_, int GR_ = 1>
 struct TileCfg {
-    static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, NT = 64 * WM * WN;
+    static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, GR = GR_, NT = 64 * WM * WN;
     static constexpr int MT = BM / WM / 16, NTT = BN / WN / 16; // fragments of a wave
     static constexpr int STAGE = (BM + BN) * GEMM_BK * 2;
-    static constexpr int LDS = 2 * STAGE;
+    static constexpr int LDS = 2 * STAGE * GR;
+    static_assert(GR == 1 || (GR - 1) * BM * BN * 4 + 1024 * WM * WN <= LDS, "the other groups' sums, and a kilobyte a wave");
     // waves per SIMD that the LDS leaves room for (160 KB)
-    static constexpr int BLOCKS = 163840 / LDS, WAVES = BLOCKS * WM * WN / 4;
+    static constexpr int BLOCKS = 163840 / LDS, WAVES = BLOCKS * GR * WM * WN / 4;
     static constexpr int PER_SIMD = WAVES < 1 ? 1 : WAVES > 4 ? 4 : WAVES;
 };
 typedef TileCfg<256, 256, 2, 4> TileL;
 typedef TileCfg<128, 128, 2, 2> TileM;
-typedef TileCfg<64, 64, 2, 2> TileS;   // few tiles: more blocks
-typedef TileCfg<32, 128, 1, 4> TileRow; // few rows
+typedef TileCfg<64, 64, 2, 2> TileS;      // few tiles: more blocks
+typedef TileCfg<64, 64, 2, 2, 4> TileK;   // fewer than compute units: more waves to a tile
+typedef TileCfg<32, 128, 1, 4> TileRow;   // few rows
 
 // what an epilogue gets beside the sums
 struct TileAt {
@@ -248,16 +258,18 @@ struct TileAt {
 // Tiles one after another in a block, the next one's fetches under the epilogue, took
 // as long: a wait for fetches is one for the stores before them.
 template <class Cfg, int AL, int BL, bool F16, class Epi>
-__global__ __launch_bounds__(Cfg::NT, Cfg::PER_SIMD) void gemm_kernel(Gemm g, uint32_t batch, Epi epi)
+__global__ __launch_bounds__(Cfg::NT * Cfg::GR, Cfg::PER_SIMD) void gemm_kernel(Gemm g, uint32_t batch, Epi epi)
 {
-    __shared__ __align__(1024) char lds[Cfg::LDS];
+    __shared__ __align__(1024) char lds_all[Cfg::LDS];
     if (g.d_m) g.M = *g.d_m;
     if (g.d_k) g.K = (*g.d_k + GEMM_BK - 1) / GEMM_BK * GEMM_BK;
     TilePlace t;
     if (!tile_of<Cfg::BM, Cfg::BN>((g.M + Cfg::BM - 1) / Cfg::BM, (g.N + Cfg::BN - 1) / Cfg::BN, g.tri, g.splits, batch,
                                    &t))
         return;
-    const uint32_t w = threadIdx.x / 64, wm = w / Cfg::WN, wn = w % Cfg::WN;
+    const uint32_t w = threadIdx.x % Cfg::NT / 64, wm = w / Cfg::WN, wn = w % Cfg::WN;
+    const uint32_t group = uniform(threadIdx.x / Cfg::NT);
+    char* const lds = lds_all + group * 2 * Cfg::STAGE;
 
     typedef TileLoader<AL, Cfg::BM, Cfg::NT> LoadA;
     typedef TileLoader<BL, Cfg::BN, Cfg::NT> LoadB;
@@ -273,7 +285,8 @@ __global__ __launch_bounds__(Cfg::NT, Cfg::PER_SIMD) void gemm_kernel(Gemm g, ui
     // this part's steps of 64 k, then all of them again for the next segment
     const uint32_t ks = (g.K + GEMM_BK - 1) / GEMM_BK, per = (ks + g.splits - 1) / g.splits;
     const uint32_t first = t.split * per < ks ? t.split * per : ks, last = first + per < ks ? first + per : ks;
-    const uint32_t steps = (last - first) * g.nseg;
+    // a group's first k of a segment, and the steps of all (a group without a k of its own multiplies zeros)
+    const uint32_t steps = (last - first + Cfg::GR - 1) / Cfg::GR * g.nseg;
 
     f32x4 acc[Cfg::MT][Cfg::NTT];
 #pragma unroll
@@ -281,7 +294,7 @@ __global__ __launch_bounds__(Cfg::NT, Cfg::PER_SIMD) void gemm_kernel(Gemm g, ui
 #pragma unroll
         for (int j = 0; j < Cfg::NTT; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
 
-    uint32_t k = first, seg = 0; // of the next step to fetch; past the last one it fetches nothing
+    uint32_t k = first, seg = 0; // of the block's next step to fetch; past the last one it fetches nothing
     struct Fetch {
         typename LoadA::Step a;
         typename LoadB::Step b;
@@ -292,10 +305,11 @@ __global__ __launch_bounds__(Cfg::NT, Cfg::PER_SIMD) void gemm_kernel(Gemm g, ui
         }
     };
     const auto fetch = [&](char* to) {
-        const bool on = seg < g.nseg;
-        const Fetch f = {la.step(k * GEMM_BK, seg == 2, on, to), lb.step(k * GEMM_BK, seg == 1, on, to + UA)};
-        const bool wrap = k + 1 >= last;
-        k = wrap ? first : k + 1;
+        const bool on = seg < g.nseg && k + group < last;
+        const uint32_t k0 = (k + group) * GEMM_BK;
+        const Fetch f = {la.step(k0, seg == 2, on, to), lb.step(k0, seg == 1, on, to + UA)};
+        const bool wrap = k + Cfg::GR >= last;
+        k = wrap ? first : k + Cfg::GR;
         seg += wrap ? 1 : 0;
         return f;
     };
@@ -350,6 +364,23 @@ __global__ __launch_bounds__(Cfg::NT, Cfg::PER_SIMD) void gemm_kernel(Gemm g, ui
         __builtin_amdgcn_s_barrier();
         asm volatile("" ::: "memory");
     }
+    if (Cfg::GR > 1) { // the groups' sums, added in their order by the first
+        f32x4* const sums = reinterpret_cast<f32x4*>(lds_all);
+        constexpr int EACH = Cfg::MT * Cfg::NTT;
+        if (group > 0) {
+#pragma unroll
+            for (int i = 0; i < EACH; ++i)
+                sums[((group - 1) * EACH + i) * Cfg::NT + threadIdx.x % Cfg::NT] = acc[i / Cfg::NTT][i % Cfg::NTT];
+        }
+        __syncthreads();
+        if (group > 0) return;
+#pragma unroll
+        for (int q = 0; q < Cfg::GR - 1; ++q)
+#pragma unroll
+            for (int i = 0; i < EACH; ++i)
+                acc[i / Cfg::NTT][i % Cfg::NTT] += sums[(q * EACH + i) * Cfg::NT + threadIdx.x];
+        // the epilogue's own LDS lies behind what another wave may still be reading
+    }
     TileAt at;
     at.bm0 = t.m * Cfg::BM;
     at.bn0 = t.n * Cfg::BN;
@@ -361,9 +392,28 @@ __global__ __launch_bounds__(Cfg::NT, Cfg::PER_SIMD) void gemm_kernel(Gemm g, ui
     at.batch = t.batch;
     at.wm = wm;
     at.wn = wn;
-    at.lds = lds;
+    at.lds = Cfg::GR > 1 ? lds_all + (Cfg::GR - 1) * Cfg::BM * Cfg::BN * 4 : lds_all;
     epi.template run<Cfg>(acc, at);
 }
+
+// Which tile, by what each was measured to take: us for a step of 64 k of a
+// round of blocks, and beside the steps (launch, first fetches, epilogue), where the
+// card is full and where there is at most one block to a compute unit (L: a quarter of
+// them).  From products of 2048 and 4096 k, bf16, every layout within a tenth.
+enum TileKind { TILE_L, TILE_M, TILE_S, TILE_K };
+static double tile_time(TileKind kind, uint64_t tiles, uint64_t steps)
+{
+    static const struct {
+        double slots, step, beside, few, few_step, few_beside;
+    } t[] = {{256, 1.42, 20.0, 64, 1.07, 12.0}, {512, 0.90, 9.5, 256, 0.62, 7.0}, {1024, 0.70, 6.5, 512, 0.50, 5.0},
+             {256, 0.225, 6.5, 256, 0.225, 6.5}};
+    const auto& k = t[kind];
+    const uint64_t full = tiles / (uint64_t)k.slots, rest = tiles % (uint64_t)k.slots;
+    double us = full * (steps * k.step + k.beside);
+    if (rest > 0) us += rest <= (uint64_t)k.few ? steps * k.few_step + k.few_beside : steps * k.step + k.beside;
+    return us;
+}
+static uint64_t tile_side(TileKind kind) { return kind == TILE_L ? 256 : kind == TILE_M ? 128 : 64; }
 
 template <class Cfg, int AL, int BL, bool F16, class Epi>
 static int launch_gemm(const Gemm& g, uint32_t batch, const Epi& epi, hipStream_t st)
@@ -373,9 +423,50 @@ static int launch_gemm(const Gemm& g, uint32_t batch, const Epi& epi, hipStream_
     if (tm * tn * g.splits * batch >= (1ull << 31) || g.splits == 0) return SG_EUNSUPPORTED;
     if (g.a.ld > GEMM_MAX_LD || g.b.ld > GEMM_MAX_LD) return SG_EUNSUPPORTED;
     const uint32_t blocks = tile_count<Cfg::BM, Cfg::BN>((uint32_t)tm, (uint32_t)tn, g.tri) * g.splits * batch;
-    gemm_kernel<Cfg, AL, BL, F16, Epi><<<blocks, Cfg::NT, 0, st>>>(g, batch, epi);
+    gemm_kernel<Cfg, AL, BL, F16, Epi><<<blocks, Cfg::NT * Cfg::GR, 0, st>>>(g, batch, epi);
     SG_TRY_LAUNCH();
     return SG_OK;
+}
+
+// A tile of 16-bit results, through LDS to rows of 16 bytes a lane: as the sums
+// lie, a store is 32 bytes of each of 16 rows.  Rows and columns inside; the
+// rows start on 16 bytes, n is the first column past the matrix.
+template <class Cfg>
+struct TileRows {
+    static constexpr int CH = Cfg::BN / 8; // 16-byte chunks of a row
+    static_assert(Cfg::BM * Cfg::BN * 2 <= Cfg::LDS, "the tile fits where the operands were");
+    // where column n of the tile's row m lies; the chunk depends on the row, so that 16 rows' stores touch every bank
+    static __device__ __forceinline__ uint32_t place(uint32_t m, uint32_t n)
+    {
+        return m * (Cfg::BN * 2) + ((n / 8) ^ (m % 16 & (CH - 1))) * 16 + n % 8 * 2;
+    }
+    static __device__ __forceinline__ void put(char* lds, uint32_t m, uint32_t n, s16x4 v) // four neighbours
+    {
+        *reinterpret_cast<s16x4*>(lds + place(m, n)) = v;
+    }
+    // all of the block's threads, after a barrier; f(row, column, chunk) stores one
+    template <class F>
+    static __device__ __forceinline__ void each(const char* lds, const F& f)
+    {
+        static_assert(Cfg::BM * CH % Cfg::NT == 0, "whole rounds");
+#pragma unroll 4
+        for (int q = 0; q < Cfg::BM * CH / Cfg::NT; ++q) {
+            const uint32_t i = q * Cfg::NT + threadIdx.x, m = i / CH, c = i % CH;
+            f(m, c * 8, *reinterpret_cast<const s16x8*>(lds + m * (Cfg::BN * 2) + (c ^ (m % 16 & (CH - 1))) * 16));
+        }
+    }
+};
+
+// eight results, of which `left` lie inside
+__device__ __forceinline__ void store_tail(uint16_t* q, s16x8 v, uint32_t left)
+{
+    if (left >= 8) {
+        *reinterpret_cast<s16x8*>(q) = v;
+    } else {
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+            if ((uint32_t)k < left) q[k] = (uint16_t)v[k];
+    }
 }
 
 // fp16 planes of an fp32 value: 22 bits of it

@@ -133,22 +133,47 @@ __device__ __forceinline__ void ce_load8(const CeSrc& s, uint64_t r, uint32_t c,
     for (int i = 0; i < 8; ++i) v[i] = c + i < s.n ? RowIO<E>::get(x + i) : 0.f;
 }
 
+// items of `per` a row; most are few enough for a 32-bit division
+struct CeItems {
+    uint64_t n;
+    uint32_t per;
+    __device__ __forceinline__ CeItems(uint64_t n_, uint32_t per_) : n(n_), per(per_) {}
+    __device__ __forceinline__ void split(uint64_t i, uint64_t* row, uint32_t* at) const
+    {
+        if (n <= 0xffffffffull) {
+            *row = (uint32_t)i / per;
+            *at = (uint32_t)i - (uint32_t)*row * per;
+        } else {
+            *row = i / per;
+            *at = (uint32_t)(i - *row * per);
+        }
+    }
+};
+
 // the largest magnitude of the rows (of the live ones: row != NULL)
 __global__ __launch_bounds__(256) void ce_max_kernel(CeSrc s, uint64_t rows, const uint32_t* row, const CeScal* scal,
                                                      uint32_t* out)
 {
     const uint64_t n = row ? scal->live : rows;
     const uint32_t per = (s.n + 7) / 8;
+    const CeItems items(n * per, per);
     uint32_t m = 0;
-    for (uint64_t i = blockIdx.x * 256ull + threadIdx.x; i < n * per; i += gridDim.x * 256ull) {
-        float v[8];
-        const uint64_t r = i / per;
-        ce_load8<float>(s, row ? row[r] : r, (uint32_t)(i % per) * 8, v);
+    for (uint64_t i0 = blockIdx.x * 256ull + threadIdx.x; i0 < items.n; i0 += gridDim.x * 1024ull) {
+        float v[4][8]; // four loads of 32 bytes under way
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-            const uint32_t b = __float_as_uint(v[k]) & 0x7fffffffu;
-            m = b > m ? b : m;
+        for (int u = 0; u < 4; ++u) {
+            uint64_t i = i0 + u * gridDim.x * 256ull, r;
+            uint32_t c;
+            items.split(i < items.n ? i : i0, &r, &c);
+            ce_load8<float>(s, row ? row[r] : r, c * 8, v[u]);
         }
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                const uint32_t b = __float_as_uint(v[u][k]) & 0x7fffffffu;
+                m = b > m ? b : m;
+            }
     }
 #pragma unroll
     for (int d = 1; d < 64; d *= 2) {
@@ -169,9 +194,12 @@ __global__ __launch_bounds__(256) void ce_pack_kernel(CeSrc s, uint64_t rows, co
     const uint64_t n = row ? scal->live : rows, padded = row ? (n + 63) / 64 * 64 : n;
     const uint32_t per = np / 8;
     const int e = lo ? ce_exponent(*max_bits) : 0;
-    for (uint64_t i = blockIdx.x * 256ull + threadIdx.x; i < padded * per; i += gridDim.x * 256ull) {
-        const uint64_t r = i / per;
-        const uint32_t c = (uint32_t)(i % per) * 8;
+    const CeItems items(padded * per, per);
+    for (uint64_t i = blockIdx.x * 256ull + threadIdx.x; i < items.n; i += gridDim.x * 256ull) {
+        uint64_t r;
+        uint32_t c;
+        items.split(i, &r, &c);
+        c *= 8;
         float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
         if (r < n && c < s.n) ce_load8<E>(s, row ? row[r] : r, c, v);
         if (lo) {
@@ -202,10 +230,13 @@ __device__ __forceinline__ float ce_decode(uint32_t code)
     return code ? __uint_as_float((code << 13) + 0x20000000u) : 0.f;
 }
 
-// g and the exponentials it comes from: rows of ld
+// g and the exponentials it comes from: panels of 256 tokens, in each the rows' 256
+// one after another.  (As rows of a vocabulary, a tile's rows lay on as many pages;
+// 8192 x 131072 x 4096: PANELNOTE)
 struct CeG {
     uint16_t *hi, *lo;
-    uint64_t ld;
+    uint64_t rows; // of a panel
+    __device__ __forceinline__ uint64_t at(uint32_t m, uint32_t n) const { return (n / 256 * rows + m) * 256 + n % 256; }
 };
 
 // Where the logits' products end the first time: the rows' statistics over the
@@ -293,13 +324,6 @@ struct CeLogitsEpi {
             sum[i] += __shfl_xor(sum[i], 16);
             sum[i] += __shfl_xor(sum[i], 32);
             if (l < 16) ls[at.wn * Cfg::BM + q] = sum[i];
-            if (g.hi && at.bm0 + q < at.M) {
-#pragma unroll
-                for (int j = 0; j < Cfg::NTT; ++j) {
-                    const uint32_t n = at.n0 + j * 16 + l / 16 * 4;
-                    if (n < Vp) keep(at.bm0 + q, n, acc[i][j]);
-                }
-            }
         }
         __syncthreads();
         if (at.wn == 0 && l < 16) {
@@ -313,21 +337,36 @@ struct CeLogitsEpi {
                     stat[(uint64_t)(at.bm0 + q) * groups + at.bn0 / Cfg::BN] = make_float2(mx[i], s);
             }
         }
+        if (g.hi) keep<Cfg>(acc, at);
     }
-    __device__ __forceinline__ void keep(uint32_t m, uint32_t n, f32x4 e) const
+    // the exponentials, a plane after another through LDS (the statistics lie there until they are written)
+    template <class Cfg>
+    __device__ __forceinline__ void keep(const f32x4 (&e)[Cfg::MT][Cfg::NTT], const TileAt& at) const
     {
-        s16x4 h, q;
+        const uint32_t l = threadIdx.x % 64;
+        typedef TileRows<Cfg> Rows;
+        const auto put = [&](uint16_t* out, auto low) {
+            __syncthreads();
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            if (PLANES) {
-                h[k] = (short)(__float_as_uint(e[k]) >> 16);
-                q[k] = (short)__float_as_uint(e[k]);
-            } else {
-                h[k] = (short)ce_code(e[k]);
-            }
-        }
-        *reinterpret_cast<s16x4*>(g.hi + m * g.ld + n) = h;
-        if (PLANES) *reinterpret_cast<s16x4*>(g.lo + m * g.ld + n) = q;
+            for (int i = 0; i < Cfg::MT; ++i)
+#pragma unroll
+                for (int j = 0; j < Cfg::NTT; ++j) {
+                    s16x4 w;
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const uint32_t bits = __float_as_uint(e[i][j][k]);
+                        w[k] = (short)(!PLANES ? ce_code(e[i][j][k]) : decltype(low)::value ? bits : bits >> 16);
+                    }
+                    Rows::put(at.lds, at.m0 - at.bm0 + i * 16 + l % 16, at.n0 - at.bn0 + j * 16 + l / 16 * 4, w);
+                }
+            __syncthreads();
+            Rows::each(at.lds, [&](uint32_t m, uint32_t n, s16x8 v) {
+                if (at.bm0 + m < at.M && at.bn0 + n < Vp)
+                    *reinterpret_cast<s16x8*>(out + g.at(at.bm0 + m, at.bn0 + n)) = v;
+            });
+        };
+        put(g.hi, std::false_type());
+        if (PLANES) put(g.lo, std::true_type());
     }
 };
 
@@ -379,8 +418,8 @@ struct CePieceEpi {
                     }
                 }
                 if (m >= at.M || n >= Vp) continue;
-                *reinterpret_cast<s16x4*>(g.hi + m * g.ld + n) = h;
-                if (PLANES) *reinterpret_cast<s16x4*>(g.lo + m * g.ld + n) = q;
+                *reinterpret_cast<s16x4*>(g.hi + g.at(m, n)) = h;
+                if (PLANES) *reinterpret_cast<s16x4*>(g.lo + g.at(m, n)) = q;
             }
     }
 };
@@ -426,16 +465,16 @@ __global__ __launch_bounds__(256) void ce_join_kernel(CeArgs p, const uint32_t* 
 }
 
 // kept exponentials -> g, in place; rows up to the next multiple of 64 are
-// zeros.  A block takes 2048 columns of a row.
+// zeros.  A block takes 8 rows of a panel.
 __global__ __launch_bounds__(256) void ce_grad_kernel(const uint32_t* row, const int32_t* label, const float2* stat,
                                                       uint32_t groups, uint32_t group_cols, const CeRow* info,
-                                                      const CeScal* scal, CeG g, uint32_t Vp, float c)
+                                                      const CeScal* scal, CeG g, float c)
 {
-    const uint32_t cols = (Vp + 2047) / 2048, j = blockIdx.x / cols, v0 = (blockIdx.x % cols) * 2048 + threadIdx.x * 8;
-    const uint32_t live = scal->live;
-    if (j >= (live + 63) / 64 * 64 || v0 >= Vp) return;
-    u32x4* const hi = reinterpret_cast<u32x4*>(g.hi + j * g.ld + v0);
-    u32x4* const lo = g.lo ? reinterpret_cast<u32x4*>(g.lo + j * g.ld + v0) : nullptr;
+    const uint32_t per = (uint32_t)(g.rows / 8), v0 = blockIdx.x / per * 256 + threadIdx.x % 32 * 8;
+    const uint32_t j = blockIdx.x % per * 8 + threadIdx.x / 32, live = scal->live;
+    if (j >= (live + 63) / 64 * 64) return;
+    u32x4* const hi = reinterpret_cast<u32x4*>(g.hi + g.at(j, v0));
+    u32x4* const lo = g.lo ? reinterpret_cast<u32x4*>(g.lo + g.at(j, v0)) : nullptr;
     if (j >= live) {
         *hi = u32x4{0, 0, 0, 0};
         if (lo) *lo = u32x4{0, 0, 0, 0};
@@ -477,7 +516,7 @@ __global__ __launch_bounds__(256) void ce_zero_kernel(const CeScal* scal, CeG g,
     const uint32_t live = scal->live, end = (live + 63) / 64 * 64;
     const uint32_t per = Vp / 8;
     for (uint64_t i = blockIdx.x * 256ull + threadIdx.x; i < (uint64_t)(end - live) * per; i += gridDim.x * 256ull) {
-        const uint64_t at = (live + i / per) * g.ld + i % per * 8;
+        const uint64_t at = g.at(live + (uint32_t)(i / per), (uint32_t)(i % per) * 8);
         *reinterpret_cast<u32x4*>(g.hi + at) = u32x4{0, 0, 0, 0};
         if (g.lo) *reinterpret_cast<u32x4*>(g.lo + at) = u32x4{0, 0, 0, 0};
     }
@@ -535,13 +574,31 @@ struct CeHeadEpi {
     const CeScal* scal;
     void* out;
     uint64_t ld;
-    bool planes, wide; // wide: four neighbours are stored at once
+    bool planes, wide; // wide: rows start on 16 bytes
     template <class Cfg>
     __device__ __forceinline__ void run(const f32x4 (&acc)[Cfg::MT][Cfg::NTT], const TileAt& at) const
     {
         const uint32_t l = threadIdx.x % 64;
         const int unit = planes ? -ce_exponent(scal->max_g) - ce_exponent(scal->max_x) : 0;
         const float top = (float)scal->top;
+        if (!planes && wide) {
+#pragma unroll
+            for (int i = 0; i < Cfg::MT; ++i)
+#pragma unroll
+                for (int j = 0; j < Cfg::NTT; ++j) {
+                    s16x4 w;
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) w[k] = __builtin_bit_cast(short, (__bf16)(acc[i][j][k] * top));
+                    TileRows<Cfg>::put(at.lds, at.m0 - at.bm0 + i * 16 + l % 16, at.n0 - at.bn0 + j * 16 + l / 16 * 4, w);
+                }
+            __syncthreads();
+            TileRows<Cfg>::each(at.lds, [&](uint32_t m, uint32_t n, s16x8 v) {
+                m += at.bm0;
+                n += at.bn0;
+                if (m < at.M && n < at.N) store_tail(static_cast<uint16_t*>(out) + m * ld + n, v, at.N - n);
+            });
+            return;
+        }
 #pragma unroll
         for (int i = 0; i < Cfg::MT; ++i)
 #pragma unroll
@@ -586,7 +643,7 @@ struct CePlan {
     uint32_t H, Hp, Tp, piece; // Hp, Tp: rounded up to 64; piece: columns of g
     uint32_t groups, splits;
     bool two, pack, kept, grads, hidden;
-    int tile; // of the logits' product: 0 large, 1 middle, 2 few rows
+    int tile, tile_w, tile_x; // of the logits' product, dw and dx: 0 large, 1 middle, 2 few rows
     CeScal* scal;
     uint32_t* row;
     int32_t* pos;
@@ -610,7 +667,15 @@ static CePlan ce_plan(Carver& cv, uint64_t T, uint64_t V, uint32_t H, sg_dtype d
     p.grads = hidden || dhead;
     // the head as it lies: bf16 rows that start on 16 bytes, near enough to one another
     p.pack = p.two || H % 8 || ld_head % 8 || reinterpret_cast<uintptr_t>(head) % 16 || ld_head > GEMM_MAX_LD;
-    p.tile = T <= 32 ? 2 : ceil_div(T, 256) * ceil_div(V, 256) >= 256 ? 0 : 1;
+    // by what the tiles take (tile_time); up to 32 rows the product is a read of the head, and a tile of 32 rows leaves
+    // room for more blocks to a compute unit (TILENOTE)
+    const uint64_t nseg = p.two ? 3 : 1, kh = ceil_div(H, 64) * nseg, kt = ceil_div(T, 64) * nseg;
+    const auto tiles = [](uint64_t m, uint64_t n, uint64_t side) { return ceil_div(m, side) * ceil_div(n, side); };
+    const auto pick = [&](uint64_t m, uint64_t n, uint64_t steps) {
+        return tile_time(TILE_L, tiles(m, n, 256), steps) <= tile_time(TILE_M, tiles(m, n, 128), steps) ? 0 : 1;
+    };
+    p.tile = T <= 32 ? 2 : pick(T, V, kh);
+    p.tile_w = pick(V, H, kt);
     p.groups = (uint32_t)ceil_div(V, ce_tile_cols(p.tile));
     const uint64_t Vp = align_up(V, 256), es = p.two ? 4 : 2;
     p.kept = Vp <= (1u << 20) && p.Tp * Vp * es <= keep;
@@ -621,10 +686,23 @@ static CePlan ce_plan(Carver& cv, uint64_t T, uint64_t V, uint32_t H, sg_dtype d
         c = c < 256 ? 256 : c > (1u << 20) ? (1u << 20) : c;
         p.piece = (uint32_t)(c < Vp ? c : Vp);
     }
-    // dx has few tiles and a long sum: the vocabulary in parts until there are blocks enough
-    const uint64_t tiles = p.tile == 2 ? ceil_div(p.Hp, 128) : ceil_div(p.Tp, 128) * ceil_div(p.Hp, 128);
-    const uint64_t want = ceil_div(512, tiles), most = ceil_div(p.piece, 512);
-    p.splits = (uint32_t)(want < most ? want : most);
+    // dx has few tiles and a long sum: the vocabulary in parts, whose sums are written and read once more
+    double least = 1e300;
+    const uint64_t kv = ceil_div(p.piece, 64);
+    for (int t = T <= 32 ? 2 : 0; t <= (T <= 32 ? 2 : 1); ++t) {
+        const uint64_t n = t == 2 ? ceil_div(H, 128) : tiles(T, H, t == 0 ? 256 : 128);
+        for (uint64_t s = 1; s <= 64 && s <= kv; ++s) {
+            const uint64_t per = ceil_div(kv, s);
+            if (ceil_div(kv, per) != s) continue; // a part without a step
+            const double us = tile_time(t == 0 ? TILE_L : t == 1 ? TILE_M : TILE_S, n * s, per * nseg) +
+                              8.0 * s * p.Tp * p.Hp / 4.5e6;
+            if (us < least) {
+                least = us;
+                p.tile_x = t;
+                p.splits = (uint32_t)s;
+            }
+        }
+    }
 
     p.scal = cv.take<CeScal>(1);
     p.row = cv.take<uint32_t>(p.Tp);
@@ -645,7 +723,7 @@ template <int AL, int BL, bool F16, class Epi>
 static int ce_product(int tile, const Gemm& g, const Epi& e, hipStream_t st)
 {
     if (tile == 0) return launch_gemm<TileL, AL, BL, F16>(g, 1, e, st);
-    if (AL == KS || tile == 1) return launch_gemm<TileM, AL, BL, F16>(g, 1, e, st); // dw has the vocabulary's rows
+    if (AL == KS || tile == 1) return launch_gemm<TileM, AL, BL, F16>(g, 1, e, st);
     if constexpr (AL == KC) return launch_gemm<TileRow, AL, BL, F16>(g, 1, e, st);
     return SG_EUNSUPPORTED;
 }
@@ -656,7 +734,7 @@ static bool ce_sizes(uint64_t T, uint64_t V, uint64_t H, sg_dtype dt)
 }
 static bool ce_supported(uint64_t T, uint64_t V, uint64_t H)
 {
-    // blocks of 128 x 128 tiles, and of 2048 columns of a row
+    // blocks of 32 x 128 tiles, and of 8 x 256 elements of g
     return H <= (1u << 20) && T <= (1u << 24) && ceil_div(T, 32) * ceil_div(V, 128) < (1ull << 31) &&
            align_up(T, 64) * ceil_div(V, 2048) < (1ull << 31);
 }
@@ -735,10 +813,10 @@ extern "C" int sg_linear_ce_loss(const void* d_hidden, uint64_t ld_hidden, const
     const uint16_t* const w0 = p.pack ? p.w[0] : static_cast<const uint16_t*>(d_head);
     // rows v0 .. v0 + n of the head
     const auto head = [&](uint64_t v0, uint64_t n) {
-        return Mat{{w0 + v0 * ldw, p.w[1] ? p.w[1] + v0 * ldw : nullptr}, ldw, (n - 1) * ldw + (p.pack ? p.Hp : H), 0};
+        return Mat{{w0 + v0 * ldw, p.w[1] ? p.w[1] + v0 * ldw : nullptr}, ldw, (n - 1) * ldw + (p.pack ? p.Hp : H), 0, 0};
     };
-    const Mat mx = {{p.x[0], p.x[1]}, p.Hp, (uint64_t)p.Tp * p.Hp, 0};
-    const CeG none = {nullptr, nullptr, 0}, g = {p.g[0], p.g[1], p.piece};
+    const Mat mx = {{p.x[0], p.x[1]}, p.Hp, (uint64_t)p.Tp * p.Hp, 0, 0};
+    const CeG none = {nullptr, nullptr, 0}, g = {p.g[0], p.g[1], p.Tp};
     const uint32_t* live = &p.scal->live;
     const uint32_t k1 = p.pack ? p.Hp : p.H;
     int rc;
@@ -757,8 +835,8 @@ extern "C" int sg_linear_ce_loss(const void* d_hidden, uint64_t ld_hidden, const
     for (uint64_t v0 = 0; v0 < V; v0 += p.piece) {
         const uint64_t n = V - v0 < p.piece ? V - v0 : p.piece, np = align_up(n, 64);
         if (p.kept) {
-            ce_grad_kernel<<<(unsigned)(p.Tp * ceil_div(p.piece, 2048)), 256, 0, st>>>(
-                p.row, d_label, p.stat, p.groups, ce_tile_cols(p.tile), p.info, p.scal, g, p.piece, c);
+            ce_grad_kernel<<<(unsigned)(p.Tp / 8 * (p.piece / 256)), 256, 0, st>>>(
+                p.row, d_label, p.stat, p.groups, ce_tile_cols(p.tile), p.info, p.scal, g, c);
             SG_TRY_LAUNCH();
         } else {
             const Gemm g2 = {mx, head(v0, n), (uint32_t)T, (uint32_t)n, k1, nseg, 1, 0, live, nullptr};
@@ -770,19 +848,17 @@ extern "C" int sg_linear_ce_loss(const void* d_hidden, uint64_t ld_hidden, const
             ce_zero_kernel<<<256, 256, 0, st>>>(p.scal, g, p.piece);
             SG_TRY_LAUNCH();
         }
-        const Mat mg = {{p.g[0], p.g[1]}, p.piece, (uint64_t)p.Tp * p.piece, 0};
+        const Mat mg = {{p.g[0], p.g[1]}, 256, (uint64_t)p.Tp * p.piece, 0, (uint64_t)p.Tp * 256};
         if (d_grad_head) {
-            const CeHeadEpi e = {p.scal, static_cast<char*>(d_grad_head) + v0 * ld_grad_head * es, ld_grad_head, p.two, wide(d_grad_head, ld_grad_head, 4 * es)};
+            const CeHeadEpi e = {p.scal, static_cast<char*>(d_grad_head) + v0 * ld_grad_head * es, ld_grad_head, p.two, wide(d_grad_head, ld_grad_head, 16)};
             const Gemm g3 = {mg, mx, (uint32_t)n, p.H, 0, nseg, 1, 0, nullptr, live};
-            const int tile = T > 64 && ceil_div(n, 256) * ceil_div(H, 256) >= 256 ? 0 : 1;
-            rc = p.two ? ce_product<KS, KS, true>(tile, g3, e, st) : ce_product<KS, KS, false>(tile, g3, e, st);
+            rc = p.two ? ce_product<KS, KS, true>(p.tile_w, g3, e, st) : ce_product<KS, KS, false>(p.tile_w, g3, e, st);
             if (rc) return rc;
         }
         if (d_grad_hidden) {
             const CeHiddenEpi e = {p.part, p.Hp, p.Tp, v0 > 0};
             const Gemm g4 = {mg, head(v0, n), (uint32_t)T, p.H, (uint32_t)np, nseg, p.splits, 0, live, nullptr};
-            const int tile = p.tile == 2 ? 2 : p.splits == 1 ? 0 : 1;
-            rc = p.two ? ce_product<KC, KS, true>(tile, g4, e, st) : ce_product<KC, KS, false>(tile, g4, e, st);
+            rc = p.two ? ce_product<KC, KS, true>(p.tile_x, g4, e, st) : ce_product<KC, KS, false>(p.tile_x, g4, e, st);
             if (rc) return rc;
         }
     }

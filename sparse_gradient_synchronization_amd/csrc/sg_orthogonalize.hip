@@ -17,6 +17,8 @@
 // outweighs the norm.  Then X itself would leave fp16 at its lower end, so the planes
 // hold X 2^q; a step multiplies X by at most 4, so q falls by 2 a step.
 #include <cmath>
+#include <type_traits>
+
 #include "sg_gemm.h"
 #include "sg_rows.h"
 
@@ -145,6 +147,19 @@ struct NsPlanes {
 };
 
 // four neighbours
+__device__ __forceinline__ f32x4 ns_get(const NsPlanes& p, uint64_t at)
+{
+    const s16x4 h = *reinterpret_cast<const s16x4*>(p.hi + at);
+    f32x4 v;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = f16_value((uint16_t)h[i]);
+    if (p.lo) {
+        const s16x4 l = *reinterpret_cast<const s16x4*>(p.lo + at);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] += f16_value((uint16_t)l[i]);
+    }
+    return v;
+}
 __device__ __forceinline__ void ns_put(const NsPlanes& p, uint64_t at, f32x4 v)
 {
     s16x4 h, l;
@@ -158,32 +173,6 @@ __device__ __forceinline__ void ns_put(const NsPlanes& p, uint64_t at, f32x4 v)
     *reinterpret_cast<s16x4*>(p.hi + at) = h;
     if (p.lo) *reinterpret_cast<s16x4*>(p.lo + at) = l;
 }
-// The mirrored place of a wave's 16 x 16 block of a symmetric result: through
-// 512 bytes of LDS of the wave's own a plane, read back transposed, so that
-// a lane again has four neighbours.  A wave's LDS operations run in order.
-__device__ __forceinline__ void ns_put_mirrored(const NsPlanes& p, uint64_t base, uint32_t m0, uint32_t n0, f32x4 v,
-                                                char* lds)
-{
-    const uint32_t l = threadIdx.x % 64;
-    s16x4 h, q;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        uint16_t x, y;
-        split_f16(v[i], &x, &y);
-        h[i] = (short)x;
-        q[i] = (short)y;
-    }
-    char* const w = lds + l % 16 * 32 + l / 16 * 8;                     // row m, columns n
-    char* const r = lds + (l / 16 * 4 + l % 16 / 4) * 32 + l % 4 * 8;   // four rows of one column
-    const uint64_t at = base + (n0 + l % 16) * p.ld + m0 + l / 16 * 4;
-    *reinterpret_cast<s16x4*>(w) = h;
-    if (p.lo) *reinterpret_cast<s16x4*>(w + 512) = q;
-    asm volatile("" ::: "memory");
-    *reinterpret_cast<s16x4*>(p.hi + at) = read_transposed((LdsS16x4*)r);
-    if (p.lo) *reinterpret_cast<s16x4*>(p.lo + at) = read_transposed((LdsS16x4*)(r + 512));
-    asm volatile("" ::: "memory");
-}
-
 // what rounding takes from the diagonal, where the four neighbours from (m, n) meet it
 __device__ __forceinline__ void ns_put_diag(const NsPlanes& p, uint32_t batch, uint32_t m, uint32_t n, f32x4 v)
 {
@@ -192,51 +181,114 @@ __device__ __forceinline__ void ns_put_diag(const NsPlanes& p, uint32_t batch, u
         if (m == n + i) p.diag[batch * p.ld + m] = v[i] - (float)(_Float16)v[i];
 }
 
-// A block of a symmetric result, and its mirror image; M and N are multiples of 64,
-// so a 16 x 16 block lies inside or outside.
-template <class Cfg>
-__device__ __forceinline__ void ns_put_symmetric(const NsPlanes& p, const TileAt& at, int i, int j, f32x4 v)
+// A tile's values as planes, through LDS (TileRows), and with `mirror` in the
+// transposed place too: there ds_read_b64_tr_b16 hands a lane eight rows of a
+// column.  M and N are multiples of 64.
+template <class Cfg, bool TWO>
+__device__ __forceinline__ void ns_put_tile(const NsPlanes& p, const TileAt& at, f32x4 (&v)[Cfg::MT][Cfg::NTT],
+                                            bool mirror)
 {
-    const uint32_t l = threadIdx.x % 64, m0 = at.m0 + i * 16, n0 = at.n0 + j * 16;
-    if (m0 >= at.M || n0 >= at.N) return;
+    static_assert(Cfg::BM == Cfg::BN, "a mirrored tile is a tile");
+    const uint32_t l = threadIdx.x % 64, mr = at.m0 - at.bm0, nr = at.n0 - at.bn0;
     const uint64_t base = at.batch * p.batch;
-    const uint32_t m = m0 + l % 16, n = n0 + l / 16 * 4;
-    ns_put(p, base + m * p.ld + n, v);
-    if (p.diag && m0 == n0) ns_put_diag(p, at.batch, m, n, v);
-    // the mirrored block's own tile, if it is taken, writes it itself
-    const uint32_t tm = n0 / Cfg::BM, tn = m0 / Cfg::BN;
-    if (m0 < n0 && tn < tri_first<Cfg::BM, Cfg::BN>(tm)) ns_put_mirrored(p, base, m0, n0, v, at.lds + (at.wm * Cfg::WN + at.wn) * 1024);
+    typedef TileRows<Cfg> Rows;
+    const auto put = [&](uint16_t* out, auto low) {
+#pragma unroll
+        for (int i = 0; i < Cfg::MT; ++i)
+#pragma unroll
+            for (int j = 0; j < Cfg::NTT; ++j) {
+                s16x4 w;
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    uint16_t x, y;
+                    split_f16(v[i][j][k], &x, &y);
+                    w[k] = (short)(decltype(low)::value ? y : x);
+                }
+                Rows::put(at.lds, mr + i * 16 + l % 16, nr + j * 16 + l / 16 * 4, w);
+            }
+        __syncthreads();
+        Rows::each(at.lds, [&](uint32_t m, uint32_t n, s16x8 w) {
+            if (at.bm0 + m < at.M && at.bn0 + n < at.N)
+                *reinterpret_cast<s16x8*>(out + base + (at.bm0 + m) * p.ld + at.bn0 + n) = w;
+        });
+        if (!mirror) return;
+        // a wave: 16 columns, 32 rows at a time
+        constexpr uint32_t WAVES = Cfg::NT / 64, PARTS = Cfg::BM / 32;
+        for (uint32_t i = threadIdx.x / 64; i < Cfg::BN / 16 * PARTS; i += WAVES) {
+            const uint32_t n0 = i / PARTS * 16, m0 = i % PARTS * 32 + l / 16 * 8;
+            // the lane's share of a group's four rows: row l % 16 / 4, columns l % 4 * 4
+            const uint32_t r = m0 + l % 16 / 4, c = n0 + l % 4 * 4;
+            const s16x4 lo = read_transposed((LdsS16x4*)(at.lds + Rows::place(r, c))),
+                        hi = read_transposed((LdsS16x4*)(at.lds + Rows::place(r + 4, c)));
+            const uint32_t n = at.bn0 + n0 + l % 16, m = at.bm0 + m0;
+            if (n < at.N && m < at.M)
+                *reinterpret_cast<s16x8*>(out + base + n * p.ld + m) = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+        }
+    };
+    // Both planes are taken from the same fp32 numbers: not rounded to fp16 from a product and a sum that were never
+    // rounded to fp32 (the first plane alone, in one instruction), and not both halves kept from the first pass (they spill).
+    const auto settle = [&]() {
+#pragma unroll
+        for (int i = 0; i < Cfg::MT; ++i)
+#pragma unroll
+            for (int j = 0; j < Cfg::NTT; ++j) asm volatile("" : "+v"(v[i][j]));
+    };
+    if (TWO) settle();
+    put(p.hi, std::false_type());
+    if (!TWO) return;
+    settle();
+    __syncthreads(); // the first plane is out
+    put(p.lo, std::true_type());
+}
+
+// what rounding takes from the diagonal of a tile on it
+template <class Cfg>
+__device__ __forceinline__ void ns_put_tile_diag(const NsPlanes& p, const TileAt& at,
+                                                 const f32x4 (&v)[Cfg::MT][Cfg::NTT])
+{
+    if (at.bm0 != at.bn0) return;
+    const uint32_t l = threadIdx.x % 64;
+#pragma unroll
+    for (int i = 0; i < Cfg::MT; ++i)
+#pragma unroll
+        for (int j = 0; j < Cfg::NTT; ++j)
+            if (at.m0 + i * 16 == at.n0 + j * 16 && at.m0 + i * 16 < at.M)
+                ns_put_diag(p, at.batch, at.m0 + i * 16 + l % 16, at.n0 + j * 16 + l / 16 * 4, v[i][j]);
 }
 
 // G = X X^T: the tiles on and above the diagonal, and their mirror images
+template <bool TWO>
 struct NsGramEpi {
     NsPlanes out;
     template <class Cfg>
-    __device__ __forceinline__ void run(const f32x4 (&acc)[Cfg::MT][Cfg::NTT], const TileAt& at) const
+    __device__ __forceinline__ void run(f32x4 (&acc)[Cfg::MT][Cfg::NTT], const TileAt& at) const
     {
 #pragma unroll
         for (int i = 0; i < Cfg::MT; ++i)
 #pragma unroll
-            for (int j = 0; j < Cfg::NTT; ++j)
-                ns_put_symmetric<Cfg>(out, at, i, j, acc[i][j] * (1.f / (1 << (2 * NS_EX - NS_EG))));
+            for (int j = 0; j < Cfg::NTT; ++j) acc[i][j] *= 1.f / (1 << (2 * NS_EX - NS_EG));
+        if (!TWO) ns_put_tile_diag<Cfg>(out, at, acc);
+        ns_put_tile<Cfg, TWO>(out, at, acc, at.bm0 != at.bn0);
     }
 };
 
 // Four neighbours of planes for the blocks of rows i0 .. i0 + R of a wave's
-// part, all loaded before the first is used (what lies outside from element 0).
-template <class Cfg, int R>
+// part, all loaded before the first is used (what lies outside from the tile's first).
+template <class Cfg, bool TWO, int R>
 __device__ __forceinline__ void ns_get_rows(const NsPlanes& p, const TileAt& at, int i0, f32x4 (&v)[R][Cfg::NTT])
 {
     const uint32_t l = threadIdx.x % 64;
     s16x4 h[R][Cfg::NTT], q[R][Cfg::NTT];
+    const uint64_t tile = at.batch * p.batch + at.bm0 * p.ld + at.bn0;
 #pragma unroll
     for (int i = 0; i < R; ++i)
 #pragma unroll
         for (int j = 0; j < Cfg::NTT; ++j) {
             const uint32_t m = at.m0 + (i0 + i) * 16 + l % 16, n = at.n0 + j * 16 + l / 16 * 4;
-            const uint64_t o = at.batch * p.batch + (m < at.M && n < at.N ? m * p.ld + n : 0);
-            h[i][j] = *reinterpret_cast<const s16x4*>(p.hi + o);
-            if (p.lo) q[i][j] = *reinterpret_cast<const s16x4*>(p.lo + o);
+            // 256 rows of GEMM_MAX_LD: 32 bits
+            const uint32_t o = m < at.M && n < at.N ? (m - at.bm0) * (uint32_t)p.ld + (n - at.bn0) : 0;
+            h[i][j] = *reinterpret_cast<const s16x4*>(p.hi + tile + o);
+            if (TWO) q[i][j] = *reinterpret_cast<const s16x4*>(p.lo + tile + o);
         }
 #pragma unroll
     for (int i = 0; i < R; ++i)
@@ -245,18 +297,19 @@ __device__ __forceinline__ void ns_get_rows(const NsPlanes& p, const TileAt& at,
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
                 v[i][j][k] = f16_value((uint16_t)h[i][j][k]);
-                if (p.lo) v[i][j][k] += f16_value((uint16_t)q[i][j][k]);
+                if (TWO) v[i][j][k] += f16_value((uint16_t)q[i][j][k]);
             }
 }
 
 // b G + c G^2 from the sums of G^2
+template <bool TWO>
 struct NsPolyEpi {
     NsPlanes gram, out;
     const NsScale* scale; // one per matrix
     uint32_t step;
     NsCoef coef;
     template <class Cfg>
-    __device__ __forceinline__ void run(const f32x4 (&acc)[Cfg::MT][Cfg::NTT], const TileAt& at) const
+    __device__ __forceinline__ void run(f32x4 (&acc)[Cfg::MT][Cfg::NTT], const TileAt& at) const
     {
         const uint32_t l = threadIdx.x % 64;
         const NsScale sc = scale[at.batch];
@@ -266,39 +319,116 @@ struct NsPolyEpi {
         // G = q + diag(d): G^2 = q^2 + d_m q + q d_n (+ d^2, below fp32's last bit)
         float dm[Cfg::MT];
         f32x4 dn[Cfg::NTT];
-        const float* const d = gram.diag ? gram.diag + at.batch * gram.ld : nullptr;
+        const float* const d = TWO ? nullptr : gram.diag + at.batch * gram.ld;
 #pragma unroll
         for (int i = 0; i < Cfg::MT; ++i) {
             const uint32_t m = at.m0 + i * 16 + l % 16;
-            dm[i] = d ? d[m < at.M ? m : 0] : 0.f;
+            dm[i] = TWO ? 0.f : d[m < at.M ? m : 0];
         }
 #pragma unroll
         for (int j = 0; j < Cfg::NTT; ++j) {
             const uint32_t n = at.n0 + j * 16 + l / 16 * 4;
-            dn[j] = d ? *reinterpret_cast<const f32x4*>(d + (n < at.N ? n : 0)) : f32x4{0.f, 0.f, 0.f, 0.f};
+            dn[j] = f32x4{0.f, 0.f, 0.f, 0.f};
+            if (!TWO) dn[j] = *reinterpret_cast<const f32x4*>(d + (n < at.N ? n : 0));
         }
-        constexpr int R = Cfg::MT % 4 == 0 ? 4 : Cfg::MT;
+        constexpr int R = Cfg::MT * Cfg::NTT > 16 ? (TWO ? 1 : 2) : Cfg::MT; // what fits beside the sums
 #pragma unroll
         for (int i0 = 0; i0 < Cfg::MT; i0 += R) {
             f32x4 q[R][Cfg::NTT];
-            ns_get_rows<Cfg>(gram, at, i0, q);
+            ns_get_rows<Cfg, TWO>(gram, at, i0, q);
 #pragma unroll
             for (int i = 0; i < R; ++i)
 #pragma unroll
                 for (int j = 0; j < Cfg::NTT; ++j) {
-                    f32x4 v = acc[i0 + i][j] + (dm[i0 + i] + dn[j]) * q[i][j];
+                    const f32x4 v = acc[i0 + i][j] + (dm[i0 + i] + dn[j]) * q[i][j];
                     const uint32_t m = at.m0 + (i0 + i) * 16 + l % 16, n = at.n0 + j * 16 + l / 16 * 4;
+                    if (!TWO) {
 #pragma unroll
-                    for (int x = 0; x < 4; ++x) q[i][j][x] += m == n + x ? dm[i0 + i] : 0.f;
-                    v = kc * v + kb * q[i][j];
-                    ns_put_symmetric<Cfg>(out, at, i0 + i, j, v);
+                        for (int x = 0; x < 4; ++x) q[i][j][x] += m == n + x ? dm[i0 + i] : 0.f;
+                    }
+                    acc[i0 + i][j] = kc * v + kb * q[i][j];
                 }
+            __builtin_amdgcn_sched_barrier(0); // the next rows' loads stay behind: all at once they spill
         }
+        if (!TWO) ns_put_tile_diag<Cfg>(out, at, acc);
+        ns_put_tile<Cfg, TWO>(out, at, acc, at.bm0 != at.bn0);
     }
 };
 
+// Sums over a part of k of a symmetric product, as they are
+struct NsPartEpi {
+    float* part; // [splits][B][sp][sp]
+    uint32_t sp, B;
+    template <class Cfg>
+    __device__ __forceinline__ void run(const f32x4 (&acc)[Cfg::MT][Cfg::NTT], const TileAt& at) const
+    {
+        const uint32_t l = threadIdx.x % 64;
+        float* const p = part + ((uint64_t)at.split * B + at.batch) * sp * sp;
+#pragma unroll
+        for (int i = 0; i < Cfg::MT; ++i)
+#pragma unroll
+            for (int j = 0; j < Cfg::NTT; ++j) {
+                const uint32_t m = at.m0 + i * 16 + l % 16, n = at.n0 + j * 16 + l / 16 * 4;
+                if (m < at.M && n < at.N) *reinterpret_cast<f32x4*>(p + (uint64_t)m * sp + n) = acc[i][j];
+            }
+    }
+};
+
+// The parts added in their order: G (gram.hi NULL) or b G + c G^2, both halves.
+// A block takes 64 x 64 on or above the diagonal.
+__global__ __launch_bounds__(1024) void ns_join_kernel(const float* part, uint32_t splits, uint32_t sp, uint32_t B,
+                                                       NsPlanes gram, NsPlanes out, const NsScale* scale,
+                                                       uint32_t step, NsCoef coef)
+{
+    __shared__ float tile[64][65];
+    const uint32_t side = sp / 64;
+    uint32_t bm = 0, in = blockIdx.x;
+    while (in >= side - bm) in -= side - bm++;
+    const uint32_t bn = bm + in, r = threadIdx.x / 16, c = threadIdx.x % 16 * 4, b = blockIdx.y;
+    const uint32_t m = bm * 64 + r, n = bn * 64 + c;
+    const uint64_t mat = (uint64_t)sp * sp, at = (uint64_t)m * sp + n;
+    f32x4 v = {0.f, 0.f, 0.f, 0.f}, q = v, d = v;
+    float dm = 0.f, kb = 0.f, kc = 0.f;
+    if (gram.hi) { // loaded beside the parts
+        const NsScale sc = scale[b];
+        const NsCoef k = step == 0 ? sc.first : coef;
+        const int q0 = ns_q(sc, step);
+        kb = ldexpf(k.b, NS_EB - NS_EG - 2 * q0);
+        kc = ldexpf(k.c, NS_EB - 2 * NS_EG - 4 * q0);
+        q = ns_get(gram, b * mat + at);
+        if (gram.diag) {
+            dm = gram.diag[(uint64_t)b * sp + m];
+            d = *reinterpret_cast<const f32x4*>(gram.diag + (uint64_t)b * sp + n);
+        }
+    }
+#pragma unroll 8
+    for (uint32_t s = 0; s < splits; ++s)
+        v += *reinterpret_cast<const f32x4*>(part + ((uint64_t)s * B + b) * mat + at);
+    if (gram.hi) {
+        v += (dm + d) * q;
+#pragma unroll
+        for (int x = 0; x < 4; ++x) q[x] += m == n + x ? dm : 0.f;
+        v = kc * v + kb * q;
+    } else {
+        v *= 1.f / (1 << (2 * NS_EX - NS_EG));
+    }
+    ns_put(out, b * mat + at, v);
+    if (bm == bn) { // the whole block: its other half is in it
+        if (out.diag) ns_put_diag(out, b, m, n, v);
+        return;
+    }
+#pragma unroll
+    for (int x = 0; x < 4; ++x) tile[r][c + x] = v[x];
+    __syncthreads();
+    f32x4 w;
+#pragma unroll
+    for (int x = 0; x < 4; ++x) w[x] = tile[c + x][r];
+    ns_put(out, b * mat + (uint64_t)(bn * 64 + r) * sp + bm * 64 + c, w);
+}
+
 // a X + (the polynomial) X, as the next planes or, after the last step, as
 // the result in the caller's type
+template <bool TWO>
 struct NsStepEpi {
     NsPlanes x, out;
     const float* diag; // the polynomial's, [B][sp], or NULL
@@ -312,7 +442,7 @@ struct NsStepEpi {
     uint32_t step;
     NsCoef coef;
     template <class Cfg>
-    __device__ __forceinline__ void run(const f32x4 (&acc)[Cfg::MT][Cfg::NTT], const TileAt& at) const
+    __device__ __forceinline__ void run(f32x4 (&acc)[Cfg::MT][Cfg::NTT], const TileAt& at) const
     {
         const NsScale sc = scale[at.batch];
         const int q0 = ns_q(sc, step), q1 = ns_q(sc, step + 1);
@@ -320,37 +450,60 @@ struct NsStepEpi {
         const float up = ldexpf(1.f, last ? -NS_EX - q0 : q1 - q0);
         const float a = step == 0 ? sc.first.a : coef.a;
         const uint32_t l = threadIdx.x % 64;
-        const float* const d = diag ? diag + at.batch * (uint64_t)sp : nullptr;
+        const float* const d = TWO ? nullptr : diag + at.batch * (uint64_t)sp;
         // a and the polynomial's diagonal, by rows, or by columns for a tall matrix
         float dm[Cfg::MT];
         f32x4 dn[Cfg::NTT];
 #pragma unroll
         for (int i = 0; i < Cfg::MT; ++i) {
             const uint32_t r = at.m0 + i * 16 + l % 16;
-            dm[i] = a + (d && !tall ? d[r < at.M ? r : 0] * (1.f / (1 << NS_EB)) : 0.f);
+            dm[i] = a + (!TWO && !tall ? d[r < at.M ? r : 0] * (1.f / (1 << NS_EB)) : 0.f);
         }
 #pragma unroll
         for (int j = 0; j < Cfg::NTT; ++j) {
             const uint32_t c = at.n0 + j * 16 + l / 16 * 4;
             dn[j] = f32x4{0.f, 0.f, 0.f, 0.f};
-            if (d && tall) dn[j] = *reinterpret_cast<const f32x4*>(d + (c < at.N ? c : 0)) * (1.f / (1 << NS_EB));
+            if (!TWO && tall) dn[j] = *reinterpret_cast<const f32x4*>(d + (c < at.N ? c : 0)) * (1.f / (1 << NS_EB));
         }
-        constexpr int R = Cfg::MT % 4 == 0 ? 4 : Cfg::MT;
+        constexpr int R = Cfg::MT * Cfg::NTT > 16 ? (TWO ? 1 : 2) : Cfg::MT; // what fits beside the sums
 #pragma unroll
         for (int i0 = 0; i0 < Cfg::MT; i0 += R) {
             f32x4 have[R][Cfg::NTT];
-            ns_get_rows<Cfg>(x, at, i0, have);
+            ns_get_rows<Cfg, TWO>(x, at, i0, have);
 #pragma unroll
             for (int i = 0; i < R; ++i)
 #pragma unroll
                 for (int j = 0; j < Cfg::NTT; ++j) {
-                    const uint32_t r = at.m0 + (i0 + i) * 16 + l % 16, c = at.n0 + j * 16 + l / 16 * 4;
-                    const f32x4 v = ((dm[i0 + i] + dn[j]) * have[i][j] + acc[i0 + i][j] * (1.f / (1 << NS_EB))) * up;
-                    if (last) {
-                        if (r < m && c < n) put_result(r, c, v, at.batch);
-                    } else if (r < at.M && c < at.N) {
-                        ns_put(out, at.batch * out.batch + r * out.ld + c, v);
-                    }
+                    acc[i0 + i][j] = ((dm[i0 + i] + dn[j]) * have[i][j] + acc[i0 + i][j] * (1.f / (1 << NS_EB))) * up;
+                }
+            __builtin_amdgcn_sched_barrier(0); // as in NsPolyEpi
+        }
+        if (!last) {
+            ns_put_tile<Cfg, TWO>(out, at, acc, false);
+        } else if (bf16 && wide) {
+            typedef TileRows<Cfg> Rows;
+#pragma unroll
+            for (int i = 0; i < Cfg::MT; ++i)
+#pragma unroll
+                for (int j = 0; j < Cfg::NTT; ++j) {
+                    s16x4 w;
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) w[x] = __builtin_bit_cast(short, (__bf16)acc[i][j][x]);
+                    Rows::put(at.lds, at.m0 - at.bm0 + i * 16 + l % 16, at.n0 - at.bn0 + j * 16 + l / 16 * 4, w);
+                }
+            __syncthreads();
+            Rows::each(at.lds, [&](uint32_t r, uint32_t c, s16x8 w) {
+                r += at.bm0;
+                c += at.bn0;
+                if (r < m && c < n) store_tail(static_cast<uint16_t*>(last) + at.batch * stride + r * ld + c, w, n - c);
+            });
+        } else {
+#pragma unroll
+            for (int i = 0; i < Cfg::MT; ++i)
+#pragma unroll
+                for (int j = 0; j < Cfg::NTT; ++j) {
+                    const uint32_t r = at.m0 + i * 16 + l % 16, c = at.n0 + j * 16 + l / 16 * 4;
+                    if (r < m && c < n) put_result(r, c, acc[i][j], at.batch);
                 }
         }
     }
@@ -362,11 +515,9 @@ struct NsStepEpi {
             s16x4 w;
 #pragma unroll
             for (int i = 0; i < 4; ++i) w[i] = __builtin_bit_cast(short, (__bf16)v[i]);
-            if (wide && c + 4 <= n) *reinterpret_cast<s16x4*>(q) = w;
-            else
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    if (c + i < n) q[i] = (uint16_t)w[i];
+            for (int i = 0; i < 4; ++i)
+                if (c + i < n) q[i] = (uint16_t)w[i];
         } else {
             float* q = static_cast<float*>(last) + o;
             if (wide && c + 4 <= n) *reinterpret_cast<f32x4*>(q) = v;
@@ -378,12 +529,43 @@ struct NsStepEpi {
     }
 };
 
+// The tile and the parts of k that take least (tile_time).  A symmetric
+// product may be split: its parts' sums are written and read once more, at
+// 4.5 TB/s, by a kernel of 6 us.
+struct NsPlan {
+    TileKind tile;
+    uint32_t splits;
+};
+static NsPlan ns_plan(uint32_t M, uint32_t N, uint32_t K, uint32_t nseg, uint32_t B, bool symmetric)
+{
+    NsPlan best = {TILE_L, 1};
+    double least = 1e300;
+    const uint64_t ks = ceil_div(K, GEMM_BK);
+    for (TileKind t : {TILE_L, TILE_M, TILE_S, TILE_K}) {
+        const uint64_t side = tile_side(t), tm = ceil_div(M, side), tn = ceil_div(N, side);
+        const uint64_t tiles = (symmetric ? tm * (tm + 1) / 2 : tm * tn) * B;
+        for (uint32_t s = 1; s <= (symmetric && t != TILE_K ? 16u : 1u) && s <= ks; ++s) {
+            const uint64_t per = ceil_div(ks, s);
+            if (ceil_div(ks, per) != s) continue; // a part without a step
+            double us = tile_time(t, tiles * s, per * nseg);
+            if (s > 1) us += 6.0 + 8.0 * s * tiles * side * side / 4.5e6;
+            if (us < least) {
+                least = us;
+                best = {t, s};
+            }
+        }
+    }
+    return best;
+}
+
 struct NsWs {
     double* part;
     NsScale* scale;
     uint16_t *x[2][2], *gram[2], *poly[2]; // [which][plane]
     float *dgram, *dpoly;                  // diagonals, one plane only
     uint32_t sp, mp, np;                   // shorter side, rows and columns, padded to 64
+    NsPlan pg, pp, ps;                     // how each product is taken
+    float* parts;                          // sums of the split ones
 };
 static NsWs ns_carve(Carver& cv, uint32_t B, uint32_t m, uint32_t n, bool two)
 {
@@ -391,6 +573,12 @@ static NsWs ns_carve(Carver& cv, uint32_t B, uint32_t m, uint32_t n, bool two)
     w.mp = (uint32_t)align_up(m, 64);
     w.np = (uint32_t)align_up(n, 64);
     w.sp = w.mp < w.np ? w.mp : w.np;
+    const uint32_t nseg = two ? 3 : 1;
+    w.pg = ns_plan(w.sp, w.sp, w.mp < w.np ? w.np : w.mp, nseg, B, true);
+    w.pp = ns_plan(w.sp, w.sp, w.sp, nseg, B, true);
+    w.ps = ns_plan(w.mp, w.np, w.sp, nseg, B, false);
+    const uint32_t most = w.pg.splits > w.pp.splits ? w.pg.splits : w.pp.splits;
+    w.parts = most > 1 ? cv.take<float>((uint64_t)most * B * w.sp * w.sp) : nullptr;
     w.part = cv.take<double>((uint64_t)B * NS_NORM_BLOCKS);
     w.scale = cv.take<NsScale>(B);
     w.dgram = two ? nullptr : cv.take<float>((uint64_t)B * w.sp);
@@ -406,17 +594,17 @@ static NsWs ns_carve(Carver& cv, uint32_t B, uint32_t m, uint32_t n, bool two)
 }
 
 template <int AL, int BL, class Epi>
-static int ns_product(const Gemm& g, uint32_t B, const Epi& e, hipStream_t st)
+static int ns_product(TileKind t, const Gemm& g, uint32_t B, const Epi& e, hipStream_t st)
 {
-    const uint64_t large = ceil_div(g.M, 256) * ceil_div(g.N, 256) * B, mid = ceil_div(g.M, 128) * ceil_div(g.N, 128) * B;
-    if (large >= 256) return launch_gemm<TileL, AL, BL, true>(g, B, e, st);
-    if (mid >= 256) return launch_gemm<TileM, AL, BL, true>(g, B, e, st);
-    return launch_gemm<TileS, AL, BL, true>(g, B, e, st);
+    if (t == TILE_L) return launch_gemm<TileL, AL, BL, true>(g, B, e, st);
+    if (t == TILE_M) return launch_gemm<TileM, AL, BL, true>(g, B, e, st);
+    if (t == TILE_S) return launch_gemm<TileS, AL, BL, true>(g, B, e, st);
+    return launch_gemm<TileK, AL, BL, true>(g, B, e, st);
 }
 
 static Mat ns_mat(uint16_t* const p[2], uint32_t rows, uint32_t ld)
 {
-    return {{p[0], p[1]}, ld, (uint64_t)rows * ld, (uint64_t)rows * ld};
+    return {{p[0], p[1]}, ld, (uint64_t)rows * ld, (uint64_t)rows * ld, 0};
 }
 
 // Whether the iterates' singular values stay where the scales were made for.
@@ -493,22 +681,42 @@ extern "C" int sg_orthogonalize(const void* d_update, sg_dtype dt, uint32_t B, u
                    poly = {w.poly[0], w.poly[1], w.sp, gb, w.dpoly};
     const Mat mg = ns_mat(w.gram, w.sp, w.sp), mb = ns_mat(w.poly, w.sp, w.sp);
     const NsCoef coef = {(float)a, (float)b, (float)c};
-    for (uint32_t s = 0; s < steps; ++s) {
-        uint16_t *const *x = w.x[s & 1], *const *y = w.x[~s & 1];
-        const Mat mx = ns_mat(x, w.mp, w.np);
-        const NsPlanes px = {x[0], x[1], w.np, xb, nullptr}, py = {y[0], y[1], w.np, xb, nullptr};
-        int rc;
-        const Gemm gg = {mx, mx, w.sp, w.sp, tall ? w.mp : w.np, nseg, 1, 1, nullptr, nullptr};
-        rc = tall ? ns_product<KS, KS>(gg, B, NsGramEpi{gram}, st) : ns_product<KC, KC>(gg, B, NsGramEpi{gram}, st);
-        if (rc) return rc;
-        const Gemm gp = {mg, mg, w.sp, w.sp, w.sp, nseg, 1, 1, nullptr, nullptr};
-        if ((rc = ns_product<KC, KC>(gp, B, NsPolyEpi{gram, poly, w.scale, s, coef}, st))) return rc;
-        const bool end = s + 1 == steps;
-        const bool owide = reinterpret_cast<uintptr_t>(d_out) % 16 == 0 && ld_out % 4 == 0 && (B == 1 || stride_out % 4 == 0);
-        const NsStepEpi e = {px, py, w.dpoly, w.sp, tall, end ? d_out : nullptr, ld_out, stride_out, m, n, dt == SG_BF16, owide, w.scale, s, coef};
-        const Gemm gx = {tall ? mx : mb, tall ? mb : mx, w.mp, w.np, w.sp, nseg, 1, 0, nullptr, nullptr};
-        rc = tall ? ns_product<KC, KC>(gx, B, e, st) : ns_product<KC, KS>(gx, B, e, st);
-        if (rc) return rc;
-    }
-    return SG_OK;
+    const auto run = [&](auto planes) -> int {
+        constexpr bool TWO = decltype(planes)::value;
+        for (uint32_t s = 0; s < steps; ++s) {
+            uint16_t *const *x = w.x[s & 1], *const *y = w.x[~s & 1];
+            const Mat mx = ns_mat(x, w.mp, w.np);
+            const NsPlanes px = {x[0], x[1], w.np, xb, nullptr}, py = {y[0], y[1], w.np, xb, nullptr};
+            int rc;
+            const Gemm gg = {mx, mx, w.sp, w.sp, tall ? w.mp : w.np, nseg, w.pg.splits, 1, nullptr, nullptr};
+            const Gemm gp = {mg, mg, w.sp, w.sp, w.sp, nseg, w.pp.splits, 1, nullptr, nullptr};
+            const dim3 jgrid(w.sp / 64 * (w.sp / 64 + 1) / 2, B);
+            const NsPartEpi parts = {w.parts, w.sp, B};
+            if (w.pg.splits > 1) {
+                rc = tall ? ns_product<KS, KS>(w.pg.tile, gg, B, parts, st) : ns_product<KC, KC>(w.pg.tile, gg, B, parts, st);
+                if (rc) return rc;
+                ns_join_kernel<<<jgrid, 1024, 0, st>>>(w.parts, w.pg.splits, w.sp, B, NsPlanes{}, gram, w.scale, s, coef);
+                SG_TRY_LAUNCH();
+            } else {
+                const NsGramEpi<TWO> e = {gram};
+                rc = tall ? ns_product<KS, KS>(w.pg.tile, gg, B, e, st) : ns_product<KC, KC>(w.pg.tile, gg, B, e, st);
+                if (rc) return rc;
+            }
+            if (w.pp.splits > 1) {
+                if ((rc = ns_product<KC, KC>(w.pp.tile, gp, B, parts, st))) return rc;
+                ns_join_kernel<<<jgrid, 1024, 0, st>>>(w.parts, w.pp.splits, w.sp, B, gram, poly, w.scale, s, coef);
+                SG_TRY_LAUNCH();
+            } else if ((rc = ns_product<KC, KC>(w.pp.tile, gp, B, NsPolyEpi<TWO>{gram, poly, w.scale, s, coef}, st))) {
+                return rc;
+            }
+            const bool end = s + 1 == steps;
+            const bool owide = reinterpret_cast<uintptr_t>(d_out) % 16 == 0 && ld_out * es % 16 == 0 && (B == 1 || stride_out * es % 16 == 0);
+            const NsStepEpi<TWO> e = {px, py, w.dpoly, w.sp, tall, end ? d_out : nullptr, ld_out, stride_out, m, n, !TWO, owide, w.scale, s, coef};
+            const Gemm gx = {tall ? mx : mb, tall ? mb : mx, w.mp, w.np, w.sp, nseg, 1, 0, nullptr, nullptr};
+            rc = tall ? ns_product<KC, KC>(w.ps.tile, gx, B, e, st) : ns_product<KC, KS>(w.ps.tile, gx, B, e, st);
+            if (rc) return rc;
+        }
+        return SG_OK;
+    };
+    return two ? run(std::true_type()) : run(std::false_type());
 }

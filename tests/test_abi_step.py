@@ -39,7 +39,7 @@ def linear_ce(L):
 def balance(L):
     return make(L, "sg_balance_loss", ("x", "dt", "T", "E", "ld", "idx", "k", "live", "alpha", "zc", "loss", "counts", "prob", "grad",
                                        "ldg", "ws", "nws", "stream"),
-                dict(x=F, dt=0, T=8, E=16, ld=16, idx=F, k=2, live=N, alpha=0.1, zc=0.1, loss=F, counts=F, prob=F, grad=G, ldg=16,
+                dict(x=F, dt=0, T=8000, E=16, ld=16, idx=F, k=2, live=N, alpha=0.1, zc=0.1, loss=F, counts=F, prob=F, grad=G, ldg=16,
                      ws=F, nws=BIG, stream=N))
 
 
@@ -115,7 +115,8 @@ def test_workspace_sizes(L):
     assert 0 < one < two <= 2 * one + 4096
     assert L.sg_orthogonalize_workspace_bytes(1, 200, 100, 0) == two
     assert L.sg_orthogonalize_workspace_bytes(0, 1, 1, 0) == 0 and L.sg_orthogonalize_workspace_bytes(1, 1 << 21, 1, 0) == 0
-    assert L.sg_balance_workspace_bytes(10, 64, 2, 0) > 0 and L.sg_balance_workspace_bytes(10, 1025, 2, 0) == 0
+    assert L.sg_balance_workspace_bytes(10000, 64, 2, 0) > 0 and L.sg_balance_workspace_bytes(10000, 1025, 2, 0) == 0
+    assert L.sg_balance_workspace_bytes(10, 64, 2, 0) == 0  # one block needs none
 
 
 def test_binding_refuses_host_tensors():

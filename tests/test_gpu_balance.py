@@ -130,7 +130,7 @@ def test_same_bits_streams_and_graph():
         x, idx, live = make(T, E, 4, "f32")
         want = sg.sg_balance_loss(x, idx, live=live, z_coef=1e-3)
         need = sg.lib().sg_balance_workspace_bytes(T, E, 4, 0)
-        ws = torch.full((need,), 255, dtype=torch.uint8, device="cuda")
+        ws = torch.full((max(need, 1),), 255, dtype=torch.uint8, device="cuda")
         s = torch.cuda.Stream()
         s.wait_stream(torch.cuda.current_stream())
         with torch.cuda.stream(s):
