@@ -802,8 +802,8 @@ def sg_balance_loss(logits: torch.Tensor, idx: torch.Tensor, live: torch.Tensor 
                     balance_coef: float = 0.01, z_coef: float = 0.0, want_grad: bool = True,
                     grad: torch.Tensor | None = None, workspace: torch.Tensor | None = None):
     """Balance loss of a router: logits [T, E], idx [T, k] int32 (the chosen
-    experts; outside [0, E): not counted), live [T] bool or None -> (loss [1]
-    float32; counts [E] int32; prob [E] float32, the mean probabilities; grad
+    experts; outside [0, E): not counted), live [T] bool or None -> (loss
+    float32, no dimensions; counts [E] int32; prob [E] float32, the mean probabilities; grad
     [T, E] of the loss, or None).  grad: where to write the gradient, logits
     itself included."""
     _need_cuda(logits)
@@ -814,7 +814,7 @@ def sg_balance_loss(logits: torch.Tensor, idx: torch.Tensor, live: torch.Tensor 
     k = idx.shape[-1]
     idx, p_idx = _beside(logits, "idx", idx, torch.int32, (T, k))
     live, p_live = _beside(logits, "live", live, torch.bool, (T,))
-    loss = torch.empty(1, dtype=torch.float32, device=dev)
+    loss = torch.empty((), dtype=torch.float32, device=dev)
     counts = torch.empty(E, dtype=torch.int32, device=dev)
     prob = torch.empty(E, dtype=torch.float32, device=dev)
     ws, p_ws, n_ws = _scratch(L.sg_balance_workspace_bytes(T, E, k, dt), workspace, dev)

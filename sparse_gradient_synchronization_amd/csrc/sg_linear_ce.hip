@@ -460,8 +460,10 @@ __global__ __launch_bounds__(256) void ce_join_kernel(CeArgs p, const uint32_t* 
     const double b = w * p.it / scal->top;
     const CeRow r = {shift, (float)log2(s), (float)(b * (1.0 + 2.0 * p.zc * lse)), (float)b};
     info[j] = r;
-    // a maximum of whole numbers: the order of the rows does not matter
-    if (planes) atomicMax(&scal->max_g, __float_as_uint(fmaxf(fabsf(r.a), fabsf(r.b))));
+    // A maximum of whole numbers: the order of the rows does not matter.  Looked at first: with equal weights
+    // most rows have nothing to add, and as many atomics on one word took 12 ns each (4088 rows: 50 us).
+    const uint32_t big = __float_as_uint(fmaxf(fabsf(r.a), fabsf(r.b)));
+    if (planes && big > *(volatile uint32_t*)&scal->max_g) atomicMax(&scal->max_g, big);
 }
 
 // kept exponentials -> g, in place; rows up to the next multiple of 64 are
@@ -522,8 +524,9 @@ __global__ __launch_bounds__(256) void ce_zero_kernel(const CeScal* scal, CeG g,
     }
 }
 
-// sums of dx, one set per part of the vocabulary; later pieces add to them
-struct CeHiddenEpi {
+// sums of dx, one set per part of the vocabulary (later pieces add to them), or
+// of dw, one set per part of the rows
+struct CePartEpi {
     float* part; // [splits][rows][ld]
     uint64_t ld, rows;
     bool add;
@@ -543,23 +546,24 @@ struct CeHiddenEpi {
     }
 };
 
-// dx of every row from its sums: 1024 columns to a block
+// The rows of dx (pos: their places, or -1) or dw (pos NULL) from the sums: 1024
+// columns to a block.  other: what the planes of g were multiplied with.
 template <typename E>
-__global__ __launch_bounds__(256) void ce_hidden_kernel(const int32_t* pos, const CeScal* scal, const float* part,
-                                                        uint64_t ldp, uint64_t rows, uint32_t splits, bool planes,
-                                                        E* out, uint64_t ld, uint32_t H)
+__global__ __launch_bounds__(256) void ce_sum_kernel(const int32_t* pos, const CeScal* scal, const uint32_t* other,
+                                                     const float* part, uint64_t ldp, uint64_t rows, uint32_t splits,
+                                                     bool planes, E* out, uint64_t ld, uint32_t H)
 {
     const uint32_t cols = (H + 1023) / 1024;
     const uint64_t t = blockIdx.x / cols;
     const uint32_t h = blockIdx.x % cols * 1024 + threadIdx.x * 4;
     if (h >= H) return;
-    const int32_t j = pos[t];
+    const int64_t j = pos ? pos[t] : (int64_t)t;
     f32x4 s = {0.f, 0.f, 0.f, 0.f};
     if (j >= 0) {
-        const float* q = part + (uint32_t)j * ldp + h;
+        const float* q = part + (uint64_t)j * ldp + h;
 #pragma unroll 8
         for (uint32_t k = 0; k < splits; ++k) s += *reinterpret_cast<const f32x4*>(q + k * rows * ldp);
-        const int unit = planes ? -ce_exponent(scal->max_g) - ce_exponent(scal->max_w) : 0;
+        const int unit = planes ? -ce_exponent(scal->max_g) - ce_exponent(*other) : 0;
         const float top = (float)scal->top;
 #pragma unroll
         for (int i = 0; i < 4; ++i) s[i] = ldexpf(s[i], unit) * top;
@@ -630,6 +634,114 @@ struct CeHeadEpi {
     }
 };
 
+// dw of up to 64 rows: a write of the whole head and little else.  A block takes
+// 64 tokens; their g stays in registers (a wave 16 tokens, all 64 k) while the
+// hidden states come by, 64 columns at a time, the next ones' fetch under way (two
+// fetches and fewer blocks to a compute unit: 29 us for 27).
+// The products' B fragments take the columns 32 p + 8 q + 4 (j % 2) .., q = 0 .. 3,
+// so that a lane's results of two fragments are eight neighbours.
+// US: 24 x 32000 x 2048 bf16, tiles of 128 42 us
+template <bool PLANES>
+__global__ __launch_bounds__(256, PLANES ? 3 : 4) void ce_head_few_kernel(Mat g, Mat x, const CeScal* scal, void* out,
+                                                                          uint64_t ld, uint32_t V, uint32_t H,
+                                                                          uint32_t cols, bool wide)
+{
+    constexpr int P = PLANES ? 2 : 1, TILE = 64 * GEMM_BK * 2;
+    __shared__ __align__(1024) char lds[3 * P * TILE];
+    // this block's columns
+    const uint32_t first = blockIdx.y * cols, end = first + cols < H ? first + cols : H;
+    typedef TileLoader<KS, 64, 256> Loader;
+    const uint32_t l = threadIdx.x % 64, w = threadIdx.x / 64, v0 = blockIdx.x * 64;
+    const bool any = scal->live > 0; // otherwise g was not written
+    const int unit = PLANES ? -ce_exponent(scal->max_g) - ce_exponent(scal->max_x) : 0;
+    const float top = (float)scal->top;
+    const auto fetch = [&](const Mat& m, uint32_t first, bool on, char* to) {
+        const Loader ld_(m, first, 0, GEMM_BK);
+#pragma unroll
+        for (int p = 0; p < P; ++p) {
+            const typename Loader::Step s = ld_.step(0, p, on, to + p * TILE);
+#pragma unroll
+            for (int i = 0; i < Loader::U; ++i) s.issue(i);
+        }
+    };
+    char* const xs = lds + P * TILE;
+    fetch(g, v0, any, lds);
+    fetch(x, first, any, xs);
+    // the lane's place in a fragment of columns; the pair's swizzle as in FragReader
+    const uint32_t sw = ((l >> 2 & 3) | (l >> 4 & 1) << 2) & 3, kr = (l / 16 * 8 + l % 16 / 4) * 128;
+    const auto column = [&](int j) { // of fragment j
+        const uint32_t c = j / 2 * 32 + l % 4 * 8 + j % 2 * 4;
+        return kr + ((c / 16) ^ sw) * 32 + c % 16 * 2;
+    };
+    const FragReader<KS, 64, 1> fa(w * 16);
+    s16x8 a[P][2];
+    wait_loads<P * Loader::U>(); // g is here
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+#pragma unroll
+    for (int p = 0; p < P; ++p)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) a[p][h] = fa.read(lds + p * TILE, 0, h);
+    const uint32_t v = v0 + w * 16 + l % 16;
+    uint32_t stage = 0;
+    for (uint32_t n0 = first; n0 < end; n0 += 64, stage ^= 1) {
+        const char* const cur = xs + stage * P * TILE;
+        fetch(x, n0 + 64, any && n0 + 64 < end, xs + (stage ^ 1) * P * TILE);
+        wait_loads<P * Loader::U>(); // all but the next columns (and, as stores count too, the stores before them)
+        __builtin_amdgcn_s_barrier();
+        asm volatile("" ::: "memory");
+        f32x4 acc[4] = {};
+        const auto multiply = [&](int pa, int pb) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const char* const q = cur + pb * TILE + column(j) + h * 32 * 128;
+                    const s16x4 lo = read_transposed((LdsS16x4*)q), hi = read_transposed((LdsS16x4*)(q + 4 * 128));
+                    acc[j] = mfma16<PLANES>(__builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7), a[pa][h], acc[j]);
+                }
+        };
+        multiply(0, 0);
+        if constexpr (PLANES) {
+            multiply(0, 1);
+            multiply(1, 0);
+        }
+#pragma unroll
+        for (int p = 0; p < 2; ++p) {
+            const uint32_t n = n0 + p * 32 + l / 16 * 8;
+            float r[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) r[i] = ldexpf(acc[2 * p + i / 4][i % 4], unit) * top;
+            if (v < V && n < H) {
+                if (PLANES) {
+                    float* const q = static_cast<float*>(out) + v * ld + n;
+                    if (wide && n + 8 <= H) {
+                        *reinterpret_cast<f32x4*>(q) = f32x4{r[0], r[1], r[2], r[3]};
+                        *reinterpret_cast<f32x4*>(q + 4) = f32x4{r[4], r[5], r[6], r[7]};
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 8; ++i)
+                            if (n + i < H) q[i] = r[i];
+                    }
+                } else {
+                    const s16x8 b = __builtin_bit_cast(s16x8, RowIO<bf16_bits>::pack(r));
+                    store_tail(static_cast<uint16_t*>(out) + v * ld + n, b, wide ? H - n : 0);
+                    if (!wide) {
+#pragma unroll
+                        for (int i = 0; i < 8; ++i)
+                            if (n + i < H) (static_cast<uint16_t*>(out) + v * ld + n)[i] = (uint16_t)b[i];
+                    }
+                }
+            }
+        }
+        // this wave's reads are done before the place is fetched into again
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+        __builtin_amdgcn_s_barrier();
+        asm volatile("" ::: "memory");
+    }
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); // the last fetch's zeros
+}
+
 // zeros where there is no row at all
 template <typename E>
 __global__ __launch_bounds__(256) void ce_no_rows_kernel(E* out, uint64_t ld, uint64_t V, uint32_t H)
@@ -641,13 +753,13 @@ __global__ __launch_bounds__(256) void ce_no_rows_kernel(E* out, uint64_t ld, ui
 // sizes and buffers of a call
 struct CePlan {
     uint32_t H, Hp, Tp, piece; // Hp, Tp: rounded up to 64; piece: columns of g
-    uint32_t groups, splits;
+    uint32_t groups, splits, splits_w; // parts of the sums of dx and dw
     bool two, pack, kept, grads, hidden;
     int tile, tile_w, tile_x; // of the logits' product, dw and dx: 0 large, 1 middle, 2 few rows
     CeScal* scal;
     uint32_t* row;
     int32_t* pos;
-    float *zy, *part;
+    float *zy, *part, *part_w;
     float2* stat;
     CeRow* info;
     uint16_t *x[2], *w[2], *g[2];
@@ -675,7 +787,6 @@ static CePlan ce_plan(Carver& cv, uint64_t T, uint64_t V, uint32_t H, sg_dtype d
         return tile_time(TILE_L, tiles(m, n, 256), steps) <= tile_time(TILE_M, tiles(m, n, 128), steps) ? 0 : 1;
     };
     p.tile = T <= 32 ? 2 : pick(T, V, kh);
-    p.tile_w = pick(V, H, kt);
     p.groups = (uint32_t)ceil_div(V, ce_tile_cols(p.tile));
     const uint64_t Vp = align_up(V, 256), es = p.two ? 4 : 2;
     p.kept = Vp <= (1u << 20) && p.Tp * Vp * es <= keep;
@@ -686,23 +797,33 @@ static CePlan ce_plan(Carver& cv, uint64_t T, uint64_t V, uint32_t H, sg_dtype d
         c = c < 256 ? 256 : c > (1u << 20) ? (1u << 20) : c;
         p.piece = (uint32_t)(c < Vp ? c : Vp);
     }
-    // dx has few tiles and a long sum: the vocabulary in parts, whose sums are written and read once more
-    double least = 1e300;
-    const uint64_t kv = ceil_div(p.piece, 64);
-    for (int t = T <= 32 ? 2 : 0; t <= (T <= 32 ? 2 : 1); ++t) {
-        const uint64_t n = t == 2 ? ceil_div(H, 128) : tiles(T, H, t == 0 ? 256 : 128);
-        for (uint64_t s = 1; s <= 64 && s <= kv; ++s) {
-            const uint64_t per = ceil_div(kv, s);
-            if (ceil_div(kv, per) != s) continue; // a part without a step
-            const double us = tile_time(t == 0 ? TILE_L : t == 1 ? TILE_M : TILE_S, n * s, per * nseg) +
-                              8.0 * s * p.Tp * p.Hp / 4.5e6;
-            if (us < least) {
-                least = us;
-                p.tile_x = t;
-                p.splits = (uint32_t)s;
+    // dx has few tiles and a long sum, dw where the vocabulary is small: in parts, whose sums are written and read once more
+    const auto parts = [&](uint64_t m, uint64_t n, uint64_t steps, bool alone, int* tile, uint32_t* splits) {
+        double least = 1e300;
+        for (int t = 0; t < 2; ++t)
+            for (uint64_t s = 1; s <= 64 && s <= steps; ++s) {
+                const uint64_t per = ceil_div(steps, s);
+                if (ceil_div(steps, per) != s) continue; // a part without a step
+                double us = tile_time(t == 0 ? TILE_L : TILE_M, tiles(m, n, t == 0 ? 256 : 128) * s, per * nseg);
+                if (s > 1 || !alone) us += 5.0 + 8.0 * s * m * n / 4.5e6;
+                if (us < least) {
+                    least = us;
+                    *tile = t;
+                    *splits = (uint32_t)s;
+                }
             }
-        }
+    };
+    const uint64_t kv = ceil_div(p.piece, 64);
+    if (T <= 32) { // as many parts as there are compute units for 4 blocks each
+        p.tile_x = 2;
+        const uint64_t want = ceil_div(1024, ceil_div(H, 128)), per = ceil_div(kv, want < kv ? want : kv);
+        p.splits = (uint32_t)ceil_div(kv, per);
+    } else {
+        parts(T, H, kv, false, &p.tile_x, &p.splits);
     }
+    p.tile_w = 2;
+    p.splits_w = 1;
+    if (kt / nseg > 1) parts(p.piece, H, kt / nseg, true, &p.tile_w, &p.splits_w);
 
     p.scal = cv.take<CeScal>(1);
     p.row = cv.take<uint32_t>(p.Tp);
@@ -716,6 +837,7 @@ static CePlan ce_plan(Carver& cv, uint64_t T, uint64_t V, uint32_t H, sg_dtype d
         p.g[i] = p.grads ? cv.take<uint16_t>((uint64_t)p.Tp * p.piece) : nullptr;
     }
     p.part = hidden ? cv.take<float>((uint64_t)p.splits * p.Tp * p.Hp) : nullptr;
+    p.part_w = dhead && p.splits_w > 1 ? cv.take<float>((uint64_t)p.splits_w * p.piece * p.Hp) : nullptr;
     return p;
 }
 
@@ -850,13 +972,37 @@ extern "C" int sg_linear_ce_loss(const void* d_hidden, uint64_t ld_hidden, const
         }
         const Mat mg = {{p.g[0], p.g[1]}, 256, (uint64_t)p.Tp * p.piece, 0, (uint64_t)p.Tp * 256};
         if (d_grad_head) {
-            const CeHeadEpi e = {p.scal, static_cast<char*>(d_grad_head) + v0 * ld_grad_head * es, ld_grad_head, p.two, wide(d_grad_head, ld_grad_head, 16)};
-            const Gemm g3 = {mg, mx, (uint32_t)n, p.H, 0, nseg, 1, 0, nullptr, live};
-            rc = p.two ? ce_product<KS, KS, true>(p.tile_w, g3, e, st) : ce_product<KS, KS, false>(p.tile_w, g3, e, st);
-            if (rc) return rc;
+            char* const out = static_cast<char*>(d_grad_head) + v0 * ld_grad_head * es;
+            const Gemm g3 = {mg, mx, (uint32_t)n, p.H, (uint32_t)T, nseg, p.splits_w, 0, nullptr, live};
+            if (p.tile_w == 2) {
+                // columns to a block: enough blocks, and 256 columns to pay for g
+                const uint64_t want = ceil_div(1024, ceil_div(n, 64)), most = ceil_div(H, 256);
+                const uint32_t cols = (uint32_t)align_up(ceil_div(H, want < most ? want : most), 64);
+                const dim3 blocks((unsigned)ceil_div(n, 64), (unsigned)ceil_div(H, cols));
+                const bool w16 = wide(d_grad_head, ld_grad_head, 16);
+                if (p.two) ce_head_few_kernel<true><<<blocks, 256, 0, st>>>(mg, mx, p.scal, out, ld_grad_head, (uint32_t)n, p.H, cols, w16);
+                else ce_head_few_kernel<false><<<blocks, 256, 0, st>>>(mg, mx, p.scal, out, ld_grad_head, (uint32_t)n, p.H, cols, w16);
+                SG_TRY_LAUNCH();
+            } else if (p.splits_w > 1) {
+                const CePartEpi e = {p.part_w, p.Hp, p.piece, false};
+                rc = p.two ? ce_product<KS, KS, true>(p.tile_w, g3, e, st) : ce_product<KS, KS, false>(p.tile_w, g3, e, st);
+                if (rc) return rc;
+                const unsigned blocks = (unsigned)(n * ceil_div(H, 1024));
+                if (p.two)
+                    ce_sum_kernel<float><<<blocks, 256, 0, st>>>(nullptr, p.scal, &p.scal->max_x, p.part_w, p.Hp, p.piece,
+                                                                 p.splits_w, true, (float*)out, ld_grad_head, p.H);
+                else
+                    ce_sum_kernel<bf16_bits><<<blocks, 256, 0, st>>>(nullptr, p.scal, nullptr, p.part_w, p.Hp, p.piece,
+                                                                     p.splits_w, false, (bf16_bits*)out, ld_grad_head, p.H);
+                SG_TRY_LAUNCH();
+            } else {
+                const CeHeadEpi e = {p.scal, out, ld_grad_head, p.two, wide(d_grad_head, ld_grad_head, 16)};
+                rc = p.two ? ce_product<KS, KS, true>(p.tile_w, g3, e, st) : ce_product<KS, KS, false>(p.tile_w, g3, e, st);
+                if (rc) return rc;
+            }
         }
         if (d_grad_hidden) {
-            const CeHiddenEpi e = {p.part, p.Hp, p.Tp, v0 > 0};
+            const CePartEpi e = {p.part, p.Hp, p.Tp, v0 > 0};
             const Gemm g4 = {mg, head(v0, n), (uint32_t)T, p.H, (uint32_t)np, nseg, p.splits, 0, live, nullptr};
             rc = p.two ? ce_product<KC, KS, true>(p.tile_x, g4, e, st) : ce_product<KC, KS, false>(p.tile_x, g4, e, st);
             if (rc) return rc;
@@ -864,8 +1010,12 @@ extern "C" int sg_linear_ce_loss(const void* d_hidden, uint64_t ld_hidden, const
     }
     if (d_grad_hidden) {
         const unsigned hblocks = (unsigned)(T * ceil_div(H, 1024));
-        if (p.two) ce_hidden_kernel<float><<<hblocks, 256, 0, st>>>(p.pos, p.scal, p.part, p.Hp, p.Tp, p.splits, true, (float*)d_grad_hidden, ld_grad_hidden, p.H);
-        else ce_hidden_kernel<bf16_bits><<<hblocks, 256, 0, st>>>(p.pos, p.scal, p.part, p.Hp, p.Tp, p.splits, false, (bf16_bits*)d_grad_hidden, ld_grad_hidden, p.H);
+        if (p.two)
+            ce_sum_kernel<float><<<hblocks, 256, 0, st>>>(p.pos, p.scal, &p.scal->max_w, p.part, p.Hp, p.Tp, p.splits, true,
+                                                          (float*)d_grad_hidden, ld_grad_hidden, p.H);
+        else
+            ce_sum_kernel<bf16_bits><<<hblocks, 256, 0, st>>>(p.pos, p.scal, nullptr, p.part, p.Hp, p.Tp, p.splits, false,
+                                                              (bf16_bits*)d_grad_hidden, ld_grad_hidden, p.H);
         SG_TRY_LAUNCH();
     }
     return SG_OK;

@@ -23,7 +23,7 @@ def check(out, x, idx, live, alpha, zc):
     loss, counts, prob, grad = out
     assert torch.equal(counts.long(), val["counts"])
     ref.close(prob, val["prob"], err["prob"], "prob")
-    ref.close(loss[0], val["loss"], err["loss"], "loss")
+    ref.close(loss, val["loss"], err["loss"], "loss")
     if grad is not None:
         ref.close(grad, val["grad"], err["grad"], "grad")
     assert sg.sg_device_error() == 0
