@@ -3,7 +3,8 @@ every worker's loss over the vocabulary gives its dense gradient, and the
 sparse synchronization path of the library turns the n gradients into one
 update.
 
-  python examples/train_head.py [--steps 12] [--loss distill|policy|preference]
+  python examples/train_head.py [--steps 12] [--loss distill|policy|preference|cross_entropy]
+                                [--update sgd|orthogonal]
 
   loss      distill     sg_topk_rows on a teacher's logits, sg_distill_loss on
                         the workers'
@@ -11,10 +12,16 @@ update.
                         teacher's opinion of them
             preference  sg_preference_loss on pairs of token sequences, the
                         teacher's favourites chosen
+            cross_entropy  sg_linear_ce_loss on hidden states and the
+                        teacher's favourites: the head's gradient without
+                        any logits
   gradient  d loss / d head = d loss / d logits ^T  hidden states
   sync      sg_topk_to_coo -> sg_hash_partition -> sg_aggregate ->
             sg_scatter_dense, the largest 5% of every worker's gradient with
             the rest kept for the next step
+  update    sgd         the sum of the gradients
+            orthogonal  sg_orthogonalize of their momentum, as the Muon
+                        optimiser does
 """
 import argparse
 import os
@@ -72,41 +79,66 @@ def preference_step(logits, teacher, batch, g):
     return loss.sum(), grad
 
 
+def cross_entropy_step(hidden, head, target):
+    """(loss, gradient of the head) from hidden states, without logits."""
+    label = (hidden @ target.t()).argmax(1).int()
+    weight = torch.full((hidden.shape[0],), 1.0 / hidden.shape[0], device=hidden.device)
+    loss, _, _, grad = sg.sg_linear_ce_loss(hidden, head, label, weight=weight, want_grad=False,
+                                            grad_head=torch.empty_like(head))
+    return loss.sum(), grad
+
+
 STEPS = {"distill": distill_step, "policy": policy_step, "preference": preference_step}
 
 
-def train(loss="distill", steps=12, workers=4, rows=256, vocab=2000, width=64, density=0.05, rate=None, seed=1):
+def train(loss="distill", steps=12, workers=4, rows=256, vocab=2000, width=64, density=0.05, rate=None, seed=1,
+          update_kind="sgd"):
     """Returns the mean loss of every step (policy: minus the teacher's mean
     log-probability of the sampled tokens)."""
-    rate = {"distill": 160.0, "policy": 60.0, "preference": 400.0}[loss] if rate is None else rate
+    if rate is None:
+        rate = {"distill": 160.0, "policy": 60.0, "preference": 400.0, "cross_entropy": 60.0}[loss]
+        if update_kind == "orthogonal":
+            rate = 2.0  # singular values near 1, whatever the gradient's size
     dev = torch.device("cuda", torch.cuda.current_device())
     g = torch.Generator(device=dev).manual_seed(seed)
     target = torch.randn(vocab, width, device=dev, generator=g) * 0.4
     head = torch.randn(vocab, width, device=dev, generator=g) * 0.05
     resid = torch.zeros(workers, vocab * width, device=dev)
+    momentum = torch.zeros_like(head)
     curve = []
     for step in range(steps):
         grads, losses = torch.empty_like(resid), []
         for w in range(workers):
             hidden = torch.randn(rows, width, device=dev, generator=g)
+            if loss == "cross_entropy":
+                value, grad = cross_entropy_step(hidden, head, target)
+                grads[w] = grad.reshape(-1)
+                losses.append(value)
+                continue
             logits = (hidden @ head.t()).bfloat16()
             teacher = (hidden @ target.t()).bfloat16()
             value, grad = STEPS[loss](logits, teacher, hidden, g)
             grads[w] = (grad.float().t().contiguous() @ hidden).reshape(-1)
             losses.append(value)
-        update = synchronize(grads, resid, density)
-        head -= rate / workers * update.view(vocab, width)
+        update = synchronize(grads, resid, density).view(vocab, width)
+        if update_kind == "orthogonal":
+            momentum.mul_(0.9).add_(update)
+            head -= rate * sg.sg_orthogonalize(momentum)
+        else:
+            head -= rate / workers * update
         curve.append(torch.stack(losses).mean())
     return [float(v) for v in torch.stack(curve).cpu()]
 
 
 def main():
     ap = argparse.ArgumentParser(description=__doc__, formatter_class=argparse.RawDescriptionHelpFormatter)
-    ap.add_argument("--loss", choices=sorted(STEPS), default=None, help="default: each in turn")
+    ap.add_argument("--loss", choices=sorted(STEPS) + ["cross_entropy"], default=None,
+                    help="default: each in turn")
+    ap.add_argument("--update", choices=["sgd", "orthogonal"], default="sgd")
     ap.add_argument("--steps", type=int, default=12)
     a = ap.parse_args()
-    for loss in [a.loss] if a.loss else sorted(STEPS):
-        curve = train(loss, a.steps)
+    for loss in [a.loss] if a.loss else sorted(STEPS) + ["cross_entropy"]:
+        curve = train(loss, a.steps, update_kind=a.update)
         print("%-10s %s" % (loss, " ".join("%.4f" % v for v in curve)))
         if sg.sg_device_error():
             raise SystemExit("a kernel noticed a violated precondition")

@@ -702,7 +702,7 @@ int sg_linear_ce_loss(const void* d_hidden, uint64_t ld_hidden, const void* d_he
  * row makes its gradient, P and the loss NaN; a logit of -inf has probability 0, a
  * row of nothing else no softmax (NaN).
  * Sums: fp32 within a row and over a block's rows, fp64 over blocks.
- * Results do not depend on timing.  No workspace is needed up to 16384 logits.
+ * Results do not depend on timing.  No workspace is needed up to 32768 logits.
  * Limits: 1 <= E, 1 <= k, T < 2^31, coefficients in [0, 1e6] (SG_EINVAL); E <= 1024, k <= E,
  * T * k < 2^31 (SG_EUNSUPPORTED). */
 size_t sg_balance_workspace_bytes(uint64_t T, uint32_t E, uint32_t k, sg_dtype dt);

@@ -22,7 +22,7 @@ namespace sg {
 constexpr uint32_t BL_MAX_E = 1024;
 constexpr int BL_NT = 1024, BL_WAVES = BL_NT / 64;
 constexpr uint32_t BL_COUNT_BLOCKS = 64; // their counts are added up by every block of the next kernel
-constexpr uint32_t BL_FEW = 16384;       // elements that one block takes alone
+constexpr uint32_t BL_FEW = 32768;       // elements that one block takes alone
 constexpr uint32_t BL_BLOCKS = 256;
 
 struct BalArgs {
@@ -333,7 +333,8 @@ static BalWs bal_carve(Carver& cv, uint32_t E)
 template <typename T, int VEC, int C>
 static int bal_launch(const BalArgs& a, hipStream_t st)
 {
-    // one launch instead of three (FEWNOTE)
+    // One launch instead of three while its one block is not the longer way.  us a call, one block and three
+    // launches: 256 x 64 fp32 13, 20; 512 x 64 17, 20; 2048 x 16 17, 20; 256 x 256 33, 20; 4096 x 16 28, 20
     if (a.T * a.E <= BL_FEW) {
         balance_few_kernel<T, VEC, C><<<1, BL_NT, 0, st>>>(a);
         SG_TRY_LAUNCH();
