@@ -665,14 +665,16 @@ int sg_preference_loss(const void* d_logits, sg_dtype dt, uint64_t T, uint64_t V
  *            vocabulary is taken in pieces that fit (at least 256 tokens), and the
  *            logits' product runs twice.
  * A NaN, or an infinity that makes a logit of a row that counts +inf or NaN,
- * makes the row's results NaN, and with them the whole grad_head.
+ * makes the row's results NaN, and with them the whole grad_head; so does a weight
+ * that is not finite.  The other rows' results keep their precision.
  * With SG_F32 every infinity in the head or in such a row does.
  * Sums: products and exponentials in fp32, a row's sums and scalars in fp64.
  * SG_BF16: g is rounded to bf16 once between the products; SG_F32: operands
  * keep 22 bits under one power of two per tensor.  Results do not depend on timing.
  * Rows of the head that start on 16 bytes (bf16, H and ld_head multiples of 8) are
  * used as they lie; others are copied to the workspace first.
- * Limits: T <= 2^24, V < 2^31, 1 <= H <= 2^20, T * V / 2048 < 2^31 (SG_EUNSUPPORTED);
+ * Limits: V < 2^31, 1 <= H <= 2^20, T * ceil(H / 1024) < 2^24, ceil(T / 128) * ceil(V / 128)
+ * < 2^24 (SG_EUNSUPPORTED);
  * ld's < 2^40, 1e-37 <= inv_temp <= 1e6, 0 <= z_coef <= 1e6 (SG_EINVAL).  The
  * workspace depends on the arguments of its query alone (d_head: its address).
  * T = 0 writes grad_head = 0 and nothing else. */

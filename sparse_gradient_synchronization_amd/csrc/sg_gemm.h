@@ -420,7 +420,7 @@ static int launch_gemm(const Gemm& g, uint32_t batch, const Epi& epi, hipStream_
 {
     const uint64_t tm = ceil_div(g.M, Cfg::BM), tn = ceil_div(g.N, Cfg::BN);
     if (tm == 0 || tn == 0 || batch == 0) return SG_OK;
-    if (tm * tn * g.splits * batch >= (1ull << 31) || g.splits == 0) return SG_EUNSUPPORTED;
+    if (g.splits == 0 || tm * tn * g.splits * batch >= (1ull << 32) / (Cfg::NT * Cfg::GR)) return SG_EUNSUPPORTED;
     if (g.a.ld > GEMM_MAX_LD || g.b.ld > GEMM_MAX_LD) return SG_EUNSUPPORTED;
     const uint32_t blocks = tile_count<Cfg::BM, Cfg::BN>((uint32_t)tm, (uint32_t)tn, g.tri) * g.splits * batch;
     gemm_kernel<Cfg, AL, BL, F16, Epi><<<blocks, Cfg::NT * Cfg::GR, 0, st>>>(g, batch, epi);

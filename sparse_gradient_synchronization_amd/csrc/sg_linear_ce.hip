@@ -41,9 +41,9 @@ struct CeRow {
 };
 
 struct CeScal { // power-of-two scales of the fp32 planes and their inverses
-    uint32_t max_x, max_w, max_g; // bits of the largest magnitudes
+    uint32_t max_x, max_w, max_g; // bits of the largest finite magnitudes
     uint32_t live;                // rows that count
-    // largest |weight / temperature| of the live rows: g is kept relative to it,
+    // largest finite |weight / temperature| of the live rows: g is kept relative to it,
     // so that with equal weights the label's -1 is a bf16 number and not 1 / N rounded
     double top;
 };
@@ -52,7 +52,6 @@ struct CeScal { // power-of-two scales of the fp32 planes and their inverses
 __device__ __forceinline__ int ce_exponent(uint32_t bits)
 {
     const int e = (int)(bits >> 23 & 255) - 127;
-    if (bits >= 0x7f800000u) return 0; // an infinity or NaN spoils its products anyway
     return 12 - (e < -126 ? -126 : e);
 }
 
@@ -82,7 +81,7 @@ __global__ __launch_bounds__(1024) void ce_rows_kernel(CeArgs p, uint32_t* row, 
             const int32_t y = p.label[t];
             const float wt = p.weight ? p.weight[t] : 1.f;
             live = y >= 0 && (uint32_t)y < p.V && wt != 0.f;
-            if (live) top = fmaxf(top, fabsf(wt));
+            if (live && fabsf(wt) < INFINITY) top = fmaxf(top, fabsf(wt));
         }
         const uint64_t b = ballot(live);
         __syncthreads();
@@ -150,7 +149,8 @@ struct CeItems {
     }
 };
 
-// the largest magnitude of the rows (of the live ones: row != NULL)
+// the largest finite magnitude of the rows (of the live ones: row != NULL); one
+// row's infinity or NaN leaves the others their precision
 __global__ __launch_bounds__(256) void ce_max_kernel(CeSrc s, uint64_t rows, const uint32_t* row, const CeScal* scal,
                                                      uint32_t* out)
 {
@@ -172,7 +172,7 @@ __global__ __launch_bounds__(256) void ce_max_kernel(CeSrc s, uint64_t rows, con
 #pragma unroll
             for (int k = 0; k < 8; ++k) {
                 const uint32_t b = __float_as_uint(v[u][k]) & 0x7fffffffu;
-                m = b > m ? b : m;
+                m = b > m && b < 0x7f800000u ? b : m;
             }
     }
 #pragma unroll
@@ -464,7 +464,7 @@ __global__ __launch_bounds__(256) void ce_join_kernel(CeArgs p, const uint32_t* 
     // A maximum of whole numbers: the order of the rows does not matter.  Looked at first: with equal weights
     // most rows have nothing to add, and as many atomics on one word took 12 ns each (4088 rows: 50 us).
     const uint32_t big = __float_as_uint(fmaxf(fabsf(r.a), fabsf(r.b)));
-    if (planes && big > *(volatile uint32_t*)&scal->max_g) atomicMax(&scal->max_g, big);
+    if (planes && big < 0x7f800000u && big > *(volatile uint32_t*)&scal->max_g) atomicMax(&scal->max_g, big);
 }
 
 // kept exponentials -> g, in place; rows up to the next multiple of 64 are
@@ -791,7 +791,8 @@ static CePlan ce_plan(Carver& cv, uint64_t T, uint64_t V, uint32_t H, sg_dtype d
     p.tile = T <= 32 ? 2 : pick(T, V, kh);
     p.groups = (uint32_t)ceil_div(V, ce_tile_cols(p.tile));
     const uint64_t Vp = align_up(V, 256), es = p.two ? 4 : 2;
-    p.kept = Vp <= (1u << 20) && p.Tp * Vp * es <= keep;
+    // 8 elements of g to a thread of ce_grad_kernel
+    p.kept = Vp <= (1u << 20) && p.Tp * Vp * es <= keep && p.Tp * Vp < (1ull << 35);
     if (p.kept) {
         p.piece = (uint32_t)Vp;
     } else {
@@ -806,6 +807,7 @@ static CePlan ce_plan(Carver& cv, uint64_t T, uint64_t V, uint32_t H, sg_dtype d
             for (uint64_t s = 1; s <= 64 && s <= steps; ++s) {
                 const uint64_t per = ceil_div(steps, s);
                 if (ceil_div(steps, per) != s) continue; // a part without a step
+                if (s > 1 && m * ceil_div(n, 1024) >= (1u << 24)) continue; // ce_sum_kernel's grid
                 double us = tile_time(t == 0 ? TILE_L : TILE_M, tiles(m, n, t == 0 ? 256 : 128) * s, per * nseg);
                 if (s > 1 || !alone) us += 5.0 + 8.0 * s * m * n / 4.5e6;
                 if (us < least) {
@@ -860,9 +862,8 @@ static bool ce_sizes(uint64_t T, uint64_t V, uint64_t H, sg_dtype dt)
 }
 static bool ce_supported(uint64_t T, uint64_t V, uint64_t H)
 {
-    // blocks of 32 x 128 tiles, and of 8 x 256 elements of g
-    return H <= (1u << 20) && T <= (1u << 24) && ceil_div(T, 32) * ceil_div(V, 128) < (1ull << 31) &&
-           align_up(T, 64) * ceil_div(V, 2048) < (1ull << 31);
+    // grids of 2^32 threads: 256 to a tile of 128 x 128, to a row and to 1024 columns of a row
+    return H <= (1u << 20) && T * ceil_div(H, 1024) < (1u << 24) && ceil_div(T, 128) * ceil_div(V, 128) < (1u << 24);
 }
 
 } // namespace sg

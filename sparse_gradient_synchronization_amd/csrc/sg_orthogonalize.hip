@@ -138,7 +138,7 @@ __global__ __launch_bounds__(256) void ns_pack_kernel(NsIn in, const double* par
 // diag: of a symmetric result in one plane, what the rounding took from the
 // diagonal.  Near the end G and its polynomial are close to multiples of the
 // identity, so most of what one plane loses is lost there (a 1000 x 1000 bf16
-// update is 1.7e-3 off with it and 2.0e-3 without; the output's rounding alone
+// update is 1.84e-3 off with it and 1.99e-3 without; the output's rounding alone
 // is 1.66e-3).
 struct NsPlanes {
     uint16_t *hi, *lo;
@@ -652,6 +652,8 @@ extern "C" int sg_orthogonalize(const void* d_update, sg_dtype dt, uint32_t B, u
     if (ld < n || ld_out < n || ld >= (1ull << 40) || ld_out >= (1ull << 40)) return SG_EINVAL;
     if (B > 1 && (stride < (m - 1) * ld + n || stride_out < (m - 1) * ld_out + n || stride >= (1ull << 60) || stride_out >= (1ull << 60))) return SG_EINVAL;
     if (!d_update || !d_out || !d_ws) return SG_EINVAL;
+    for (const void* q : {d_update, (const void*)d_out})
+        if (reinterpret_cast<uintptr_t>(q) % (dt == SG_F32 ? 4 : 2)) return SG_EINVAL;
     if (d_out == d_update && (ld != ld_out || (B > 1 && stride != stride_out))) return SG_EINVAL;
     if (!ns_sizes(m, n) || B > 65535 || !ns_in_range(steps, a, b, c)) return SG_EUNSUPPORTED;
     if (ws_bytes < sg_orthogonalize_workspace_bytes(B, m, n, dt)) return SG_ECAPACITY;

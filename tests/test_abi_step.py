@@ -64,6 +64,10 @@ def test_linear_ce_arguments(L):
     assert f(H=(1 << 20) + 8, ldx=1 << 21, ldw=1 << 21, ldgx=1 << 21, ldgw=1 << 21) == SG_EUNSUPPORTED
     assert f(T=(1 << 24) + 1) == SG_EUNSUPPORTED
     assert f(T=1 << 24, V=1 << 30) == SG_EUNSUPPORTED
+    # grids of 2^32 threads: rows of long hidden states, logits in tiles of 128 x 128
+    long = dict(H=4096, ldx=4096, ldw=4096, ldgx=4096, ldgw=4096)
+    assert f(T=1 << 22, **long) == SG_EUNSUPPORTED and f(T=1 << 19, V=(1 << 19) + 1) == SG_EUNSUPPORTED
+    assert f(T=(1 << 22) - 1, nws=0, **long) == SG_ECAPACITY and f(T=1 << 19, V=1 << 18, nws=0) == SG_ECAPACITY
     assert f(nws=0) == SG_ECAPACITY
     assert f(T=0, x=N, label=N, loss=N, gw=N) == SG_OK
 
@@ -98,7 +102,7 @@ def test_orthogonalize_arguments(L):
     f = ortho(L)
     for bad in (dict(dt=2), dict(steps=0), dict(steps=65), dict(eps=-1.0), dict(eps=NAN), dict(eps=INF), dict(a=NAN), dict(b=INF),
                 dict(c=-INF), dict(ld=23), dict(ldo=23), dict(ld=1 << 40), dict(ldo=1 << 40), dict(stride=383), dict(so=383),
-                dict(x=N), dict(out=N), dict(ws=N), dict(out=F, ldo=25, so=400), dict(out=F, so=400)):
+                dict(x=N), dict(out=N), dict(ws=N), dict(x=ODD), dict(out=ODD), dict(out=F, ldo=25, so=400), dict(out=F, so=400)):
         assert f(**bad) == SG_EINVAL, bad
     # coefficients whose iterates leave the scales' range
     for bad in (dict(a=5.0), dict(a=3.0, b=3.0, c=3.0), dict(b=-200.0), dict(a=1.0, b=0.0, c=60.0)):

@@ -59,6 +59,27 @@ def test_large_tiles(dtype):
         check(out, x, w, label, weight)
 
 
+# The variants that a rule on sizes chooses, at both sides of each rule's edge: dw as a stream of rows (64 rows)
+# with the hidden dimension in parts or whole, dw in parts of the rows, dx in many parts of the vocabulary
+VARIANTS = [(63, 700, 700), (64, 700, 257), (65, 700, 257), (3, 130, 2056), (40, 70000, 65), (4088, 3264, 64),
+            (6000, 150, 96), (200, 40000, 60), (1100, 300, 1030)]
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("T,V,H", VARIANTS)
+def test_variants(T, V, H, dtype):
+    """Into rows apart that start on 16 bytes and into rows that start anywhere."""
+    need_gpu()
+    x, w, label, weight = make(T, V, H, dtype, T)
+    out = sg.sg_linear_ce_loss(x, w, label, weight=weight)
+    check(out, x, w, label, weight)
+    for pad in (16 - H % 8, 1):
+        flat = torch.full((V * (H + pad) + 3,), 7.0, device="cuda", dtype=x.dtype)
+        gw = flat[int(pad == 1):][:V * (H + pad)].view(V, H + pad)
+        sg.sg_linear_ce_loss(x, w, label, weight=weight, grad_head=gw[:, :H])
+        assert torch.equal(gw[:, :H], out[3]) and bool((gw[:, H:] == 7.0).all()) and bool((flat[-2:] == 7.0).all())
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 def test_outputs_alone(dtype):
     """Each gradient alone, none, and the loss the same bits whatever is asked for."""
@@ -149,6 +170,28 @@ def test_not_finite(dtype):
     v[7, 2] = float("nan")
     out = sg.sg_linear_ce_loss(x, v, label, weight=weight)
     assert bool(out[0].isnan().all()) and bool(out[2].isnan().all())
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("where", ["hidden", "weight"])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf")])
+def test_a_row_not_finite_leaves_the_others_their_precision(bad, where, dtype):
+    """The other rows against their definition, small operands among them."""
+    need_gpu()
+    x, w, label, weight = make(50, 700, 64, dtype, masked=0.0, scale=1e-3)
+    x = (x.float() * 1e-4).to(x.dtype)
+    lone = label.clone()
+    lone[20] = -100
+    val, err = ref.linear_ce(x, w, lone, weight, 1.0, 0.0)
+    if where == "hidden":
+        x[20, 11] = bad
+    else:
+        weight[20] = bad
+    out = sg.sg_linear_ce_loss(x, w, label, weight=weight)
+    rest = torch.arange(50, device="cuda") != 20
+    for name, got in zip(NAMES[:3], out):
+        ref.close(got[rest], val[name][rest], err[name][rest], name)
+    assert not bool(out[0][20].isfinite()) and not bool(out[2][20].isfinite().all())
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])

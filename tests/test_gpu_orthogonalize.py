@@ -50,6 +50,22 @@ def test_large_tiles(shape, dtype):
     check(sg.sg_orthogonalize(u), u)
 
 
+# what the rule on tiles and parts of k chooses between: short and long k at a small side (the product in parts,
+# joined; four groups of a block on one tile), many small matrices, one of some hundreds
+VARIANTS = [(64, 5000), (5000, 64), (130, 3300), (3300, 130), (256, 512), (512, 256), (40, 70, 50), (9, 512, 128),
+            (512, 512), (640, 2600), (2600, 640)]
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("shape", VARIANTS)
+def test_variants(shape, dtype):
+    need_gpu()
+    g = torch.Generator(device="cuda").manual_seed(sum(shape))
+    u = torch.randn(shape, device="cuda", generator=g).to(DT[dtype])
+    check(sg.sg_orthogonalize(u), u)
+    check(sg.sg_orthogonalize(u, steps=1), u, steps=1)
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 def test_singular_values(dtype):
     """Known singular values: the result has the polynomial's, in the same directions."""
