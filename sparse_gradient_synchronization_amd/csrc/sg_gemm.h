@@ -458,14 +458,25 @@ struct TileRows {
 };
 
 // eight results, of which `left` lie inside
+// up to 8 elements or 4 of a row that may start anywhere: gfx950 stores 16 bytes at any element's address
 __device__ __forceinline__ void store_tail(uint16_t* q, s16x8 v, uint32_t left)
 {
     if (left >= 8) {
-        *reinterpret_cast<s16x8*>(q) = v;
+        __builtin_memcpy(q, &v, 16);
     } else {
 #pragma unroll
         for (int k = 0; k < 8; ++k)
             if ((uint32_t)k < left) q[k] = (uint16_t)v[k];
+    }
+}
+__device__ __forceinline__ void store_tail(float* q, f32x4 v, uint32_t left)
+{
+    if (left >= 4) {
+        __builtin_memcpy(q, &v, 16);
+    } else {
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            if ((uint32_t)k < left) q[k] = v[k];
     }
 }
 

@@ -547,46 +547,60 @@ struct CePartEpi {
     }
 };
 
-// The rows of dx (pos: their places, or -1) or dw (pos NULL) from the sums: 1024
-// columns to a block.  other: what the planes of g were multiplied with.
-template <typename E>
-__global__ __launch_bounds__(256) void ce_sum_kernel(const int32_t* pos, const CeScal* scal, const uint32_t* other,
-                                                     const float* part, uint64_t ldp, uint64_t rows, uint32_t splits,
-                                                     bool planes, E* out, uint64_t ld, uint32_t H)
+// The rows of dx (pos: their places, or -1) or dw (pos NULL) from the sums, four
+// columns to S threads, each with every S-th part.  other: what the planes of g were
+// multiplied with.
+template <typename E, int S>
+__global__ __launch_bounds__(256) void ce_sum_kernel(const int32_t* pos, uint64_t n, const CeScal* scal,
+                                                     const uint32_t* other, const float* part, uint64_t ldp,
+                                                     uint64_t rows, uint32_t splits, bool planes, E* out, uint64_t ld,
+                                                     uint32_t H)
 {
-    const uint32_t cols = (H + 1023) / 1024;
-    const uint64_t t = blockIdx.x / cols;
-    const uint32_t h = blockIdx.x % cols * 1024 + threadIdx.x * 4;
-    if (h >= H) return;
-    const int64_t j = pos ? pos[t] : (int64_t)t;
+    constexpr uint32_t W = 256 / S;
+    const uint32_t sl = threadIdx.x / W, per = (H + 3) / 4;
+    const uint64_t i0 = blockIdx.x * (uint64_t)W + threadIdx.x % W;
+    const CeItems items(n * per, per);
+    const bool in = i0 < items.n;
+    uint64_t t = 0;
+    uint32_t h = 0;
+    if (in) items.split(i0, &t, &h);
+    h *= 4;
+    const int64_t j = !in ? -1 : pos ? pos[t] : (int64_t)t;
+    const int unit = planes ? -ce_exponent(scal->max_g) - ce_exponent(*other) : 0;
+    const float top = (float)scal->top;
     f32x4 s = {0.f, 0.f, 0.f, 0.f};
     if (j >= 0) {
         const float* q = part + (uint64_t)j * ldp + h;
 #pragma unroll 8
-        for (uint32_t k = 0; k < splits; ++k) s += *reinterpret_cast<const f32x4*>(q + k * rows * ldp);
-        const int unit = planes ? -ce_exponent(scal->max_g) - ce_exponent(*other) : 0;
-        const float top = (float)scal->top;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) s[i] = ldexpf(s[i], unit) * top;
+        for (uint32_t k = sl; k < splits; k += S) s += *reinterpret_cast<const f32x4*>(q + k * rows * ldp);
     }
+    if constexpr (S > 1) {
+        __shared__ f32x4 lds[S - 1][W];
+        if (sl > 0) lds[sl - 1][threadIdx.x % W] = s;
+        __syncthreads();
+        if (sl > 0) return;
+#pragma unroll
+        for (int k = 0; k < S - 1; ++k) s += lds[k][threadIdx.x];
+    }
+    if (!in) return;
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-        if (h + i < H) RowIO<E>::put(out + t * ld + h + i, s[i]);
+        if (h + i < H) RowIO<E>::put(out + t * ld + h + i, j < 0 ? 0.f : ldexpf(s[i], unit) * top);
 }
 
 // dw, rounded once to the caller's type
+template <bool PLANES>
 struct CeHeadEpi {
     const CeScal* scal;
     void* out;
     uint64_t ld;
-    bool planes, wide; // wide: rows start on 16 bytes
     template <class Cfg>
     __device__ __forceinline__ void run(const f32x4 (&acc)[Cfg::MT][Cfg::NTT], const TileAt& at) const
     {
         const uint32_t l = threadIdx.x % 64;
-        const int unit = planes ? -ce_exponent(scal->max_g) - ce_exponent(scal->max_x) : 0;
+        const int unit = PLANES ? -ce_exponent(scal->max_g) - ce_exponent(scal->max_x) : 0;
         const float top = (float)scal->top;
-        if (!planes && wide) {
+        if constexpr (!PLANES) {
 #pragma unroll
             for (int i = 0; i < Cfg::MT; ++i)
 #pragma unroll
@@ -613,24 +627,7 @@ struct CeHeadEpi {
                 f32x4 v = acc[i][j];
 #pragma unroll
                 for (int k = 0; k < 4; ++k) v[k] = ldexpf(v[k], unit) * top;
-                if (planes) {
-                    float* q = static_cast<float*>(out) + m * ld + n;
-                    if (wide && n + 4 <= at.N) *reinterpret_cast<f32x4*>(q) = v;
-                    else
-#pragma unroll
-                        for (int k = 0; k < 4; ++k)
-                            if (n + k < at.N) q[k] = v[k];
-                } else {
-                    uint16_t* q = static_cast<uint16_t*>(out) + m * ld + n;
-                    s16x4 w;
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) w[k] = __builtin_bit_cast(short, (__bf16)v[k]);
-                    if (wide && n + 4 <= at.N) *reinterpret_cast<s16x4*>(q) = w;
-                    else
-#pragma unroll
-                        for (int k = 0; k < 4; ++k)
-                            if (n + k < at.N) q[k] = (uint16_t)w[k];
-                }
+                store_tail(static_cast<float*>(out) + m * ld + n, v, at.N - n);
             }
     }
 };
@@ -645,7 +642,7 @@ struct CeHeadEpi {
 template <bool PLANES>
 __global__ __launch_bounds__(256, PLANES ? 3 : 4) void ce_head_few_kernel(Mat g, Mat x, const CeScal* scal, void* out,
                                                                           uint64_t ld, uint32_t V, uint32_t H,
-                                                                          uint32_t cols, bool wide)
+                                                                          uint32_t cols)
 {
     constexpr int P = PLANES ? 2 : 1, TILE = 64 * GEMM_BK * 2;
     __shared__ __align__(1024) char lds[3 * P * TILE];
@@ -716,22 +713,11 @@ __global__ __launch_bounds__(256, PLANES ? 3 : 4) void ce_head_few_kernel(Mat g,
             if (v < V && n < H) {
                 if (PLANES) {
                     float* const q = static_cast<float*>(out) + v * ld + n;
-                    if (wide && n + 8 <= H) {
-                        *reinterpret_cast<f32x4*>(q) = f32x4{r[0], r[1], r[2], r[3]};
-                        *reinterpret_cast<f32x4*>(q + 4) = f32x4{r[4], r[5], r[6], r[7]};
-                    } else {
-#pragma unroll
-                        for (int i = 0; i < 8; ++i)
-                            if (n + i < H) q[i] = r[i];
-                    }
+                    store_tail(q, f32x4{r[0], r[1], r[2], r[3]}, H - n);
+                    if (n + 4 < H) store_tail(q + 4, f32x4{r[4], r[5], r[6], r[7]}, H - n - 4);
                 } else {
-                    const s16x8 b = __builtin_bit_cast(s16x8, RowIO<bf16_bits>::pack(r));
-                    store_tail(static_cast<uint16_t*>(out) + v * ld + n, b, wide ? H - n : 0);
-                    if (!wide) {
-#pragma unroll
-                        for (int i = 0; i < 8; ++i)
-                            if (n + i < H) (static_cast<uint16_t*>(out) + v * ld + n)[i] = (uint16_t)b[i];
-                    }
+                    store_tail(static_cast<uint16_t*>(out) + v * ld + n,
+                               __builtin_bit_cast(s16x8, RowIO<bf16_bits>::pack(r)), H - n);
                 }
             }
         }
@@ -791,7 +777,9 @@ static CePlan ce_plan(Carver& cv, uint64_t T, uint64_t V, uint32_t H, sg_dtype d
     p.tile = T <= 32 ? 2 : pick(T, V, kh);
     p.groups = (uint32_t)ceil_div(V, ce_tile_cols(p.tile));
     const uint64_t Vp = align_up(V, 256), es = p.two ? 4 : 2;
-    // 8 elements of g to a thread of ce_grad_kernel
+    // 8 elements of g to a thread of ce_grad_kernel.  All kept where they fit: a second product instead costs more than
+    // the pass over them from some hundreds of H on.  us a call, kept and again, 4096 x 32768 x H bf16: 128 424, 370; 256
+    // 476, 468; 512 620, 643; 1024 886, 998; fp32: 128 887, 939; 512 1477, 1715
     p.kept = Vp <= (1u << 20) && p.Tp * Vp * es <= keep && p.Tp * Vp < (1ull << 35);
     if (p.kept) {
         p.piece = (uint32_t)Vp;
@@ -862,7 +850,7 @@ static bool ce_sizes(uint64_t T, uint64_t V, uint64_t H, sg_dtype dt)
 }
 static bool ce_supported(uint64_t T, uint64_t V, uint64_t H)
 {
-    // grids of 2^32 threads: 256 to a tile of 128 x 128, to a row and to 1024 columns of a row
+    // grids of 2^32 threads: 256 to a tile of 128 x 128 and to a row, one to 4 columns of a row
     return H <= (1u << 20) && T * ceil_div(H, 1024) < (1u << 24) && ceil_div(T, 128) * ceil_div(V, 128) < (1u << 24);
 }
 
@@ -911,8 +899,6 @@ extern "C" int sg_linear_ce_loss(const void* d_hidden, uint64_t ld_hidden, const
     const CePlan p = ce_plan(cv, T, V, (uint32_t)H, dt, d_head, ld_head, d_grad_hidden != nullptr, d_grad_head != nullptr, keep_bytes);
     const float c = (float)(inv_temp * 1.4426950408889634);
     const CeArgs a = {d_label, d_weight, d_loss, d_lse, T, (uint32_t)V, inv_temp, z_coef, c};
-    const auto wide = [&](const void* q, uint64_t ld, uint64_t b) { return reinterpret_cast<uintptr_t>(q) % b == 0 && ld * es % b == 0; };
-
     ce_rows_kernel<<<1, 1024, 0, st>>>(a, p.row, p.pos, p.scal);
     SG_TRY_LAUNCH();
     const CeSrc sx = {d_hidden, ld_hidden, p.H}, sw = {d_head, ld_head, p.H};
@@ -984,25 +970,24 @@ extern "C" int sg_linear_ce_loss(const void* d_hidden, uint64_t ld_hidden, const
                 const uint64_t want = ceil_div(1024, ceil_div(n, 64)), most = ceil_div(H, 256);
                 const uint32_t cols = (uint32_t)align_up(ceil_div(H, want < most ? want : most), 64);
                 const dim3 blocks((unsigned)ceil_div(n, 64), (unsigned)ceil_div(H, cols));
-                const bool w16 = wide(d_grad_head, ld_grad_head, 16);
-                if (p.two) ce_head_few_kernel<true><<<blocks, 256, 0, st>>>(mg, mx, p.scal, out, ld_grad_head, (uint32_t)n, p.H, cols, w16);
-                else ce_head_few_kernel<false><<<blocks, 256, 0, st>>>(mg, mx, p.scal, out, ld_grad_head, (uint32_t)n, p.H, cols, w16);
+                if (p.two) ce_head_few_kernel<true><<<blocks, 256, 0, st>>>(mg, mx, p.scal, out, ld_grad_head, (uint32_t)n, p.H, cols);
+                else ce_head_few_kernel<false><<<blocks, 256, 0, st>>>(mg, mx, p.scal, out, ld_grad_head, (uint32_t)n, p.H, cols);
                 SG_TRY_LAUNCH();
             } else if (p.splits_w > 1) {
                 const CePartEpi e = {p.part_w, p.Hp, p.piece, false};
                 rc = p.two ? ce_product<KS, KS, true>(p.tile_w, g3, e, st) : ce_product<KS, KS, false>(p.tile_w, g3, e, st);
                 if (rc) return rc;
-                const unsigned blocks = (unsigned)(n * ceil_div(H, 1024));
+                const unsigned blocks = (unsigned)ceil_div(n * ceil_div(H, 4), 256);
                 if (p.two)
-                    ce_sum_kernel<float><<<blocks, 256, 0, st>>>(nullptr, p.scal, &p.scal->max_x, p.part_w, p.Hp, p.piece,
-                                                                 p.splits_w, true, (float*)out, ld_grad_head, p.H);
+                    ce_sum_kernel<float, 1><<<blocks, 256, 0, st>>>(nullptr, n, p.scal, &p.scal->max_x, p.part_w, p.Hp, p.piece,
+                                                                    p.splits_w, true, (float*)out, ld_grad_head, p.H);
                 else
-                    ce_sum_kernel<bf16_bits><<<blocks, 256, 0, st>>>(nullptr, p.scal, nullptr, p.part_w, p.Hp, p.piece,
-                                                                     p.splits_w, false, (bf16_bits*)out, ld_grad_head, p.H);
+                    ce_sum_kernel<bf16_bits, 1><<<blocks, 256, 0, st>>>(nullptr, n, p.scal, nullptr, p.part_w, p.Hp, p.piece,
+                                                                        p.splits_w, false, (bf16_bits*)out, ld_grad_head, p.H);
                 SG_TRY_LAUNCH();
             } else {
-                const CeHeadEpi e = {p.scal, out, ld_grad_head, p.two, wide(d_grad_head, ld_grad_head, 16)};
-                rc = p.two ? ce_product<KS, KS, true>(p.tile_w, g3, e, st) : ce_product<KS, KS, false>(p.tile_w, g3, e, st);
+                if (p.two) rc = ce_product<KS, KS, true>(p.tile_w, g3, CeHeadEpi<true>{p.scal, out, ld_grad_head}, st);
+                else rc = ce_product<KS, KS, false>(p.tile_w, g3, CeHeadEpi<false>{p.scal, out, ld_grad_head}, st);
                 if (rc) return rc;
             }
         }
@@ -1014,13 +999,19 @@ extern "C" int sg_linear_ce_loss(const void* d_hidden, uint64_t ld_hidden, const
         }
     }
     if (d_grad_hidden) {
-        const unsigned hblocks = (unsigned)(T * ceil_div(H, 1024));
-        if (p.two)
-            ce_sum_kernel<float><<<hblocks, 256, 0, st>>>(p.pos, p.scal, &p.scal->max_w, p.part, p.Hp, p.Tp, p.splits, true,
-                                                          (float*)d_grad_hidden, ld_grad_hidden, p.H);
-        else
-            ce_sum_kernel<bf16_bits><<<hblocks, 256, 0, st>>>(p.pos, p.scal, nullptr, p.part, p.Hp, p.Tp, p.splits, false,
-                                                              (bf16_bits*)d_grad_hidden, ld_grad_hidden, p.H);
+        // few rows have many parts: four threads to a sum.  us a call, 24 x 32000 x 2048 bf16: 96 for 98
+        const auto sum = [&](auto zero, auto slices) {
+            typedef decltype(zero) E;
+            constexpr int S = decltype(slices)::value;
+            ce_sum_kernel<E, S><<<(unsigned)ceil_div(T * ceil_div(H, 4), 256 / S), 256, 0, st>>>(
+                p.pos, T, p.scal, &p.scal->max_w, p.part, p.Hp, p.Tp, p.splits, p.two, (E*)d_grad_hidden, ld_grad_hidden, p.H);
+        };
+        const auto by_rows = [&](auto zero) {
+            if (T <= 32) sum(zero, std::integral_constant<int, 4>());
+            else sum(zero, std::integral_constant<int, 1>());
+        };
+        if (p.two) by_rows(float());
+        else by_rows(bf16_bits());
         SG_TRY_LAUNCH();
     }
     return SG_OK;

@@ -437,7 +437,6 @@ struct NsStepEpi {
     void* last; // NULL: planes
     uint64_t ld, stride;
     uint32_t m, n;
-    bool bf16, wide;
     const NsScale* scale;
     uint32_t step;
     NsCoef coef;
@@ -480,7 +479,7 @@ struct NsStepEpi {
         }
         if (!last) {
             ns_put_tile<Cfg, TWO>(out, at, acc, false);
-        } else if (bf16 && wide) {
+        } else if constexpr (!TWO) { // an update of one plane is bf16
             typedef TileRows<Cfg> Rows;
 #pragma unroll
             for (int i = 0; i < Cfg::MT; ++i)
@@ -503,28 +502,8 @@ struct NsStepEpi {
 #pragma unroll
                 for (int j = 0; j < Cfg::NTT; ++j) {
                     const uint32_t r = at.m0 + i * 16 + l % 16, c = at.n0 + j * 16 + l / 16 * 4;
-                    if (r < m && c < n) put_result(r, c, acc[i][j], at.batch);
+                    if (r < m && c < n) store_tail(static_cast<float*>(last) + at.batch * stride + r * ld + c, acc[i][j], n - c);
                 }
-        }
-    }
-    __device__ __forceinline__ void put_result(uint32_t r, uint32_t c, f32x4 v, uint32_t batch) const
-    {
-        const uint64_t o = batch * stride + r * ld + c;
-        if (bf16) {
-            uint16_t* q = static_cast<uint16_t*>(last) + o;
-            s16x4 w;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) w[i] = __builtin_bit_cast(short, (__bf16)v[i]);
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                if (c + i < n) q[i] = (uint16_t)w[i];
-        } else {
-            float* q = static_cast<float*>(last) + o;
-            if (wide && c + 4 <= n) *reinterpret_cast<f32x4*>(q) = v;
-            else
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    if (c + i < n) q[i] = v[i];
         }
     }
 };
@@ -712,8 +691,7 @@ extern "C" int sg_orthogonalize(const void* d_update, sg_dtype dt, uint32_t B, u
                 return rc;
             }
             const bool end = s + 1 == steps;
-            const bool owide = reinterpret_cast<uintptr_t>(d_out) % 16 == 0 && ld_out * es % 16 == 0 && (B == 1 || stride_out * es % 16 == 0);
-            const NsStepEpi<TWO> e = {px, py, w.dpoly, w.sp, tall, end ? d_out : nullptr, ld_out, stride_out, m, n, !TWO, owide, w.scale, s, coef};
+            const NsStepEpi<TWO> e = {px, py, w.dpoly, w.sp, tall, end ? d_out : nullptr, ld_out, stride_out, m, n, w.scale, s, coef};
             const Gemm gx = {tall ? mx : mb, tall ? mb : mx, w.mp, w.np, w.sp, nseg, 1, 0, nullptr, nullptr};
             rc = tall ? ns_product<KC, KC>(w.ps.tile, gx, B, e, st) : ns_product<KC, KS>(w.ps.tile, gx, B, e, st);
             if (rc) return rc;
