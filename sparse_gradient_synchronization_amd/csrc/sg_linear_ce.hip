@@ -149,20 +149,35 @@ struct CeItems {
     }
 };
 
-// the largest finite magnitude of the rows (of the live ones: row != NULL); one
-// row's infinity or NaN leaves the others their precision
-__global__ __launch_bounds__(256) void ce_max_kernel(CeSrc s, uint64_t rows, const uint32_t* row, const CeScal* scal,
-                                                     uint32_t* out)
+// One of the two matrices that a kernel takes in one launch, and its blocks
+struct CeSide {
+    CeSrc s;
+    uint64_t rows;
+    const uint32_t* row; // the live ones, NULL: all
+    uint32_t* max_bits;
+    uint16_t *hi, *lo;
+    uint32_t blocks;
+};
+
+// the largest finite magnitudes of the rows; one row's infinity or NaN leaves the
+// others their precision
+__global__ __launch_bounds__(256) void ce_max_kernel(CeSide x, CeSide w, const CeScal* scal)
 {
-    const uint64_t n = row ? scal->live : rows;
+    const bool first = blockIdx.x < x.blocks;
+    const CeSide& side = first ? x : w;
+    const CeSrc s = side.s;
+    const uint32_t* const row = side.row;
+    uint32_t* const out = side.max_bits;
+    const uint32_t block = first ? blockIdx.x : blockIdx.x - x.blocks, blocks = side.blocks;
+    const uint64_t n = row ? scal->live : side.rows;
     const uint32_t per = (s.n + 7) / 8;
     const CeItems items(n * per, per);
     uint32_t m = 0;
-    for (uint64_t i0 = blockIdx.x * 256ull + threadIdx.x; i0 < items.n; i0 += gridDim.x * 1024ull) {
+    for (uint64_t i0 = block * 256ull + threadIdx.x; i0 < items.n; i0 += blocks * 1024ull) {
         float v[4][8]; // four loads of 32 bytes under way
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
-            uint64_t i = i0 + u * gridDim.x * 256ull, r;
+            uint64_t i = i0 + u * blocks * 256ull, r;
             uint32_t c;
             items.split(i < items.n ? i : i0, &r, &c);
             ce_load8<float>(s, row ? row[r] : r, c * 8, v[u]);
@@ -187,15 +202,19 @@ __global__ __launch_bounds__(256) void ce_max_kernel(CeSrc s, uint64_t rows, con
 // Rows as planes: gathered (row != NULL; rows up to the next multiple of 64 are
 // zeros), columns padded with zeros to np.
 template <typename E>
-__global__ __launch_bounds__(256) void ce_pack_kernel(CeSrc s, uint64_t rows, const uint32_t* row, const CeScal* scal,
-                                                      const uint32_t* max_bits, uint16_t* hi, uint16_t* lo,
-                                                      uint32_t np)
+__global__ __launch_bounds__(256) void ce_pack_kernel(CeSide x, CeSide w, const CeScal* scal, uint32_t np)
 {
-    const uint64_t n = row ? scal->live : rows, padded = row ? (n + 63) / 64 * 64 : n;
+    const bool first = blockIdx.x < x.blocks;
+    const CeSide& side = first ? x : w;
+    const CeSrc s = side.s;
+    const uint32_t* const row = side.row;
+    uint16_t *const hi = side.hi, *const lo = side.lo;
+    const uint32_t block = first ? blockIdx.x : blockIdx.x - x.blocks, blocks = side.blocks;
+    const uint64_t n = row ? scal->live : side.rows, padded = row ? (n + 63) / 64 * 64 : n;
     const uint32_t per = np / 8;
-    const int e = lo ? ce_exponent(*max_bits) : 0;
+    const int e = lo ? ce_exponent(*side.max_bits) : 0;
     const CeItems items(padded * per, per);
-    for (uint64_t i = blockIdx.x * 256ull + threadIdx.x; i < items.n; i += gridDim.x * 256ull) {
+    for (uint64_t i = block * 256ull + threadIdx.x; i < items.n; i += blocks * 256ull) {
         uint64_t r;
         uint32_t c;
         items.split(i, &r, &c);
@@ -425,7 +444,20 @@ struct CePieceEpi {
     }
 };
 
-// A live row's statistics joined: loss, lse and what g needs.  A block a row.
+// loss, lse (write) and what g needs of live row t from its joined sums
+__device__ __forceinline__ CeRow ce_finish(const CeArgs& p, uint32_t t, float shift, double s, float zy, double top,
+                                           bool write)
+{
+    const double w = p.weight ? (double)p.weight[t] : 1.0, lse = p.it * (double)shift + log(s);
+    if (write) {
+        p.loss[t] = (float)(w * (lse - p.it * (double)zy + p.zc * lse * lse));
+        if (p.lse) p.lse[t] = (float)lse;
+    }
+    const double b = w * p.it / top;
+    return {shift, (float)log2(s), (float)(b * (1.0 + 2.0 * p.zc * lse)), (float)b};
+}
+
+// A live row's statistics joined.  A block a row.
 __global__ __launch_bounds__(256) void ce_join_kernel(CeArgs p, const uint32_t* row, const float2* stat,
                                                       uint32_t groups, const float* zy, CeRow* info, CeScal* scal,
                                                       bool planes)
@@ -453,13 +485,8 @@ __global__ __launch_bounds__(256) void ce_join_kernel(CeArgs p, const uint32_t* 
     __syncthreads();
     if (threadIdx.x) return;
     s = ss[0] + ss[1] + ss[2] + ss[3];
-    const uint32_t t = row[j];
-    const double w = p.weight ? (double)p.weight[t] : 1.0, lse = p.it * (double)shift + log(s);
-    p.loss[t] = (float)(w * (lse - p.it * (double)zy[j] + p.zc * lse * lse));
-    if (p.lse) p.lse[t] = (float)lse;
+    const CeRow r = ce_finish(p, row[j], shift, s, zy[j], scal->top, true);
     if (!info) return;
-    const double b = w * p.it / scal->top;
-    const CeRow r = {shift, (float)log2(s), (float)(b * (1.0 + 2.0 * p.zc * lse)), (float)b};
     info[j] = r;
     // A maximum of whole numbers: the order of the rows does not matter.  Looked at first: with equal weights
     // most rows have nothing to add, and as many atomics on one word took 12 ns each (4088 rows: 50 us).
@@ -468,10 +495,12 @@ __global__ __launch_bounds__(256) void ce_join_kernel(CeArgs p, const uint32_t* 
 }
 
 // kept exponentials -> g, in place; rows up to the next multiple of 64 are
-// zeros.  A block takes 8 rows of a panel.
-__global__ __launch_bounds__(256) void ce_grad_kernel(const uint32_t* row, const int32_t* label, const float2* stat,
-                                                      uint32_t groups, uint32_t group_cols, const CeRow* info,
-                                                      const CeScal* scal, CeG g, float c)
+// zeros.  A block takes 8 rows of a panel.  JOIN: it joins its rows' statistics
+// itself, the first panel's blocks write loss and lse.
+template <bool JOIN>
+__global__ __launch_bounds__(256) void ce_grad_kernel(CeArgs p, const uint32_t* row, const float2* stat,
+                                                      uint32_t groups, uint32_t group_cols, const float* zy,
+                                                      const CeRow* info, const CeScal* scal, CeG g)
 {
     const uint32_t per = (uint32_t)(g.rows / 8), v0 = blockIdx.x / per * 256 + threadIdx.x % 32 * 8;
     const uint32_t j = blockIdx.x % per * 8 + threadIdx.x / 32, live = scal->live;
@@ -483,11 +512,27 @@ __global__ __launch_bounds__(256) void ce_grad_kernel(const uint32_t* row, const
         if (lo) *lo = u32x4{0, 0, 0, 0};
         return;
     }
-    const CeRow r = info[j];
-    const uint32_t y = (uint32_t)label[row[j]];
+    const uint32_t t = row[j], y = (uint32_t)p.label[t];
+    CeRow r;
+    if constexpr (JOIN) { // 32 lanes have the row
+        const float2* const q = stat + (uint64_t)j * groups;
+        const float z = zy[j];
+        float m = -INFINITY;
+        for (uint32_t i = threadIdx.x % 32; i < groups; i += 32) m = fmaxf(m, q[i].x);
+#pragma unroll
+        for (int d = 1; d < 32; d *= 2) m = fmaxf(m, __shfl_xor(m, d));
+        const float shift = shift_of(m);
+        double s = 0.0;
+        for (uint32_t i = threadIdx.x % 32; i < groups; i += 32) s += (double)q[i].y * exp2_fast(p.c * (q[i].x - shift));
+#pragma unroll
+        for (int d = 1; d < 32; d *= 2) s += __shfl_xor(s, d);
+        r = ce_finish(p, t, shift, s, z, scal->top, blockIdx.x < per && threadIdx.x % 32 == 0);
+    } else {
+        r = info[j];
+    }
     // a group past the vocabulary's end (padding columns): its exponentials are 0
     const uint32_t grp = v0 / group_cols;
-    const float scale = grp < groups ? r.a * exp2_fast(c * (stat[(uint64_t)j * groups + grp].x - r.m) - r.ls) : 0.f;
+    const float scale = grp < groups ? r.a * exp2_fast(p.c * (stat[(uint64_t)j * groups + grp].x - r.m) - r.ls) : 0.f;
     const u32x4 h = grp < groups ? *hi : u32x4{0, 0, 0, 0};
     float v[8];
     if (lo) {
@@ -901,26 +946,19 @@ extern "C" int sg_linear_ce_loss(const void* d_hidden, uint64_t ld_hidden, const
     const CeArgs a = {d_label, d_weight, d_loss, d_lse, T, (uint32_t)V, inv_temp, z_coef, c};
     ce_rows_kernel<<<1, 1024, 0, st>>>(a, p.row, p.pos, p.scal);
     SG_TRY_LAUNCH();
-    const CeSrc sx = {d_hidden, ld_hidden, p.H}, sw = {d_head, ld_head, p.H};
-    const auto blocks = [](uint64_t items) { const uint64_t b = ceil_div(items, 256); return (unsigned)(b < 8192 ? b : 8192); };
-    const unsigned bx = blocks((uint64_t)p.Tp * p.Hp / 8), bw = blocks(V * p.Hp / 8);
+    // the hidden states' and (head copied) the head's blocks
+    const auto blocks = [](uint64_t items, unsigned most) { const uint64_t b = ceil_div(items, 256); return (unsigned)(b < most ? b : most); };
+    CeSide sx = {{d_hidden, ld_hidden, p.H}, T, p.row, &p.scal->max_x, p.x[0], p.x[1], blocks((uint64_t)p.Tp * p.Hp / 8, 1024)};
+    CeSide sw = {{d_head, ld_head, p.H}, V, nullptr, &p.scal->max_w, p.w[0], p.w[1], blocks(V * p.Hp / 8, 2048)};
     if (p.two) {
-        ce_max_kernel<<<bx < 1024 ? bx : 1024, 256, 0, st>>>(sx, T, p.row, p.scal, &p.scal->max_x);
+        ce_max_kernel<<<sx.blocks + sw.blocks, 256, 0, st>>>(sx, sw, p.scal);
         SG_TRY_LAUNCH();
-        ce_max_kernel<<<bw < 2048 ? bw : 2048, 256, 0, st>>>(sw, V, nullptr, p.scal, &p.scal->max_w);
-        SG_TRY_LAUNCH();
-        ce_pack_kernel<float><<<bx, 256, 0, st>>>(sx, T, p.row, p.scal, &p.scal->max_x, p.x[0], p.x[1], p.Hp);
-        SG_TRY_LAUNCH();
-        ce_pack_kernel<float><<<bw, 256, 0, st>>>(sw, V, nullptr, p.scal, &p.scal->max_w, p.w[0], p.w[1], p.Hp);
-        SG_TRY_LAUNCH();
-    } else {
-        ce_pack_kernel<bf16_bits><<<bx, 256, 0, st>>>(sx, T, p.row, p.scal, nullptr, p.x[0], nullptr, p.Hp);
-        SG_TRY_LAUNCH();
-        if (p.pack) {
-            ce_pack_kernel<bf16_bits><<<bw, 256, 0, st>>>(sw, V, nullptr, p.scal, nullptr, p.w[0], nullptr, p.Hp);
-            SG_TRY_LAUNCH();
-        }
     }
+    sx.blocks = blocks((uint64_t)p.Tp * p.Hp / 8, 8192);
+    sw.blocks = p.pack ? blocks(V * p.Hp / 8, 8192) : 0;
+    if (p.two) ce_pack_kernel<float><<<sx.blocks + sw.blocks, 256, 0, st>>>(sx, sw, p.scal, p.Hp);
+    else ce_pack_kernel<bf16_bits><<<sx.blocks + sw.blocks, 256, 0, st>>>(sx, sw, p.scal, p.Hp);
+    SG_TRY_LAUNCH();
     const uint32_t nseg = p.two ? 3 : 1;
     const uint64_t ldw = p.pack ? p.Hp : ld_head;
     const uint16_t* const w0 = p.pack ? p.w[0] : static_cast<const uint16_t*>(d_head);
@@ -941,15 +979,22 @@ extern "C" int sg_linear_ce_loss(const void* d_hidden, uint64_t ld_hidden, const
         return ce_product<KC, KC, decltype(planes)::value>(p.tile, g1, e, st);
     };
     if ((rc = p.two ? first(std::true_type()) : first(std::false_type()))) return rc;
-    ce_join_kernel<<<(unsigned)T, 256, 0, st>>>(a, p.row, p.stat, p.groups, p.zy, p.info, p.scal, p.two);
-    SG_TRY_LAUNCH();
+    // One launch less where a row's statistics are one load a lane (and g needs no scale of its largest element, as fp32
+    // does).  us a call, two launches and one, bf16: 56 x 1856 x 79 44, 40, 8192 x 512 x 512 81, 73; 24 x 32000 x 2048 97,
+    // 98, 2048 x 8000 x 256 96, 100
+    const bool join = !p.two && keep && p.groups <= 32;
+    if (!join) {
+        ce_join_kernel<<<(unsigned)T, 256, 0, st>>>(a, p.row, p.stat, p.groups, p.zy, p.info, p.scal, p.two);
+        SG_TRY_LAUNCH();
+    }
     if (!p.grads) return SG_OK;
 
     for (uint64_t v0 = 0; v0 < V; v0 += p.piece) {
         const uint64_t n = V - v0 < p.piece ? V - v0 : p.piece, np = align_up(n, 64);
         if (p.kept) {
-            ce_grad_kernel<<<(unsigned)(p.Tp / 8 * (p.piece / 256)), 256, 0, st>>>(
-                p.row, d_label, p.stat, p.groups, ce_tile_cols(p.tile), p.info, p.scal, g, c);
+            const unsigned blocks = (unsigned)(p.Tp / 8 * (p.piece / 256));
+            if (join) ce_grad_kernel<true><<<blocks, 256, 0, st>>>(a, p.row, p.stat, p.groups, ce_tile_cols(p.tile), p.zy, p.info, p.scal, g);
+            else ce_grad_kernel<false><<<blocks, 256, 0, st>>>(a, p.row, p.stat, p.groups, ce_tile_cols(p.tile), p.zy, p.info, p.scal, g);
             SG_TRY_LAUNCH();
         } else {
             const Gemm g2 = {mx, head(v0, n), (uint32_t)T, (uint32_t)n, k1, nseg, 1, 0, live, nullptr};
