@@ -60,8 +60,10 @@ def test_large_tiles(dtype):
 
 
 # The variants that a rule on sizes chooses, at both sides of each rule's edge: dw as a stream of rows (64 rows)
-# with the hidden dimension in parts or whole, dw in parts of the rows, dx in many parts of the vocabulary
-VARIANTS = [(63, 700, 700), (64, 700, 257), (65, 700, 257), (3, 130, 2056), (40, 70000, 65), (4088, 3264, 64),
+# with the hidden dimension in parts or whole, dw in parts of the rows, dx in many parts of the vocabulary, rows found
+# by the blocks that pack them (1024), statistics joined in the pass to g (32 tiles of columns)
+VARIANTS = [(1023, 4096, 40), (1024, 4097, 40), (1025, 4096, 40), (50, 8192, 72), (50, 8193, 72),
+            (63, 700, 700), (64, 700, 257), (65, 700, 257), (3, 130, 2056), (40, 70000, 65), (4088, 3264, 64),
             (6000, 150, 96), (200, 40000, 60), (1100, 300, 1030)]
 
 
